@@ -1,0 +1,339 @@
+"""Binding of libipttt.so's operators around the TTT MLP layer: norms of queries and keys
+with the position rotation, linear attention with a decay for each head (prompts, single
+tokens, gradients), and the softmax cross entropy of a linear head with its gradients.
+
+As in ipttt.py: argument marshalling only, no fallback.  Every function checks its tensors
+(device, type, shape, strides), runs on the tensors' device and on `stream` (default: that
+device's current stream), and takes what it allocates from that stream.  Token tensors
+[B, T, heads, width] may be views whose tokens lie apart (q, k and v of one fused
+projection): heads and width packed, any token stride that is a multiple of 8 elements.
+"""
+from __future__ import annotations
+
+import contextlib
+import ctypes
+from dataclasses import dataclass
+
+import torch
+
+from .ipttt import BF16, F32, LinattnParams, QKParams, XentParams, _check, lib
+
+_DTYPES = {"bf16": (BF16, torch.bfloat16), "f32": (F32, torch.float32)}
+
+
+def _dtype(name: str):
+    if name not in _DTYPES:
+        raise ValueError(f"dtype {name!r}, expected 'bf16' or 'f32'")
+    return _DTYPES[name]
+
+
+@contextlib.contextmanager
+def _on(t: torch.Tensor, stream):
+    """Runs the block on t's device and on `stream`; yields the stream's handle."""
+    if not t.is_cuda:
+        raise ValueError("the tensors must be CUDA tensors")
+    if stream is None:
+        if t.device.index == torch.cuda.current_device():
+            yield torch.cuda.current_stream().cuda_stream
+        else:
+            with torch.cuda.device(t.device):
+                yield torch.cuda.current_stream().cuda_stream
+        return
+    if stream.device != t.device:
+        raise ValueError(f"stream of {stream.device}, tensors on {t.device}")
+    with torch.cuda.device(t.device), torch.cuda.stream(stream):  # what is allocated inside belongs to `stream`
+        yield stream.cuda_stream
+
+
+def _flat(t, name, shape, dtype, device):
+    """Pointer of a packed tensor (None: None)."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.device != device or tuple(t.shape) != shape:
+        raise ValueError(f"{name}: {tuple(t.shape)} {t.dtype} on {t.device}, expected {shape} {dtype} on {device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _tokens(t, name, shape, dtype, device):
+    """(pointer, token stride) of a token tensor [B, T, heads, width]."""
+    if t.dtype != dtype or t.device != device or tuple(t.shape) != shape:
+        raise ValueError(f"{name}: {tuple(t.shape)} {t.dtype} on {t.device}, expected {shape} {dtype} on {device}")
+    B, T, H, D = shape
+    if t.is_contiguous():
+        return t.data_ptr(), H * D
+    sb, st, sh, sd = t.stride()
+    ld = st if T > 1 else sb if B > 1 else H * D
+    if (sd != 1 and D > 1) or (sh != D and H > 1) or (B > 1 and sb != T * ld) or ld < H * D or ld % 8:
+        raise ValueError(f"{name}: strides {t.stride()}; heads and width must be packed, tokens a constant multiple of "
+                         "8 elements apart")
+    return t.data_ptr(), ld
+
+
+def _starts(doc_starts, device):
+    """(pointer, count, tensor to keep) of document starts b*T + t on `device`."""
+    if doc_starts is None:
+        return None, 0, None
+    ds = doc_starts if isinstance(doc_starts, torch.Tensor) else torch.as_tensor(doc_starts, dtype=torch.int32)
+    ds = ds.to(device=device, dtype=torch.int32).contiguous()
+    return (ds.data_ptr() if ds.numel() else None), ds.numel(), ds
+
+
+def _workspace(workspace, need, device):
+    if workspace is None:
+        return torch.empty(need, dtype=torch.uint8, device=device)
+    if workspace.dtype != torch.uint8 or workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous uint8 tensor on {device}")
+    return workspace
+
+
+def _size(fn, params, what):
+    n = int(fn(ctypes.byref(params)))
+    if n == 0:
+        raise ValueError(f"invalid configuration {what}")
+    return n
+
+
+# ---------------------------------------------------------------- norms and rotation
+
+@dataclass
+class QKNormRopeConfig:
+    """B sequences of T tokens; Hq query and Hk key heads of width D, of which the first R
+    elements are rotated (pairs (i, i + R/2), or (2i, 2i+1) when interleaved)."""
+    B: int
+    T: int
+    Hq: int
+    Hk: int
+    D: int
+    R: int
+    eps: float = 1e-6
+    interleaved: bool = False
+    dtype: str = "bf16"
+
+    def params(self, **ld) -> QKParams:
+        return QKParams(self.B, self.T, self.Hq, self.Hk, self.D, self.R, _dtype(self.dtype)[0], int(self.interleaved),
+                        float(self.eps), *(int(ld.get(n, 0)) for n in ("ldq", "ldk", "ldqo", "ldko", "ldgq", "ldgk")))
+
+
+def _qk_inputs(cfg, q, k, wq, wk, inv_freq, positions):
+    dt, dev = _dtype(cfg.dtype)[1], q.device
+    pq, ldq = _tokens(q, "q", (cfg.B, cfg.T, cfg.Hq, cfg.D), dt, dev)
+    pk, ldk = _tokens(k, "k", (cfg.B, cfg.T, cfg.Hk, cfg.D), dt, dev)
+    ptrs = [pq, pk, _flat(wq, "wq", (cfg.D,), dt, dev), _flat(wk, "wk", (cfg.D,), dt, dev)]
+    if cfg.R:
+        ptrs += [_flat(inv_freq, "inv_freq", (cfg.R // 2,), torch.float64, dev),
+                 _flat(positions, "positions", (cfg.B, cfg.T), torch.int64, dev)]
+    else:
+        ptrs += [None, None]
+    return ptrs, ldq, ldk, dt, dev
+
+
+def qk_norm_rope(cfg: QKNormRopeConfig, q, k, wq, wk, inv_freq, positions, *, q_out=None, k_out=None, stream=None):
+    """RMS norm of every head of q [B,T,Hq,D] and k [B,T,Hk,D] with weights wq, wk [D], then
+    the rotation by positions [B,T] (int64) * inv_freq [R/2] (float64, radians a
+    position).  Returns (q_out, k_out), packed unless given; q_out may be q, k_out k."""
+    (*ptrs,), ldq, ldk, dt, dev = _qk_inputs(cfg, q, k, wq, wk, inv_freq, positions)
+    with _on(q, stream) as st:
+        if q_out is None:
+            q_out = torch.empty(cfg.B, cfg.T, cfg.Hq, cfg.D, dtype=dt, device=dev)
+        if k_out is None:
+            k_out = torch.empty(cfg.B, cfg.T, cfg.Hk, cfg.D, dtype=dt, device=dev)
+        po, ldqo = _tokens(q_out, "q_out", (cfg.B, cfg.T, cfg.Hq, cfg.D), dt, dev)
+        pk, ldko = _tokens(k_out, "k_out", (cfg.B, cfg.T, cfg.Hk, cfg.D), dt, dev)
+        p = cfg.params(ldq=ldq, ldk=ldk, ldqo=ldqo, ldko=ldko)
+        _check(lib().ipttt_qk_norm_rope(ctypes.byref(p), *ptrs, po, pk, st), "ipttt_qk_norm_rope")
+    return q_out, k_out
+
+
+def qk_norm_rope_backward(cfg: QKNormRopeConfig, q, k, wq, wk, inv_freq, positions, gq_out, gk_out, *, gq=None,
+                          gk=None, workspace=None, stream=None):
+    """Gradients of <gq_out, q_out> + <gk_out, k_out>: a dict with q and k (the call's dtype,
+    packed unless gq, gk are given; they may be gq_out, gk_out) and wq, wk (fp32)."""
+    (*ptrs,), ldq, ldk, dt, dev = _qk_inputs(cfg, q, k, wq, wk, inv_freq, positions)
+    sq, sk = (cfg.B, cfg.T, cfg.Hq, cfg.D), (cfg.B, cfg.T, cfg.Hk, cfg.D)
+    pgq, ldqo = _tokens(gq_out, "gq_out", sq, dt, dev)
+    pgk, ldko = _tokens(gk_out, "gk_out", sk, dt, dev)
+    with _on(q, stream) as st:
+        gq = torch.empty(*sq, dtype=dt, device=dev) if gq is None else gq
+        gk = torch.empty(*sk, dtype=dt, device=dev) if gk is None else gk
+        po, ldgq = _tokens(gq, "gq", sq, dt, dev)
+        pk, ldgk = _tokens(gk, "gk", sk, dt, dev)
+        gw = torch.empty(2, cfg.D, dtype=torch.float32, device=dev)
+        p = cfg.params(ldq=ldq, ldk=ldk, ldqo=ldqo, ldko=ldko, ldgq=ldgq, ldgk=ldgk)
+        ws = _workspace(workspace, _size(lib().ipttt_qk_norm_rope_backward_workspace_size, p, cfg), dev)
+        _check(lib().ipttt_qk_norm_rope_backward(ctypes.byref(p), *ptrs, pgq, pgk, po, pk, gw.data_ptr(),
+                                                 gw.data_ptr() + 4 * cfg.D, ws.data_ptr(), ws.numel(), st),
+               "ipttt_qk_norm_rope_backward")
+    return {"q": gq, "k": gk, "wq": gw[0], "wk": gw[1]}
+
+
+# ---------------------------------------------------------------- linear attention
+
+@dataclass
+class LinearAttentionConfig:
+    """B sequences of T tokens; H query heads over Hkv key/value heads, widths Dk and Dv."""
+    B: int
+    T: int
+    H: int
+    Hkv: int
+    Dk: int
+    Dv: int
+    scale: float
+    dtype: str = "bf16"
+
+    def params(self, **ld) -> LinattnParams:
+        return LinattnParams(self.B, self.T, self.H, self.Hkv, self.Dk, self.Dv, _dtype(self.dtype)[0],
+                             float(self.scale),
+                             *(int(ld.get(n, 0)) for n in ("ldq", "ldk", "ldv", "ldo", "ldgq", "ldgk", "ldgv")))
+
+    def shapes(self):
+        B, T = self.B, self.T
+        return {"q": (B, T, self.H, self.Dk), "k": (B, T, self.Hkv, self.Dk), "v": (B, T, self.Hkv, self.Dv),
+                "O": (B, T, self.H, self.Dv), "S": (B, self.H, self.Dk, self.Dv)}
+
+
+def linear_attention_workspace_size(cfg: LinearAttentionConfig, backward: bool = False) -> int:
+    L = lib()
+    return _size(L.ipttt_linattn_backward_workspace_size if backward else L.ipttt_linattn_workspace_size, cfg.params(),
+                 cfg)
+
+
+def linear_attention(cfg: LinearAttentionConfig, q, k, v, log_decay, doc_starts=None, *, S0=None, O=None,
+                     S_final=False, workspace=None, stream=None):
+    """o_t = scale q_t S_t with S_t = exp(log_decay) S_{t-1} + k_t v_t^T, S reset at document
+    starts (offsets b*T + t).  S0: the state before the first token, fp32 [B,H,Dk,Dv]
+    (None: zero).  Returns O [B,T,H,Dv], or (O, S_T) with S_final=True or with S_final an
+    fp32 [B,H,Dk,Dv] tensor to write (S0 itself may be it)."""
+    dt, dev, sh = _dtype(cfg.dtype)[1], q.device, cfg.shapes()
+    f32 = torch.float32
+    pq, ldq = _tokens(q, "q", sh["q"], dt, dev)
+    pk, ldk = _tokens(k, "k", sh["k"], dt, dev)
+    pv, ldv = _tokens(v, "v", sh["v"], dt, dev)
+    pd = _flat(log_decay, "log_decay", (cfg.H,), f32, dev)
+    p0 = _flat(S0, "S0", sh["S"], f32, dev)
+    with _on(q, stream) as st:
+        if O is None:
+            O = torch.empty(*sh["O"], dtype=dt, device=dev)
+        Sf = torch.empty(*sh["S"], dtype=f32, device=dev) if S_final is True else S_final if S_final is not False else None
+        po, ldo = _tokens(O, "O", sh["O"], dt, dev)
+        p = cfg.params(ldq=ldq, ldk=ldk, ldv=ldv, ldo=ldo)
+        ws = _workspace(workspace, _size(lib().ipttt_linattn_workspace_size, p, cfg), dev)
+        dp, nd, keep = _starts(doc_starts, dev)
+        _check(lib().ipttt_linattn_forward(ctypes.byref(p), pq, pk, pv, pd, dp, nd, p0, po,
+                                           _flat(Sf, "S_final", sh["S"], f32, dev), ws.data_ptr(), ws.numel(), st),
+               "ipttt_linattn_forward")
+    return O if Sf is None else (O, Sf)
+
+
+def linear_attention_backward(cfg: LinearAttentionConfig, q, k, v, log_decay, doc_starts, gO, *, S0=None,
+                              gS_final=None, workspace=None, stream=None):
+    """Gradients of <gO, O> + <gS_final, S_T>: a dict with q, k and v (the call's dtype) and,
+    when S0 is given, S0 (fp32)."""
+    dt, dev, sh = _dtype(cfg.dtype)[1], q.device, cfg.shapes()
+    f32 = torch.float32
+    pq, ldq = _tokens(q, "q", sh["q"], dt, dev)
+    pk, ldk = _tokens(k, "k", sh["k"], dt, dev)
+    pv, ldv = _tokens(v, "v", sh["v"], dt, dev)
+    pg, ldo = _tokens(gO, "gO", sh["O"], dt, dev)
+    pd = _flat(log_decay, "log_decay", (cfg.H,), f32, dev)
+    p0 = _flat(S0, "S0", sh["S"], f32, dev)
+    ps = _flat(gS_final, "gS_final", sh["S"], f32, dev)
+    with _on(q, stream) as st:
+        out = {n: torch.empty(*sh[n], dtype=dt, device=dev) for n in ("q", "k", "v")}
+        if S0 is not None:
+            out["S0"] = torch.empty(*sh["S"], dtype=f32, device=dev)
+        p = cfg.params(ldq=ldq, ldk=ldk, ldv=ldv, ldo=ldo)
+        ws = _workspace(workspace, _size(lib().ipttt_linattn_backward_workspace_size, p, cfg), dev)
+        dp, nd, keep = _starts(doc_starts, dev)
+        _check(lib().ipttt_linattn_backward(ctypes.byref(p), pq, pk, pv, pd, dp, nd, p0, pg, ps, out["q"].data_ptr(),
+                                            out["k"].data_ptr(), out["v"].data_ptr(),
+                                            out["S0"].data_ptr() if S0 is not None else None, ws.data_ptr(),
+                                            ws.numel(), st), "ipttt_linattn_backward")
+    return out
+
+
+def linear_attention_step(cfg: LinearAttentionConfig, S, q, k, v, log_decay, starts=None, *, o=None, stream=None):
+    """One token of every row on the state S (fp32 [B,H,Dk,Dv], updated in place): q [B,H,Dk],
+    k [B,Hkv,Dk], v [B,Hkv,Dv]; starts: int32 [B] on the device, nonzero where the row's token
+    starts a document.  Returns o [B,H,Dv].  cfg.T is ignored."""
+    dt, dev = _dtype(cfg.dtype)[1], q.device
+    B, H, Hkv, Dk, Dv = cfg.B, cfg.H, cfg.Hkv, cfg.Dk, cfg.Dv
+
+    def rows(t, name, heads, width):
+        if t.dim() != 3:
+            raise ValueError(f"{name}: {tuple(t.shape)}, expected {(B, heads, width)}")
+        return _tokens(t.unsqueeze(1), name, (B, 1, heads, width), dt, dev)
+
+    pq, ldq = rows(q, "q", H, Dk)
+    pk, ldk = rows(k, "k", Hkv, Dk)
+    pv, ldv = rows(v, "v", Hkv, Dv)
+    ps = _flat(S, "S", (B, H, Dk, Dv), torch.float32, dev)
+    pd = _flat(log_decay, "log_decay", (H,), torch.float32, dev)
+    pn = _flat(starts, "starts", (B,), torch.int32, dev)
+    if ps is None:
+        raise ValueError("S is missing")
+    with _on(q, stream) as st:
+        if o is None:
+            o = torch.empty(B, H, Dv, dtype=dt, device=dev)
+        po, ldo = rows(o, "o", H, Dv)
+        p = cfg.params(ldq=ldq, ldk=ldk, ldv=ldv, ldo=ldo)
+        p.T = 1
+        _check(lib().ipttt_linattn_step(ctypes.byref(p), ps, pq, pk, pv, pd, pn, po, st), "ipttt_linattn_step")
+    return o
+
+
+# ---------------------------------------------------------------- softmax cross entropy
+
+@dataclass
+class CrossEntropyConfig:
+    """N tokens, a vocabulary of V, width d; targets equal to ignore_index take no part.
+    piece: vocabulary rows the backward handles at a time (0: chosen by the library)."""
+    N: int
+    V: int
+    d: int
+    ignore_index: int = -100
+    dtype: str = "bf16"
+    piece: int = 0
+
+    def params(self) -> XentParams:
+        return XentParams(self.N, self.V, self.d, _dtype(self.dtype)[0], self.piece, self.ignore_index)
+
+
+def cross_entropy_workspace_size(cfg: CrossEntropyConfig, backward: bool = False) -> int:
+    L = lib()
+    return _size(L.ipttt_xent_backward_workspace_size if backward else L.ipttt_xent_workspace_size, cfg.params(), cfg)
+
+
+def cross_entropy(cfg: CrossEntropyConfig, H, W, targets, *, workspace=None, stream=None):
+    """Per-token loss of the head W [V,d] on H [N,d] for targets [N] (int64): returns (loss,
+    lse), fp32 [N]; lse goes to cross_entropy_backward.  The logits are never kept."""
+    dt, dev, f32 = _dtype(cfg.dtype)[1], H.device, torch.float32
+    ptrs = [_flat(H, "H", (cfg.N, cfg.d), dt, dev), _flat(W, "W", (cfg.V, cfg.d), dt, dev),
+            _flat(targets, "targets", (cfg.N,), torch.int64, dev)]
+    with _on(H, stream) as st:
+        loss, lse = torch.empty(cfg.N, dtype=f32, device=dev), torch.empty(cfg.N, dtype=f32, device=dev)
+        ws = _workspace(workspace, cross_entropy_workspace_size(cfg), dev)
+        p = cfg.params()
+        _check(lib().ipttt_xent_forward(ctypes.byref(p), *ptrs, loss.data_ptr(), lse.data_ptr(), ws.data_ptr(),
+                                        ws.numel(), st), "ipttt_xent_forward")
+    return loss, lse
+
+
+def cross_entropy_backward(cfg: CrossEntropyConfig, H, W, targets, lse, gloss, *, gH=None, gW=None, workspace=None,
+                           stream=None):
+    """Gradients of <gloss, loss> (gloss fp32 [N]; 1/count everywhere for a mean): a dict
+    with H and W in the call's dtype, from the lse that cross_entropy returned."""
+    dt, dev, f32 = _dtype(cfg.dtype)[1], H.device, torch.float32
+    ptrs = [_flat(H, "H", (cfg.N, cfg.d), dt, dev), _flat(W, "W", (cfg.V, cfg.d), dt, dev),
+            _flat(targets, "targets", (cfg.N,), torch.int64, dev), _flat(lse, "lse", (cfg.N,), f32, dev),
+            _flat(gloss, "gloss", (cfg.N,), f32, dev)]
+    with _on(H, stream) as st:
+        gH = torch.empty(cfg.N, cfg.d, dtype=dt, device=dev) if gH is None else gH
+        gW = torch.empty(cfg.V, cfg.d, dtype=dt, device=dev) if gW is None else gW
+        ws = _workspace(workspace, cross_entropy_workspace_size(cfg, backward=True), dev)
+        p = cfg.params()
+        _check(lib().ipttt_xent_backward(ctypes.byref(p), *ptrs, _flat(gH, "gH", (cfg.N, cfg.d), dt, dev),
+                                         _flat(gW, "gW", (cfg.V, cfg.d), dt, dev), ws.data_ptr(), ws.numel(), st),
+               "ipttt_xent_backward")
+    return {"H": gH, "W": gW}

@@ -67,6 +67,12 @@ enum Phase { PH_PREP = 0, PH_GATEUP = 1, PH_TARGET = 2, PH_GRAM = 3, PH_APPLY = 
 std::atomic<uint64_t> g_launches{0};
 std::atomic<int> g_profile_on{0};
 
+}  // namespace
+
+void count_launches(long long n) { g_launches.fetch_add((uint64_t)n); }
+
+namespace {
+
 struct Profiler {
   std::mutex mu;
   std::vector<cudaEvent_t> pool;
@@ -115,7 +121,7 @@ struct PhaseScope {
   }
 };
 
-inline void counted(long long n) { g_launches.fetch_add((uint64_t)n); }
+inline void counted(long long n) { count_launches(n); }
 
 inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -356,10 +362,14 @@ StreamState state_of(const ipttt_params& p, void* state) {
 // The detail behind the last IPTTT_ERR_CUDA of this thread (ipttt_last_error_detail).
 thread_local char g_err_detail[320];
 
+}  // namespace
+
 ipttt_status cuda_fail(const char* step, cudaError_t e) {
   snprintf(g_err_detail, sizeof(g_err_detail), "%s: %s (%s)", step, cudaGetErrorName(e), cudaGetErrorString(e));
   return IPTTT_ERR_CUDA;
 }
+
+namespace {
 
 #define IP_CHECK(expr)                                  \
   do {                                                  \

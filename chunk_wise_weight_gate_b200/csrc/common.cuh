@@ -53,6 +53,10 @@ __device__ __forceinline__ float silu_precise(float x) { return x / (1.0f + expf
 
 // Host helpers (implemented in api.cu).
 ipttt_status cuda_status(cudaError_t e);
+// Records the CUDA error behind an IPTTT_ERR_CUDA of this thread and returns that code.
+ipttt_status cuda_fail(const char* step, cudaError_t e);
+// Adds to the kernels counted by ipttt_kernel_launches.
+void count_launches(long long n);
 // Tokens per step of the chunk scan: 512 when the bf16 path scans chunks of 64,
 // 128 or 256 tokens in groups, else C.  Streaming pieces that are multiples of it give
 // one call's result bit for bit.

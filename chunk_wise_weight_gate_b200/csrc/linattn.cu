@@ -1,0 +1,652 @@
+// Linear attention with a decay for each head: entry points, the pass on the CUDA
+// cores (fp32, and widths that the tensor-core pass does not take), the single-token
+// step, and the sum of a shared head's gradients.  linattn.h has the mathematics.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+
+#include <algorithm>
+
+#include "linattn.h"
+
+namespace ipttt {
+namespace la {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxWidth = 256;
+constexpr int L = kSimtChunk;
+constexpr int kSlice = 64;  // columns of the state a block holds
+
+__device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
+  const uint2 v = *reinterpret_cast<const uint2*>(p);
+  const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&v.x));
+  const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&v.y));
+  return make_float4(a.x, a.y, b.x, b.y);
+}
+__device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
+__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
+  const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
+  uint2 u;
+  u.x = *reinterpret_cast<const uint32_t*>(&a);
+  u.y = *reinterpret_cast<const uint32_t*>(&b);
+  *reinterpret_cast<uint2*>(p) = u;
+}
+__device__ __forceinline__ void fma4(float4& acc, float s, float4 v) {
+  acc.x = fmaf(s, v.x, acc.x);
+  acc.y = fmaf(s, v.y, acc.y);
+  acc.z = fmaf(s, v.z, acc.z);
+  acc.w = fmaf(s, v.w, acc.w);
+}
+__device__ __forceinline__ float4 scale4(float4 a, float s) { return make_float4(a.x * s, a.y * s, a.z * s, a.w * s); }
+
+// ------------------------------------------------------------------ document starts
+
+// Bit t of a row's words for every listed start (strictly increasing offsets b*T + t).
+__global__ void k_mark(uint32_t* words, long long wpr, int B, int T, const int32_t* ds, int n, int* status) {
+  const int i = blockIdx.x * blockDim.x + threadIdx.x;
+  if (i >= n) return;
+  const long long g = ds[i];
+  if (g < 0 || g >= (long long)B * T || (i > 0 && (long long)ds[i - 1] >= g)) {
+    set_status(status, IPTTT_ERR_ARG);
+    return;
+  }
+  atomicOr(words + (g / T) * wpr + (g % T) / 32, 1u << ((g % T) % 32));
+}
+
+// ------------------------------------------------------------------ the pass on the CUDA cores
+
+size_t simt_smem(int Da) {
+  return sizeof(float) * ((size_t)Da * kSlice + 2 * (size_t)L * (Da + 4) + (size_t)L * kSlice + L * (L + 1) + 3 * L + 4);
+}
+
+// One block walks a segment's chunks of 32 tokens for one (row, head) and 64 columns
+// of c, with its columns of the state in shared memory: the chunk's a, b and c are
+// staged as fp32, the 32 x 32 products a . b under the decay formed, the chunk's
+// output written and the state advanced.  Bound by the fp32 pipe and shared memory;
+// a 2 x 4 tile of outputs a thread halves the shared-memory reads a product takes.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) k_pass(const Pass p) {
+  extern __shared__ __align__(16) float smem[];
+  const int Da = p.Da, lda = Da + 4;
+  float* F = smem;                      // [Da][kSlice]
+  float* sa = F + (size_t)Da * kSlice;  // [L][lda]
+  float* sb = sa + (size_t)L * lda;     // [L][lda]
+  float* sc = sb + (size_t)L * lda;     // [L][kSlice]
+  float* sp = sc + L * kSlice;          // [L][L + 1]
+  float* pw = sp + L * (L + 1);         // [L + 1] powers of gamma
+  float* win = pw + L + 1;              // [L] the state's weight in each row
+  float* wout = win + L;                // [L] each row's weight in the new state
+  int* sh = reinterpret_cast<int*>(wout + L);
+
+  const int b = blockIdx.y / p.H, h = blockIdx.y % p.H;
+  const int seg = blockIdx.z;
+  const int c0 = blockIdx.x * kSlice;
+  const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
+  const float g = p.log_decay[h];
+  if (threadIdx.x == 0 && !(g <= 0.0f)) set_status(p.status, IPTTT_ERR_ARG);
+  if (threadIdx.x <= L) pw[threadIdx.x] = decay_pow(g, threadIdx.x);
+  const T* A = static_cast<const T*>(p.a) + (long long)b * p.T * p.lda + (long long)(h / p.ga) * Da;
+  const T* Bm = static_cast<const T*>(p.b) + (long long)b * p.T * p.ldb + (long long)(h / p.gb) * Da;
+  const T* C = static_cast<const T*>(p.c) + (long long)b * p.T * p.ldc + (long long)(h / p.gc) * p.Dc;
+  const uint32_t* words = p.starts ? p.starts + b * p.words : nullptr;
+  const bool only_state = p.out == nullptr;
+  if (only_state && seg == (p.rev ? 0 : p.segs - 1)) return;  // no segment comes after it
+
+  const int nchunks = (p.T + L - 1) / L;
+  const int first = seg * p.seg_chunks, last = min(nchunks, first + p.seg_chunks);
+  const int lo = first * L, hi = min(p.T, last * L);
+  const size_t bh = (size_t)b * p.H + h, nstate = (size_t)Da * p.Dc;
+  // the state the segment starts from
+  const int c = c0 + 4 * tx;
+  {
+    const int start = only_state ? 0 : nearest_start(p, b, p.rev ? hi : lo, sh);
+    __syncthreads();
+    for (int r = ty; r < Da; r += 16) {
+      float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (!only_state && c < p.Dc) {
+        float* e = reinterpret_cast<float*>(&f);
+        const float w0 = p.init ? p.init_mul * reach(p, g, -1, lo, hi, start, L) : 0.0f;
+        if (w0 != 0.0f)
+          for (int k = 0; k < 4; ++k) e[k] = w0 * p.init[bh * nstate + state_index(p, p.init_t, r, c + k)];
+        const int s0 = p.rev ? seg + 1 : 0, s1 = p.rev ? p.segs : seg;
+        for (int s = s0; s < s1; ++s) {
+          const float w = reach(p, g, s, lo, hi, start, L);
+          if (w == 0.0f) continue;
+          const float* in = p.seg_in + (bh * p.segs + s) * nstate;
+          for (int k = 0; k < 4; ++k) e[k] = fmaf(w, in[state_index(p, p.seg_t, r, c + k)], e[k]);
+        }
+      }
+      *reinterpret_cast<float4*>(F + r * kSlice + 4 * tx) = f;
+    }
+  }
+
+  for (int n = 0; n < last - first; ++n) {
+    const int ch = p.rev ? last - 1 - n : first + n;
+    const int t0 = ch * L, len = min(L, p.T - t0);
+    const uint32_t w = words ? words[ch] : 0u;  // one word of starts a chunk
+    const int first_start = w ? __ffs(w) - 1 : L, last_start = w ? 31 - __clz(w) : 0;
+    const int lag = p.rev && t0 + len == p.T ? 1 : 0;
+    __syncthreads();  // the last chunk's readers
+    const float4 zero = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int i = threadIdx.x; i < L * (Da / 4); i += kThreads) {
+      const int r = i / (Da / 4), q = 4 * (i % (Da / 4));
+      const bool on = r < len;
+      *reinterpret_cast<float4*>(sb + r * lda + q) = on ? load4(Bm + (t0 + r) * p.ldb + q) : zero;
+      if (!only_state) *reinterpret_cast<float4*>(sa + r * lda + q) = on ? load4(A + (t0 + r) * p.lda + q) : zero;
+    }
+    for (int i = threadIdx.x; i < L * (kSlice / 4); i += kThreads) {
+      const int r = i / (kSlice / 4), q = 4 * (i % (kSlice / 4));
+      *reinterpret_cast<float4*>(sc + r * kSlice + q) =
+          r < len && c0 + q < p.Dc ? load4(C + (t0 + r) * p.ldc + c0 + q) : zero;
+    }
+    if (threadIdx.x < L) {
+      const int i = threadIdx.x;
+      const bool in = p.rev ? i >= last_start : i < first_start;
+      const bool out = p.rev ? i < first_start : i >= last_start;
+      win[i] = in && i < len ? pw[p.rev ? len - i - lag : i + 1] : 0.0f;
+      wout[i] = out && i < len ? pw[p.rev ? i : len - 1 - i] : 0.0f;
+    }
+    __syncthreads();
+    if (!only_state) {
+      float s[2][2] = {};
+      for (int d = 0; d < Da; d += 4) {
+        float4 x[2], y[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          x[u] = *reinterpret_cast<const float4*>(sa + (ty + 16 * u) * lda + d);
+          y[u] = *reinterpret_cast<const float4*>(sb + (tx + 16 * u) * lda + d);
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int v = 0; v < 2; ++v)
+            s[u][v] = fmaf(x[u].x, y[v].x, fmaf(x[u].y, y[v].y, fmaf(x[u].z, y[v].z, fmaf(x[u].w, y[v].w, s[u][v]))));
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int i = ty + 16 * u;
+        // the tokens of i's document on the side the pass looks at: [from, to)
+        const uint32_t below = w & ((2u << i) - 1u), above = i == 31 ? 0u : w >> (i + 1);
+        const int from = p.rev ? i : (below ? 31 - __clz(below) : 0);
+        const int to = p.rev ? (above ? i + __ffs(above) : L) : i + 1;
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+          const int j = tx + 16 * v;
+          sp[i * (L + 1) + j] = j >= from && j < to ? s[u][v] * pw[abs(i - j)] : 0.0f;
+        }
+      }
+      __syncthreads();
+      float4 o[2], e[2];
+      o[0] = o[1] = e[0] = e[1] = zero;
+      for (int j = 0; j < L; ++j) {
+        const float4 v = *reinterpret_cast<const float4*>(sc + j * kSlice + 4 * tx);
+        fma4(o[0], sp[ty * (L + 1) + j], v);
+        fma4(o[1], sp[(ty + 16) * (L + 1) + j], v);
+      }
+      for (int d = 0; d < Da; ++d) {
+        const float4 f = *reinterpret_cast<const float4*>(F + d * kSlice + 4 * tx);
+        fma4(e[0], sa[ty * lda + d], f);
+        fma4(e[1], sa[(ty + 16) * lda + d], f);
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int i = ty + 16 * u;
+        if (i >= len || c >= p.Dc) continue;
+        if (win[i] != 0.0f) fma4(o[u], win[i], e[u]);
+        const long long at = ((long long)b * p.T + t0 + i) * p.ldo + (long long)h * p.Dc + c;
+        const float4 r = scale4(o[u], p.scale);
+        if (p.out_f32) store4(static_cast<float*>(p.out) + at, r);
+        else store4(static_cast<T*>(p.out) + at, r);
+      }
+      __syncthreads();
+    }
+    const float keep = w ? 0.0f : pw[len - lag];
+    for (int r = ty; r < Da; r += 16) {
+      float4* fp = reinterpret_cast<float4*>(F + r * kSlice + 4 * tx);
+      float4 f = keep != 0.0f ? scale4(*fp, keep) : zero;
+      for (int j = 0; j < len; ++j) {
+        const float x = wout[j];
+        if (x != 0.0f) fma4(f, sb[j * lda + r] * x, *reinterpret_cast<const float4*>(sc + j * kSlice + 4 * tx));
+      }
+      *fp = f;
+    }
+  }
+
+  float* dst = nullptr;
+  float mul = 1.0f;
+  if (only_state) {
+    dst = p.seg_state + (bh * p.segs + seg) * nstate;
+  } else if (p.fin && (p.rev ? seg == 0 : seg == p.segs - 1)) {
+    dst = p.fin + bh * nstate;
+    if (p.fin_scale) mul = p.scale * decay_pow(g, 1);
+  }
+  if (dst && c < p.Dc) {
+    for (int r = ty; r < Da; r += 16)  // a thread's own elements: no barrier since they were written
+      store4(dst + (size_t)r * p.Dc + c, scale4(*reinterpret_cast<const float4*>(F + r * kSlice + 4 * tx), mul));
+  }
+}
+
+// ------------------------------------------------------------------ shared heads
+
+// out[token][hk] = the sum over the group's heads, in head order, of part[token][hk * G + g] (fp32).
+template <typename T>
+__global__ void __launch_bounds__(kThreads) k_sum_heads(const float* part, T* out, long long tokens, int Hkv, int G, int D,
+                                                      long long ldo) {
+  const int dq = D / 4;
+  const long long per = (long long)Hkv * dq, n = tokens * per;
+  for (long long i = blockIdx.x * (long long)kThreads + threadIdx.x; i < n; i += (long long)gridDim.x * kThreads) {
+    const long long t = i / per;
+    const int e = (int)(i % per), hk = e / dq, q = 4 * (e % dq);
+    const float* x = part + ((t * Hkv + hk) * G) * (long long)D + q;
+    float4 s = load4(x);
+    for (int g = 1; g < G; ++g) {
+      const float4 y = load4(x + (long long)g * D);
+      s = make_float4(s.x + y.x, s.y + y.y, s.z + y.z, s.w + y.w);
+    }
+    store4(out + t * ldo + (long long)hk * D + q, s);
+  }
+}
+
+// ------------------------------------------------------------------ one token
+
+// S <- gamma S + k v^T and o = scale q S for one (row, head) and COLS columns of the state
+// a block.  Bound by HBM: the state is read and written once; a thread has all its
+// rows' loads in flight before it uses one.
+template <typename T, int COLS, int ROWS>
+__global__ void __launch_bounds__(kThreads) k_step(float* S, const T* q, const T* k, const T* v, const float* log_decay,
+                                                 const int32_t* starts, T* o, int H, int G, int Dk, int Dv,
+                                                 long long ldq, long long ldk, long long ldv, long long ldo,
+                                                 float scale, int* status) {
+  constexpr int LANES = COLS / 4, GROUPS = kThreads / LANES;  // a group of LANES threads takes a row of the state
+  __shared__ __align__(16) float part[GROUPS][COLS];
+  __shared__ float sq[kMaxWidth], sk[kMaxWidth];
+  const int b = blockIdx.x / H, h = blockIdx.x % H;
+  const int grp = threadIdx.x / LANES, c = blockIdx.y * COLS + 4 * (threadIdx.x % LANES);
+  const float g = log_decay[h];
+  if (threadIdx.x == 0 && !(g <= 0.0f)) set_status(status, IPTTT_ERR_ARG);
+  const bool fresh = starts && starts[b] != 0;
+  const float gamma = decay_pow(g, 1);
+  const T* qp = q + b * ldq + (long long)h * Dk;
+  const T* kp = k + b * ldk + (long long)(h / G) * Dk;
+  for (int i = threadIdx.x; i < Dk; i += kThreads) {
+    sq[i] = to_f(qp[i]);
+    sk[i] = to_f(kp[i]);
+  }
+  const float4 zero = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  float* st = S + ((size_t)blockIdx.x * Dk) * Dv + c;
+  const bool on = c < Dv;
+  float4 vv = zero, acc = zero;
+  if (on) vv = load4(v + b * ldv + (long long)(h / G) * Dv + c);
+  bool waited = false;
+  for (int r0 = grp; r0 < Dk || !waited; r0 += GROUPS * ROWS) {
+    float4 s[ROWS];
+#pragma unroll
+    for (int u = 0; u < ROWS; ++u) {
+      const int r = r0 + u * GROUPS;
+      s[u] = on && !fresh && r < Dk ? load4(st + (size_t)r * Dv) : zero;
+    }
+    if (!waited) {  // sq and sk; the state's loads are under way
+      __syncthreads();
+      waited = true;
+    }
+#pragma unroll
+    for (int u = 0; u < ROWS; ++u) {
+      const int r = r0 + u * GROUPS;
+      if (!on || r >= Dk) continue;
+      float4 x = scale4(s[u], gamma);
+      fma4(x, sk[r], vv);
+      fma4(acc, sq[r], x);
+      store4(st + (size_t)r * Dv, x);
+    }
+  }
+  *reinterpret_cast<float4*>(&part[grp][4 * (threadIdx.x % LANES)]) = acc;
+  __syncthreads();
+  const int e = blockIdx.y * COLS + threadIdx.x;
+  if (threadIdx.x < COLS && e < Dv) {
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < GROUPS; ++i) s += part[i][threadIdx.x];
+    o[b * ldo + (long long)h * Dv + e] = from_f<T>(s * scale);
+  }
+}
+
+template <typename T>
+cudaError_t launch_step(const ipttt_linattn_params& p, float* S, const void* q, const void* k, const void* v,
+                        const float* ld, const int32_t* starts, void* o, int* status, cudaStream_t st) {
+  const int blocks = p.B * p.H, G = p.H / p.Hkv;
+  // whole rows of the state where (row, head) pairs alone fill the SMs twice, else quarter rows
+  if (blocks >= 296)
+    k_step<T, 128, 16><<<dim3(blocks, (p.Dv + 127) / 128), kThreads, 0, st>>>(
+        S, static_cast<const T*>(q), static_cast<const T*>(k), static_cast<const T*>(v), ld, starts, static_cast<T*>(o),
+        p.H, G, p.Dk, p.Dv, p.ldq, p.ldk, p.ldv, p.ldo, p.scale, status);
+  else
+    k_step<T, 32, 4><<<dim3(blocks, (p.Dv + 31) / 32), kThreads, 0, st>>>(
+        S, static_cast<const T*>(q), static_cast<const T*>(k), static_cast<const T*>(v), ld, starts, static_cast<T*>(o),
+        p.H, G, p.Dk, p.Dv, p.ldq, p.ldk, p.ldv, p.ldo, p.scale, status);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+int simt_segments(int B, int T, int H, int Da, int Dc, int* seg_chunks) {
+  (void)Da;
+  const int nchunks = (T + L - 1) / L;
+  const long long blocks = (long long)B * H * ((Dc + kSlice - 1) / kSlice);
+  // one segment where the rows, heads and column slices fill the SMs, else enough
+  // segments of at least 8 chunks to do so
+  int segs = (int)std::min<long long>((nchunks + 7) / 8, (148 + blocks - 1) / blocks);
+  segs = std::max(1, segs);
+  *seg_chunks = (nchunks + segs - 1) / segs;
+  return (nchunks + *seg_chunks - 1) / *seg_chunks;
+}
+
+cudaError_t run_simt(const Pass& p, int dtype, cudaStream_t st) {
+  const size_t smem = simt_smem(p.Da);
+  const dim3 grid((p.Dc + kSlice - 1) / kSlice, p.B * p.H, p.segs);
+  cudaError_t e;
+  if (dtype == IPTTT_BF16) {
+    e = cudaFuncSetAttribute(k_pass<__nv_bfloat16>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    k_pass<__nv_bfloat16><<<grid, kThreads, smem, st>>>(p);
+  } else {
+    e = cudaFuncSetAttribute(k_pass<float>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    k_pass<float><<<grid, kThreads, smem, st>>>(p);
+  }
+  return cudaGetLastError();
+}
+
+// ------------------------------------------------------------------ entry points
+
+namespace {
+
+size_t al256(size_t x) { return (x + 255) & ~size_t(255); }
+
+ipttt_status check(const ipttt_linattn_params* p) {
+  if (!p) return IPTTT_ERR_ARG;
+  if (p->dtype != IPTTT_F32 && p->dtype != IPTTT_BF16) return IPTTT_ERR_DTYPE;
+  if (p->B <= 0 || p->T <= 0 || p->H <= 0 || p->Hkv <= 0 || p->Dk <= 0 || p->Dv <= 0) return IPTTT_ERR_ARG;
+  if (p->H % p->Hkv != 0 || !isfinite(p->scale) || p->scale == 0.0f) return IPTTT_ERR_ARG;
+  if (p->Dk % 8 != 0 || p->Dv % 8 != 0 || p->Dk > kMaxWidth || p->Dv > kMaxWidth) return IPTTT_ERR_UNSUPPORTED;
+  if ((long long)p->B * p->T > (1ll << 30) || (long long)p->B * p->H > 65535 || p->H > 65535) return IPTTT_ERR_SHAPE;
+  struct { long long ld, packed; } lds[] = {
+      {p->ldq, (long long)p->H * p->Dk},   {p->ldk, (long long)p->Hkv * p->Dk}, {p->ldv, (long long)p->Hkv * p->Dv},
+      {p->ldo, (long long)p->H * p->Dv},   {p->ldgq, (long long)p->H * p->Dk},  {p->ldgk, (long long)p->Hkv * p->Dk},
+      {p->ldgv, (long long)p->Hkv * p->Dv}};
+  for (const auto& x : lds)
+    if (x.ld != 0 && (x.ld < x.packed || x.ld % 8 != 0 || x.ld > (1ll << 31))) return IPTTT_ERR_ARG;
+  return IPTTT_OK;
+}
+
+// The parameters with every stride filled in.
+ipttt_linattn_params filled(const ipttt_linattn_params& p) {
+  ipttt_linattn_params f = p;
+  auto set = [](int64_t& ld, long long packed) { if (ld == 0) ld = packed; };
+  set(f.ldq, (long long)p.H * p.Dk);
+  set(f.ldk, (long long)p.Hkv * p.Dk);
+  set(f.ldv, (long long)p.Hkv * p.Dv);
+  set(f.ldo, (long long)p.H * p.Dv);
+  set(f.ldgq, (long long)p.H * p.Dk);
+  set(f.ldgk, (long long)p.Hkv * p.Dk);
+  set(f.ldgv, (long long)p.Hkv * p.Dv);
+  return f;
+}
+
+bool aligned16(std::initializer_list<const void*> ps) {
+  uintptr_t any = 0;
+  for (const void* q : ps) any |= reinterpret_cast<uintptr_t>(q);
+  return any % 16 == 0;
+}
+
+struct Work {
+  size_t starts, seg, S0, parts, total;
+  long long words;
+  int segs_o, chunks_o;  // passes whose output is Dv wide (O, gv)
+  int segs_q, chunks_q;  // passes whose output is Dk wide (gq, gk)
+};
+
+Work work_of(const ipttt_linattn_params& p, bool backward) {
+  Work w{};
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t o = off;
+    off += al256(bytes);
+    return o;
+  };
+  w.words = (p.T + 31) / 32;
+  w.starts = take((size_t)p.B * w.words * 4);
+  w.segs_o = simt_segments(p.B, p.T, p.H, p.Dk, p.Dv, &w.chunks_o);
+  w.segs_q = simt_segments(p.B, p.T, p.H, p.Dv, p.Dk, &w.chunks_q);
+  const int segs = backward ? std::max(w.segs_o, w.segs_q) : w.segs_o;
+  w.seg = take(segs > 1 ? (size_t)p.B * p.H * segs * p.Dk * p.Dv * 4 : 0);
+  w.S0 = take(!backward && segs > 1 ? (size_t)p.B * p.H * p.Dk * p.Dv * 4 : 0);
+  w.parts = take(backward && p.H != p.Hkv ? (size_t)p.B * p.T * p.H * std::max(p.Dk, p.Dv) * 4 : 0);
+  w.total = std::max<size_t>(off, 256);
+  return w;
+}
+
+// A pass, after its segments' own states where the row is cut into segments.
+cudaError_t run_pass(const ipttt_linattn_params& p, Pass q, float* seg, int* launches, cudaStream_t st) {
+  if (q.segs > 1) {
+    Pass s = q;
+    s.out = nullptr;
+    s.seg_state = seg;
+    const cudaError_t e = run_simt(s, p.dtype, st);
+    if (e != cudaSuccess) return e;
+    ++*launches;
+    q.seg_in = seg;
+  }
+  ++*launches;
+  return run_simt(q, p.dtype, st);
+}
+
+// The start bits of the call, or null where no start is listed.
+cudaError_t mark_starts(const ipttt_linattn_params& p, const Work& w, uint8_t* ws, const int32_t* ds, int n, int* status,
+                        const uint32_t** out, int* launches, cudaStream_t st) {
+  *out = nullptr;
+  if (n == 0) return cudaSuccess;
+  uint32_t* words = reinterpret_cast<uint32_t*>(ws + w.starts);
+  cudaError_t e = cudaMemsetAsync(words, 0, (size_t)p.B * w.words * 4, st);
+  if (e != cudaSuccess) return e;
+  k_mark<<<(n + 255) / 256, 256, 0, st>>>(words, w.words, p.B, p.T, ds, n, status);
+  ++*launches;
+  *out = words;
+  return cudaGetLastError();
+}
+
+}  // namespace
+}  // namespace la
+}  // namespace ipttt
+
+using namespace ipttt;
+using namespace ipttt::la;
+
+extern "C" {
+
+size_t ipttt_linattn_workspace_size(const ipttt_linattn_params* p) {
+  return check(p) == IPTTT_OK ? work_of(*p, false).total : 0;
+}
+
+size_t ipttt_linattn_backward_workspace_size(const ipttt_linattn_params* p) {
+  return check(p) == IPTTT_OK ? work_of(*p, true).total : 0;
+}
+
+ipttt_status ipttt_linattn_forward(const ipttt_linattn_params* pp, const void* q, const void* k, const void* v,
+                                   const float* log_decay, const int32_t* doc_starts, int32_t n_doc_starts,
+                                   const float* S0_opt, void* O, float* S_final_opt, void* workspace,
+                                   size_t workspace_bytes, void* stream) {
+  const ipttt_status rc = check(pp);
+  if (rc != IPTTT_OK) return rc;
+  if (!q || !k || !v || !log_decay || !O || n_doc_starts < 0 || (n_doc_starts > 0 && !doc_starts)) return IPTTT_ERR_ARG;
+  if (!aligned16({q, k, v, O, S0_opt, S_final_opt})) return IPTTT_ERR_ALIGN;
+  const Work w = work_of(*pp, false);
+  if (!workspace || workspace_bytes < w.total) return IPTTT_ERR_WORKSPACE;
+  if (reinterpret_cast<uintptr_t>(workspace) % 256) return IPTTT_ERR_ALIGN;
+  const ipttt_linattn_params p = filled(*pp);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  int* status = device_status();
+  int launches = 0;
+  Pass a{};
+  a.B = p.B;
+  a.T = p.T;
+  a.H = p.H;
+  a.log_decay = log_decay;
+  a.words = w.words;
+  a.scale = p.scale;
+  a.init_mul = 1.0f;
+  a.status = status;
+  const int G = p.H / p.Hkv;
+  a.a = q;
+  a.lda = p.ldq;
+  a.ga = 1;
+  a.b = k;
+  a.ldb = p.ldk;
+  a.gb = G;
+  a.c = v;
+  a.ldc = p.ldv;
+  a.gc = G;
+  a.Da = p.Dk;
+  a.Dc = p.Dv;
+  a.out = O;
+  a.ldo = p.ldo;
+  a.init = S0_opt;
+  a.fin = S_final_opt;
+  a.segs = w.segs_o;
+  a.seg_chunks = w.chunks_o;
+  cudaError_t e = mark_starts(p, w, ws, doc_starts, n_doc_starts, status, &a.starts, &launches, st);
+  if (e == cudaSuccess && S0_opt && S0_opt == S_final_opt && a.segs > 1) {
+    // the last segment may write the final state before the others have read the first
+    a.init = reinterpret_cast<const float*>(ws + w.S0);
+    e = cudaMemcpyAsync(ws + w.S0, S0_opt, (size_t)p.B * p.H * p.Dk * p.Dv * 4, cudaMemcpyDeviceToDevice, st);
+  }
+  if (e == cudaSuccess) e = run_pass(p, a, reinterpret_cast<float*>(ws + w.seg), &launches, st);
+  if (e != cudaSuccess) return cuda_fail("linattn_forward", e);
+  count_launches(launches);
+  return IPTTT_OK;
+}
+
+ipttt_status ipttt_linattn_backward(const ipttt_linattn_params* pp, const void* q, const void* k, const void* v,
+                                    const float* log_decay, const int32_t* doc_starts, int32_t n_doc_starts,
+                                    const float* S0_opt, const void* gO, const float* gS_final_opt, void* gq, void* gk,
+                                    void* gv, float* gS0_opt, void* workspace, size_t workspace_bytes, void* stream) {
+  const ipttt_status rc = check(pp);
+  if (rc != IPTTT_OK) return rc;
+  if (!q || !k || !v || !log_decay || !gO || !gq || !gk || !gv || n_doc_starts < 0 || (n_doc_starts > 0 && !doc_starts))
+    return IPTTT_ERR_ARG;
+  if (gS0_opt && gS0_opt == gS_final_opt) return IPTTT_ERR_ARG;  // gS0 is written before gS_final's last reader
+  if (!aligned16({q, k, v, gO, gq, gk, gv, S0_opt, gS_final_opt, gS0_opt})) return IPTTT_ERR_ALIGN;
+  const Work w = work_of(*pp, true);
+  if (!workspace || workspace_bytes < w.total) return IPTTT_ERR_WORKSPACE;
+  if (reinterpret_cast<uintptr_t>(workspace) % 256) return IPTTT_ERR_ALIGN;
+  const ipttt_linattn_params p = filled(*pp);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  float* seg = reinterpret_cast<float*>(ws + w.seg);
+  float* parts = reinterpret_cast<float*>(ws + w.parts);
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  int* status = device_status();
+  int launches = 0;
+  const int G = p.H / p.Hkv;
+  Pass base{};
+  base.B = p.B;
+  base.T = p.T;
+  base.H = p.H;
+  base.log_decay = log_decay;
+  base.words = w.words;
+  base.scale = p.scale;
+  base.status = status;
+  cudaError_t e = mark_starts(p, w, ws, doc_starts, n_doc_starts, status, &base.starts, &launches, st);
+
+  struct Arg {
+    const void* x;
+    long long ld;
+    int g;
+  };
+  const Arg xq{q, p.ldq, 1}, xk{k, p.ldk, G}, xv{v, p.ldv, G}, xg{gO, p.ldo, 1};
+  auto pass_of = [&](const Arg& a, const Arg& b, const Arg& c, int Da, int Dc) {
+    Pass s = base;
+    s.a = a.x;
+    s.lda = a.ld;
+    s.ga = a.g;
+    s.b = b.x;
+    s.ldb = b.ld;
+    s.gb = b.g;
+    s.c = c.x;
+    s.ldc = c.ld;
+    s.gc = c.g;
+    s.Da = Da;
+    s.Dc = Dc;
+    s.segs = Dc == p.Dv && Da == p.Dk ? w.segs_o : w.segs_q;
+    s.seg_chunks = Dc == p.Dv && Da == p.Dk ? w.chunks_o : w.chunks_q;
+    return s;
+  };
+  // a gradient of k or v: straight to the output, or per head in fp32 and then summed over the group
+  auto shared = [&](Pass s, void* out, long long ldo, int D) {
+    s.rev = 1;
+    s.init = gS_final_opt;
+    s.init_mul = 1.0f / p.scale;
+    if (G == 1) {
+      s.out = out;
+      s.ldo = ldo;
+      return run_pass(p, s, seg, &launches, st);
+    }
+    s.out = parts;
+    s.out_f32 = 1;
+    s.ldo = (long long)p.H * D;
+    const cudaError_t err = run_pass(p, s, seg, &launches, st);
+    if (err != cudaSuccess) return err;
+    const long long tokens = (long long)p.B * p.T, n = tokens * p.Hkv * (D / 4);
+    const unsigned grid = (unsigned)std::min<long long>((n + kThreads - 1) / kThreads, 148 * 16);
+    if (p.dtype == IPTTT_BF16)
+      k_sum_heads<<<grid, kThreads, 0, st>>>(parts, static_cast<__nv_bfloat16*>(out), tokens, p.Hkv, G, D, ldo);
+    else
+      k_sum_heads<<<grid, kThreads, 0, st>>>(parts, static_cast<float*>(out), tokens, p.Hkv, G, D, ldo);
+    ++launches;
+    return cudaGetLastError();
+  };
+
+  if (e == cudaSuccess) {
+    Pass s = pass_of(xg, xv, xk, p.Dv, p.Dk);  // gq, the state transposed
+    s.init = S0_opt;
+    s.init_mul = 1.0f;
+    s.init_t = 1;
+    s.out = gq;
+    s.ldo = p.ldgq;
+    e = run_pass(p, s, seg, &launches, st);
+  }
+  if (e == cudaSuccess) {
+    Pass s = pass_of(xk, xq, xg, p.Dk, p.Dv);  // gv, and R's last value gives gS0
+    s.fin = gS0_opt;
+    s.fin_scale = 1;
+    e = shared(s, gv, p.ldgv, p.Dv);
+  }
+  if (e == cudaSuccess) {
+    Pass s = pass_of(xv, xg, xq, p.Dv, p.Dk);  // gk, R transposed
+    s.init_t = 1;
+    e = shared(s, gk, p.ldgk, p.Dk);
+  }
+  if (e != cudaSuccess) return cuda_fail("linattn_backward", e);
+  count_launches(launches);
+  return IPTTT_OK;
+}
+
+ipttt_status ipttt_linattn_step(const ipttt_linattn_params* pp, float* S, const void* q, const void* k, const void* v,
+                                const float* log_decay, const int32_t* starts_opt, void* o, void* stream) {
+  const ipttt_status rc = check(pp);
+  if (rc != IPTTT_OK) return rc;
+  if (pp->T != 1 || !S || !q || !k || !v || !log_decay || !o) return IPTTT_ERR_ARG;
+  if (!aligned16({S, q, k, v, o})) return IPTTT_ERR_ALIGN;
+  const ipttt_linattn_params p = filled(*pp);
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = p.dtype == IPTTT_BF16
+                            ? launch_step<__nv_bfloat16>(p, S, q, k, v, log_decay, starts_opt, o, device_status(), st)
+                            : launch_step<float>(p, S, q, k, v, log_decay, starts_opt, o, device_status(), st);
+  if (e != cudaSuccess) return cuda_fail("linattn_step", e);
+  count_launches(1);
+  return IPTTT_OK;
+}
+
+}  // extern "C"

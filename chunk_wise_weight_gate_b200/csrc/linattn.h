@@ -1,0 +1,104 @@
+// Linear attention with a decay for each head: what the entry points (linattn.cu) and
+// the tensor-core kernel (linattn_tc.cu) share.
+//
+// Everything is one pass, run with different operands:
+//   out_i = scale * sum_j w(i, j) (a_i . b_j) c_j + (what the state brought in adds),
+// w = gamma^{|i - j|} over the tokens j of i's document up to i (forwards) or from i on
+// (backwards in time, `rev`), with the state F = sum_j gamma^{..} b_j c_j^T [Da, Dc]:
+//   O  : a = q,  b = k,  c = v,  forwards;     F = S
+//   gq : a = gO, b = v,  c = k,  forwards;     F = S^T
+//   gv : a = k,  b = q,  c = gO, backwards;    F = R = sum gamma^{..} q gO^T
+//   gk : a = v,  b = gO, c = q,  backwards;    F = R^T
+// Forwards, F after a token is S at that token; row i of a chunk sees the state from
+// before the chunk with gamma^{i+1}.  Backwards, F is R at the token last taken; the
+// state's gradient enters before the last token without a decay of its own (`rev`
+// passes take one factor less in the row's last chunk).
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include "common.cuh"
+
+namespace ipttt {
+namespace la {
+
+struct Pass {
+  const void *a, *b, *c;         // [B*T tokens][heads][width], strides in elements
+  long long lda, ldb, ldc;
+  int ga, gb, gc;                // head h of the pass reads head h / g of the operand
+  void* out;                     // null: the pass leaves only each segment's state (in seg_state)
+  long long ldo;
+  int out_f32;                   // out is fp32 whatever the operands' type
+  const float* init;             // [B][H] states before the first token taken, or null
+  int init_t, seg_t;             // init, seg_in are stored transposed ([Dc][Da])
+  float init_mul;                // factor on init
+  float* fin;                    // [B][H][Da][Dc] state after the last token taken, or null
+  int fin_scale;                 // fin gets scale * gamma * F: the gradient of S0 from R
+  const float* log_decay;        // [H]
+  const uint32_t* starts;        // bit t % 32 of word [b][t / 32]: token t starts a document; null: none
+  long long words;               // words of a row
+  const float* seg_in;           // [B][H][segs][Da][Dc]: the segments' own states (segs > 1)
+  float* seg_state;              // the same array, written when out is null
+  int segs, seg_chunks;          // segments of a row, chunks of each (the last may have fewer)
+  int B, T, H, Da, Dc;
+  int rev;
+  float scale;
+  int* status;
+};
+
+__device__ __forceinline__ float decay_pow(float g, int n) { return n <= 0 ? 1.0f : expf(g * (float)n); }
+
+// The nearest start on the far side of a segment: forwards the last start before token
+// `at` (-1: none), backwards the first start from token `at` on (T: none).  All threads
+// of the block take part; `sh` is one int of shared memory.
+__device__ __forceinline__ int nearest_start(const Pass& p, int b, int at, int* sh) {
+  const int none = p.rev ? p.T : -1;
+  if (!p.starts) return none;
+  if (threadIdx.x == 0) *sh = none;
+  __syncthreads();
+  const uint32_t* w = p.starts + b * p.words;
+  int best = none;
+  if (p.rev) {
+    for (int i = at / 32 + threadIdx.x; i < p.words; i += blockDim.x)
+      if (w[i]) {
+        const uint32_t m = i == at / 32 ? w[i] & (0xffffffffu << (at % 32)) : w[i];
+        if (m) best = min(best, 32 * i + __ffs(m) - 1);
+      }
+    if (best != none) atomicMin(sh, best);
+  } else {
+    for (int i = threadIdx.x; 32 * i < at; i += blockDim.x)
+      if (w[i]) {
+        const uint32_t m = i == at / 32 ? w[i] & ((1u << (at % 32)) - 1u) : w[i];
+        if (m) best = max(best, 32 * i + 31 - __clz(m));
+      }
+    if (best != none) atomicMax(sh, best);
+  }
+  __syncthreads();
+  return *sh;
+}
+
+// Factor with which segment s's own state, and the initial state (s = -1), reach the
+// segment of tokens [lo, hi): 0 where a document starts between.
+__device__ __forceinline__ float reach(const Pass& p, float g, int s, int lo, int hi, int start, int chunk) {
+  if (p.rev) {
+    if (s < 0) return start < p.T ? 0.0f : decay_pow(g, p.T - 1 - hi);
+    const int s0 = s * p.seg_chunks * chunk;
+    return s0 <= start ? decay_pow(g, s0 - hi) : 0.0f;
+  }
+  if (s < 0) return start >= 0 ? 0.0f : decay_pow(g, lo);
+  const int end = (s + 1) * p.seg_chunks * chunk;
+  return end > start ? decay_pow(g, lo - end) : 0.0f;
+}
+
+// Where element (r, c) of a state lies.
+__device__ __forceinline__ size_t state_index(const Pass& p, int transposed, int r, int c) {
+  return transposed ? (size_t)c * p.Da + r : (size_t)r * p.Dc + c;
+}
+
+// The CUDA-core pass (any widths up to 256, fp32 or bf16 operands), chunks of 32 tokens.
+constexpr int kSimtChunk = 32;
+cudaError_t run_simt(const Pass& p, int dtype, cudaStream_t st);
+int simt_segments(int B, int T, int H, int Da, int Dc, int* seg_chunks);
+
+}  // namespace la
+}  // namespace ipttt

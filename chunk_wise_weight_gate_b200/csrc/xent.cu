@@ -1,0 +1,416 @@
+// Softmax cross entropy of a linear head in pieces of the vocabulary
+// (ipttt_xent_forward, ipttt_xent_backward).
+//
+// Mathematics: the logits l = H W^T of a piece are formed, folded into each row's
+// running maximum m and sum s = sum exp(l - m), and dropped; lse = m + log s and
+// loss = lse - l[target].  Backward: the piece's logits again, p = (exp(l - lse) -
+// onehot) gloss, then gH += p W_piece and gW_piece = p^T H.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+
+#include <algorithm>
+
+#include "common.cuh"
+#include "gemm.h"
+
+namespace ipttt {
+namespace {
+
+constexpr int kThreads = 256;
+
+// ------------------------------------------------------------------ fp32 products
+
+// out[slice][m][n] = sum over the slice of k of A(m, k) B(k, n), fp32 FMA.  An operand is
+// either K-major (A[m * lda + k]) or MN-major (A[k * lda + m]); K-major operands have
+// K a multiple of 4, MN-major ones rows readable up to a multiple of 4 columns.
+// 128 x 128 tiles, 8 x 8 products a thread (two 4-wide strips 64 apart in either
+// direction), 16 k a step, the next step's operands in registers meanwhile.
+constexpr int SM = 128, SK = 16;
+struct Sgemm {
+  const float *A, *B;
+  float* out;
+  long long lda, ldb, ldo, osz;
+  int M, N, K, slices;
+  int a_cols, b_cols;  // MN-major operands: readable columns
+  int add;             // add to out
+};
+
+template <bool KMAJOR>
+__device__ __forceinline__ void fetch(const float* X, long long ld, int rows, int cols, int k1, int r0, int k0, float4 (&v)[2]) {
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int i = threadIdx.x + u * kThreads;
+    v[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (KMAJOR) {
+      const int r = r0 + i / 4, k = k0 + 4 * (i % 4);
+      if (r < rows && k < k1) v[u] = *reinterpret_cast<const float4*>(X + r * ld + k);
+    } else {
+      const int k = k0 + i / 32, r = r0 + 4 * (i % 32);
+      if (k < k1 && r < cols) v[u] = *reinterpret_cast<const float4*>(X + k * ld + r);
+    }
+  }
+}
+
+template <bool KMAJOR>
+__device__ __forceinline__ void place(float (*s)[SM + 4], const float4 (&v)[2]) {
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int i = threadIdx.x + u * kThreads;
+    if (KMAJOR) {
+      const int r = i / 4, k = 4 * (i % 4);
+      s[k][r] = v[u].x;
+      s[k + 1][r] = v[u].y;
+      s[k + 2][r] = v[u].z;
+      s[k + 3][r] = v[u].w;
+    } else {
+      *reinterpret_cast<float4*>(&s[i / 32][4 * (i % 32)]) = v[u];
+    }
+  }
+}
+
+template <bool AK, bool BK>
+__global__ void __launch_bounds__(kThreads, 2) k_sgemm(const Sgemm g) {
+  __shared__ __align__(16) float as[2][SK][SM + 4], bs[2][SK][SM + 4];
+  const int m0 = blockIdx.y * SM, n0 = blockIdx.x * SM;
+  const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
+  const int blocks = (g.K + SK - 1) / SK;
+  const int kb0 = (int)((long long)blocks * blockIdx.z / g.slices), kb1 = (int)((long long)blocks * (blockIdx.z + 1) / g.slices);
+  float acc[8][8] = {};
+  float4 av[2], bv[2];
+  if (kb0 < kb1) {
+    fetch<AK>(g.A, g.lda, g.M, g.a_cols, g.K, m0, kb0 * SK, av);
+    fetch<BK>(g.B, g.ldb, g.N, g.b_cols, g.K, n0, kb0 * SK, bv);
+    place<AK>(as[0], av);
+    place<BK>(bs[0], bv);
+  }
+  __syncthreads();
+  for (int kb = kb0; kb < kb1; ++kb) {
+    const int cur = (kb - kb0) & 1;
+    const bool more = kb + 1 < kb1;
+    if (more) {
+      fetch<AK>(g.A, g.lda, g.M, g.a_cols, g.K, m0, (kb + 1) * SK, av);
+      fetch<BK>(g.B, g.ldb, g.N, g.b_cols, g.K, n0, (kb + 1) * SK, bv);
+    }
+#pragma unroll
+    for (int k = 0; k < SK; ++k) {
+      float x[8], y[8];
+      *reinterpret_cast<float4*>(x) = *reinterpret_cast<const float4*>(&as[cur][k][4 * ty]);
+      *reinterpret_cast<float4*>(x + 4) = *reinterpret_cast<const float4*>(&as[cur][k][64 + 4 * ty]);
+      *reinterpret_cast<float4*>(y) = *reinterpret_cast<const float4*>(&bs[cur][k][4 * tx]);
+      *reinterpret_cast<float4*>(y + 4) = *reinterpret_cast<const float4*>(&bs[cur][k][64 + 4 * tx]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[i][j] = fmaf(x[i], y[j], acc[i][j]);
+    }
+    if (more) {
+      place<AK>(as[cur ^ 1], av);
+      place<BK>(bs[cur ^ 1], bv);
+    }
+    __syncthreads();
+  }
+  float* out = g.out + blockIdx.z * g.osz;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int m = m0 + (i / 4) * 64 + 4 * ty + i % 4;
+    if (m >= g.M) continue;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int n = n0 + (j / 4) * 64 + 4 * tx + j % 4;
+      if (n >= g.N) continue;
+      float* o = out + m * g.ldo + n;
+      *o = g.add ? *o + acc[i][j] : acc[i][j];
+    }
+  }
+}
+
+template <bool AK, bool BK>
+cudaError_t sgemm(const Sgemm& g, cudaStream_t st) {
+  k_sgemm<AK, BK><<<dim3((g.N + SM - 1) / SM, (g.M + SM - 1) / SM, g.slices), kThreads, 0, st>>>(g);
+  return cudaGetLastError();
+}
+
+// ------------------------------------------------------------------ the rows' statistics and gradients
+
+__device__ __forceinline__ float2 merge(float2 a, float2 b) {  // (maximum, sum) of two sets of logits
+  const float m = fmaxf(a.x, b.x);
+  if (m == -INFINITY) return make_float2(m, 0.0f);
+  return make_float2(m, a.y * expf(a.x - m) + b.y * expf(b.x - m));
+}
+
+__device__ __forceinline__ float2 block_merge(float2 v, float2* sh) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    v = merge(v, make_float2(__shfl_xor_sync(0xffffffffu, v.x, o), __shfl_xor_sync(0xffffffffu, v.y, o)));
+  if (threadIdx.x % 32 == 0) sh[threadIdx.x / 32] = v;
+  __syncthreads();
+  v = sh[0];
+  for (int i = 1; i < kThreads / 32; ++i) v = merge(v, sh[i]);
+  return v;
+}
+
+// One block a row: the piece's logits into the row's running maximum and sum, and
+// its target's logit.  The last piece writes lse and loss.
+__global__ void __launch_bounds__(kThreads) k_row_stats(const float* l, long long ld, int v0, int cols, int V, int last,
+                                                      const int64_t* targets, int64_t ignore, float2* run, float* tl,
+                                                      float* loss, float* lse, int* status) {
+  __shared__ float2 sh[kThreads / 32];
+  const int n = blockIdx.x;
+  const float* x = l + (long long)n * ld;
+  float2 v = make_float2(-INFINITY, 0.0f);
+  for (int i = threadIdx.x; i < cols; i += kThreads) v = merge(v, make_float2(x[i], 1.0f));
+  v = block_merge(v, sh);
+  if (threadIdx.x != 0) return;
+  if (v0 > 0) v = merge(run[n], v);
+  run[n] = v;
+  const int64_t t = targets[n];
+  if (t >= v0 && t < v0 + cols) tl[n] = x[t - v0];
+  if (!last) return;
+  const float s = v.x + logf(v.y);
+  lse[n] = s;
+  const bool out = t < 0 || t >= V;
+  if (out && t != ignore) set_status(status, IPTTT_ERR_ARG);
+  loss[n] = out || t == ignore ? 0.0f : s - tl[n];
+}
+
+// p = (exp(l - lse) - onehot) gloss for the piece's columns; 0 in the padding.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) k_row_grad(const float* l, T* p, long long ld, int v0, int cols, int padded, int V,
+                                                     const int64_t* targets, int64_t ignore, const float* lse,
+                                                     const float* gloss, int* status) {
+  const int n = blockIdx.x;
+  const int64_t t = targets[n];
+  const bool out = t < 0 || t >= V;
+  if (out && t != ignore && threadIdx.x == 0) set_status(status, IPTTT_ERR_ARG);
+  const bool on = !out && t != ignore;
+  const float s = lse[n], g = on ? gloss[n] : 0.0f;
+  for (int i = threadIdx.x; i < padded; i += kThreads) {
+    float v = 0.0f;
+    if (on && i < cols) v = (expf(l[(long long)n * ld + i] - s) - (t - v0 == i ? 1.0f : 0.0f)) * g;
+    p[(long long)n * ld + i] = from_f<T>(v);
+  }
+}
+
+// gH (in T) = the sum of the fp32 slices, in slice order.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) k_sum_slices(const float* part, T* out, long long n, int slices) {
+  for (long long i = blockIdx.x * (long long)kThreads + threadIdx.x; i < n; i += (long long)gridDim.x * kThreads) {
+    float s = part[i];
+    for (int q = 1; q < slices; ++q) s += part[q * n + i];
+    out[i] = from_f<T>(s);
+  }
+}
+
+// ------------------------------------------------------------------ sizes
+
+size_t al256(size_t x) { return (x + 255) & ~size_t(255); }
+
+constexpr size_t kPieceBytes = size_t(512) << 20;  // of a piece's logits and p
+
+ipttt_status check(const ipttt_xent_params* p) {
+  if (!p) return IPTTT_ERR_ARG;
+  if (p->dtype != IPTTT_F32 && p->dtype != IPTTT_BF16) return IPTTT_ERR_DTYPE;
+  if (p->N <= 0 || p->V <= 0 || p->d <= 0 || p->piece < 0 || p->piece % 256 != 0) return IPTTT_ERR_ARG;
+  if (p->d % (p->dtype == IPTTT_BF16 ? 32 : 4) != 0) return IPTTT_ERR_UNSUPPORTED;
+  if (p->N > (1 << 24) || p->V > (1 << 26) || p->d > (1 << 16)) return IPTTT_ERR_SHAPE;
+  return IPTTT_OK;
+}
+
+struct Work {
+  int piece;  // vocabulary rows at a time, a multiple of 256
+  int slices; // partial sums of gH: slices of a piece's columns
+  size_t logits, p, run, tl, gH, total;
+};
+
+Work work_of(const ipttt_xent_params& p, bool backward) {
+  Work w{};
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t o = off;
+    off += al256(bytes);
+    return o;
+  };
+  const long long all = ((long long)p.V + 255) / 256 * 256;
+  const long long row = (long long)p.N * 4;
+  w.piece = p.piece ? p.piece : (int)std::max<long long>(256, (long long)(kPieceBytes / row) / 256 * 256);
+  w.piece = (int)std::min<long long>(w.piece, all);
+  w.logits = take((size_t)p.N * w.piece * 4);
+  if (!backward) {
+    w.run = take((size_t)p.N * sizeof(float2));
+    w.tl = take((size_t)p.N * 4);
+  } else {
+    w.p = p.dtype == IPTTT_BF16 ? take((size_t)p.N * w.piece * 2) : w.logits;
+    // enough slices of K for gH's product to fill the SMs twice, each of at least 256 columns
+    const long long tiles = (long long)((p.N + 127) / 128) * ((p.d + 127) / 128);
+    w.slices = (int)std::max<long long>(1, std::min<long long>({(296 + tiles - 1) / tiles, w.piece / 256, 32}));
+    w.gH = take((size_t)p.N * p.d * 4 * w.slices);
+  }
+  w.total = off;
+  return w;
+}
+
+// The logits of vocabulary rows [v0, v0 + cols).
+cudaError_t logits_of(const ipttt_xent_params& p, const void* H, const void* W, int v0, int cols, float* out, long long ld,
+                      cudaStream_t st) {
+  if (p.dtype == IPTTT_F32) {
+    Sgemm g{static_cast<const float*>(H), static_cast<const float*>(W) + (long long)v0 * p.d, out, p.d, p.d, ld, 0,
+            p.N, cols, p.d, 1, 0, 0};
+    return sgemm<true, true>(g, st);
+  }
+  gemm::Args a{};
+  a.A = {H, (uint64_t)p.d, (uint64_t)p.N, 1};
+  a.Bop = {static_cast<const __nv_bfloat16*>(W) + (long long)v0 * p.d, (uint64_t)p.d, (uint64_t)cols, 1};
+  a.mode = gemm::GM_PLAIN;
+  a.M = p.N;
+  a.N = (cols + 31) / 32 * 32;
+  a.K = p.d;
+  a.out_kind = gemm::GO_F32;
+  a.out = out;
+  a.ldo = ld;
+  a.status = device_status();
+  return gemm::run(a, device_sms(), st);
+}
+
+bool aligned(std::initializer_list<const void*> ps, unsigned bytes) {
+  uintptr_t any = 0;
+  for (const void* q : ps) any |= reinterpret_cast<uintptr_t>(q);
+  return any % bytes == 0;
+}
+
+cudaError_t forward(const ipttt_xent_params& p, const Work& w, const void* H, const void* W, const int64_t* targets,
+                    float* loss, float* lse, uint8_t* ws, int* launches, cudaStream_t st) {
+  float* l = reinterpret_cast<float*>(ws + w.logits);
+  for (int v0 = 0; v0 < p.V; v0 += w.piece) {
+    const int cols = std::min(w.piece, p.V - v0);
+    const cudaError_t e = logits_of(p, H, W, v0, cols, l, w.piece, st);
+    if (e != cudaSuccess) return e;
+    k_row_stats<<<p.N, kThreads, 0, st>>>(l, w.piece, v0, cols, p.V, v0 + cols == p.V, targets, p.ignore_index,
+                                          reinterpret_cast<float2*>(ws + w.run), reinterpret_cast<float*>(ws + w.tl),
+                                          loss, lse, device_status());
+    *launches += 2;
+  }
+  return cudaGetLastError();
+}
+
+cudaError_t backward(const ipttt_xent_params& p, const Work& w, const void* H, const void* W, const int64_t* targets,
+                     const float* lse, const float* gloss, void* gH, void* gW, uint8_t* ws, int* launches,
+                     cudaStream_t st) {
+  float* l = reinterpret_cast<float*>(ws + w.logits);
+  float* acc = reinterpret_cast<float*>(ws + w.gH);
+  const long long nd = (long long)p.N * p.d;
+  int slices = 0, all_slices = 0;
+  for (int v0 = 0; v0 < p.V; v0 += w.piece) {
+    const int cols = std::min(w.piece, p.V - v0);
+    slices = std::max(1, std::min(w.slices, cols / 256));
+    if (v0 == 0) all_slices = slices;  // a shorter last piece adds to the first ones
+    cudaError_t e = logits_of(p, H, W, v0, cols, l, w.piece, st);
+    if (e != cudaSuccess) return e;
+    if (p.dtype == IPTTT_F32) {
+      k_row_grad<<<p.N, kThreads, 0, st>>>(l, l, w.piece, v0, cols, w.piece, p.V, targets, p.ignore_index, lse, gloss,
+                                           device_status());
+      Sgemm a{l, static_cast<const float*>(W) + (long long)v0 * p.d, acc, w.piece, p.d, p.d, nd,
+              p.N, p.d, cols, slices, 0, p.d, v0 > 0};
+      // p's columns past the vocabulary are zero, and W's rows past it are not read
+      e = sgemm<true, false>(a, st);
+      if (e != cudaSuccess) return e;
+      Sgemm b{l, static_cast<const float*>(H), static_cast<float*>(gW) + (long long)v0 * p.d, w.piece, p.d, p.d, 0,
+              cols, p.d, p.N, 1, w.piece, p.d};
+      e = sgemm<false, false>(b, st);
+      if (e != cudaSuccess) return e;
+    } else {
+      __nv_bfloat16* pb = reinterpret_cast<__nv_bfloat16*>(ws + w.p);
+      k_row_grad<<<p.N, kThreads, 0, st>>>(l, pb, w.piece, v0, cols, w.piece, p.V, targets, p.ignore_index, lse, gloss,
+                                           device_status());
+      gemm::Args a{};
+      a.A = {pb, (uint64_t)w.piece, (uint64_t)p.N, 1};
+      a.Bop = {static_cast<const __nv_bfloat16*>(W) + (long long)v0 * p.d, (uint64_t)p.d, (uint64_t)cols, 1};
+      a.b_mn = 1;
+      a.mode = gemm::GM_PLAIN;
+      a.M = p.N;
+      a.N = p.d;
+      a.K = cols;
+      a.out_kind = v0 > 0 ? gemm::GO_F32_ADD : gemm::GO_F32;
+      a.out = acc;
+      a.ldo = p.d;
+      a.osz = nd;
+      a.ksplit = slices;
+      a.status = device_status();
+      e = gemm::run(a, device_sms(), st);
+      if (e != cudaSuccess) return e;
+      gemm::Args b{};
+      b.A = {pb, (uint64_t)w.piece, (uint64_t)p.N, 1};
+      b.a_mn = 1;
+      b.Bop = {H, (uint64_t)p.d, (uint64_t)p.N, 1};
+      b.b_mn = 1;
+      b.mode = gemm::GM_PLAIN;
+      b.M = cols;
+      b.N = p.d;
+      b.K = p.N;
+      b.out_kind = gemm::GO_BF16;
+      b.out = static_cast<__nv_bfloat16*>(gW) + (long long)v0 * p.d;
+      b.ldo = p.d;
+      b.status = device_status();
+      e = gemm::run(b, device_sms(), st);
+      if (e != cudaSuccess) return e;
+    }
+    *launches += 4;
+  }
+  const unsigned grid = (unsigned)std::min<long long>((nd + kThreads - 1) / kThreads, 148 * 16);
+  if (p.dtype == IPTTT_F32) k_sum_slices<<<grid, kThreads, 0, st>>>(acc, static_cast<float*>(gH), nd, all_slices);
+  else k_sum_slices<<<grid, kThreads, 0, st>>>(acc, static_cast<__nv_bfloat16*>(gH), nd, all_slices);
+  ++*launches;
+  return cudaGetLastError();
+}
+
+}  // namespace
+}  // namespace ipttt
+
+using namespace ipttt;
+
+extern "C" {
+
+size_t ipttt_xent_workspace_size(const ipttt_xent_params* p) {
+  return check(p) == IPTTT_OK ? work_of(*p, false).total : 0;
+}
+
+size_t ipttt_xent_backward_workspace_size(const ipttt_xent_params* p) {
+  return check(p) == IPTTT_OK ? work_of(*p, true).total : 0;
+}
+
+ipttt_status ipttt_xent_forward(const ipttt_xent_params* p, const void* H, const void* W, const int64_t* targets,
+                                float* loss, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  const ipttt_status rc = check(p);
+  if (rc != IPTTT_OK) return rc;
+  if (!H || !W || !targets || !loss || !lse) return IPTTT_ERR_ARG;
+  if (!aligned({H, W}, 16) || !aligned({targets}, 8) || !aligned({loss, lse}, 4)) return IPTTT_ERR_ALIGN;
+  const Work w = work_of(*p, false);
+  if (!workspace || workspace_bytes < w.total) return IPTTT_ERR_WORKSPACE;
+  if (reinterpret_cast<uintptr_t>(workspace) % 256) return IPTTT_ERR_ALIGN;
+  int launches = 0;
+  const cudaError_t e = forward(*p, w, H, W, targets, loss, lse, static_cast<uint8_t*>(workspace), &launches,
+                                static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail("xent_forward", e);
+  count_launches(launches);
+  return IPTTT_OK;
+}
+
+ipttt_status ipttt_xent_backward(const ipttt_xent_params* p, const void* H, const void* W, const int64_t* targets,
+                                 const float* lse, const float* gloss, void* gH, void* gW, void* workspace,
+                                 size_t workspace_bytes, void* stream) {
+  const ipttt_status rc = check(p);
+  if (rc != IPTTT_OK) return rc;
+  if (!H || !W || !targets || !lse || !gloss || !gH || !gW) return IPTTT_ERR_ARG;
+  if (!aligned({H, W, gH, gW}, 16) || !aligned({targets}, 8) || !aligned({lse, gloss}, 4)) return IPTTT_ERR_ALIGN;
+  const Work w = work_of(*p, true);
+  if (!workspace || workspace_bytes < w.total) return IPTTT_ERR_WORKSPACE;
+  if (reinterpret_cast<uintptr_t>(workspace) % 256) return IPTTT_ERR_ALIGN;
+  int launches = 0;
+  const cudaError_t e = backward(*p, w, H, W, targets, lse, gloss, gH, gW, static_cast<uint8_t*>(workspace), &launches,
+                                 static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail("xent_backward", e);
+  count_launches(launches);
+  return IPTTT_OK;
+}
+
+}  // extern "C"

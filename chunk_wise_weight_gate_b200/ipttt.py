@@ -28,7 +28,11 @@ EXPORTS = ("ipttt_workspace_size", "ipttt_forward", "ipttt_forward_ex", "ipttt_c
            "ipttt_forward_host_size", "ipttt_forward_host", "ipttt_decode_state_size", "ipttt_decode_host_size",
            "ipttt_decode_reset", "ipttt_decode_step", "ipttt_decode_export", "ipttt_cp_workspace_size",
            "ipttt_cp_plan", "ipttt_cp_begin", "ipttt_cp_finish", "ipttt_last_error_detail",
-           "ipttt_backward_workspace_size", "ipttt_backward")
+           "ipttt_backward_workspace_size", "ipttt_backward", "ipttt_qk_norm_rope",
+           "ipttt_qk_norm_rope_backward_workspace_size", "ipttt_qk_norm_rope_backward",
+           "ipttt_linattn_workspace_size", "ipttt_linattn_forward", "ipttt_linattn_backward_workspace_size",
+           "ipttt_linattn_backward", "ipttt_linattn_step", "ipttt_xent_workspace_size", "ipttt_xent_forward",
+           "ipttt_xent_backward_workspace_size", "ipttt_xent_backward")
 PHASES = ("prep", "gate_up", "target", "gram", "apply", "update")
 DEBUG_OUTPUTS = ("D", "S_final", "alpha", "Z", "V")
 
@@ -37,6 +41,22 @@ class Params(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int32), ("T", ctypes.c_int32), ("d", ctypes.c_int32), ("F", ctypes.c_int32),
                 ("C", ctypes.c_int32), ("dtype", ctypes.c_int32), ("eta", ctypes.c_float),
                 ("clip_thresh", ctypes.c_float), ("flags", ctypes.c_int32)]
+
+
+class QKParams(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("B", "T", "Hq", "Hk", "D", "R", "dtype", "interleaved")]
+                + [("eps", ctypes.c_float)]
+                + [(n, ctypes.c_int64) for n in ("ldq", "ldk", "ldqo", "ldko", "ldgq", "ldgk")])
+
+
+class LinattnParams(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("B", "T", "H", "Hkv", "Dk", "Dv", "dtype")]
+                + [("scale", ctypes.c_float)]
+                + [(n, ctypes.c_int64) for n in ("ldq", "ldk", "ldv", "ldo", "ldgq", "ldgk", "ldgv")])
+
+
+class XentParams(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("N", "V", "d", "dtype", "piece")] + [("ignore_index", ctypes.c_int64)])
 
 
 FLAG_RESIDUAL = 1
@@ -122,6 +142,22 @@ def lib() -> ctypes.CDLL:
         L.ipttt_cp_begin.restype = ctypes.c_int
         L.ipttt_cp_finish.argtypes = [P, i32, i32, vp, i32, vp, vp, vp, vp, vp, vp, sz, vp]
         L.ipttt_cp_finish.restype = ctypes.c_int
+        QP, LP, XP = ctypes.POINTER(QKParams), ctypes.POINTER(LinattnParams), ctypes.POINTER(XentParams)
+        L.ipttt_qk_norm_rope.argtypes = [QP] + [vp] * 9
+        L.ipttt_qk_norm_rope_backward_workspace_size.argtypes = [QP]
+        L.ipttt_qk_norm_rope_backward.argtypes = [QP] + [vp] * 13 + [sz, vp]
+        L.ipttt_linattn_workspace_size.argtypes = [LP]
+        L.ipttt_linattn_forward.argtypes = [LP] + [vp] * 5 + [i32] + [vp] * 4 + [sz, vp]
+        L.ipttt_linattn_backward_workspace_size.argtypes = [LP]
+        L.ipttt_linattn_backward.argtypes = [LP] + [vp] * 5 + [i32] + [vp] * 8 + [sz, vp]
+        L.ipttt_linattn_step.argtypes = [LP] + [vp] * 8
+        L.ipttt_xent_workspace_size.argtypes = [XP]
+        L.ipttt_xent_forward.argtypes = [XP] + [vp] * 6 + [sz, vp]
+        L.ipttt_xent_backward_workspace_size.argtypes = [XP]
+        L.ipttt_xent_backward.argtypes = [XP] + [vp] * 8 + [sz, vp]
+        for name in ("qk_norm_rope", "linattn", "xent"):
+            for fn in (f for f in EXPORTS if f.startswith("ipttt_" + name)):
+                getattr(L, fn).restype = sz if fn.endswith("workspace_size") else ctypes.c_int
         _lib = L
     return _lib
 

@@ -372,6 +372,134 @@ IPTTT_API ipttt_status ipttt_backward(const ipttt_params* p, const void* H, cons
                                       float* gWgate, float* gWup, float* gWdown0, float* gconv_w,
                                       float* gWtarget, void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Operators around the layer: what a block puts before the MLP (norms of queries
+ * and keys with the position rotation, linear attention with a decay for each
+ * head) and the loss that the model trains with.  The conventions at the top of
+ * this file hold: device pointers owned by the caller and 16-byte aligned (the
+ * state arrays and workspaces 256-byte), nothing allocated, asynchronous on
+ * `stream` of the current device, argument errors returned before any launch,
+ * results deterministic run to run.  A workspace holds nothing between calls.
+ * Token tensors [B, T, heads, width] are read through a token stride: the elements
+ * between a token and the next (b, t) -> (b*T + t) * ld, heads packed within a
+ * token; 0 means packed tokens (heads * width).  Strides are multiples of 8
+ * elements.  So q, k and v may be views of one projection's output.
+ * ------------------------------------------------------------------------- */
+
+/* Norms of queries and keys for each head, and the position rotation, in one
+ * pass.  For every vector x [D] of every head of q (and of k, with its own weight),
+ *   z = x * w / sqrt(mean(x^2) + eps)
+ * and for each of the R/2 pairs (a, b) of z's first R elements, with the angle
+ * th = position * inv_freq[i] of pair i,
+ *   (y_a, y_b) = (z_a cos th - z_b sin th, z_b cos th + z_a sin th);
+ * elements from R on are z.  Pair i is (i, i + R/2), or (2i, 2i+1) when
+ * `interleaved`.  Angles are reduced to a turn in 64 bits, so far positions keep
+ * fp32 accuracy.  The output may be the input itself (same pointer and stride).
+ * D and R are multiples of 8, 0 <= R <= D <= 256. */
+typedef struct {
+  int32_t B, T;          /* sequences, tokens of each (1 when decoding)       */
+  int32_t Hq, Hk;        /* heads of q and of k                               */
+  int32_t D, R;          /* head width; rotated elements (0: norms alone)     */
+  int32_t dtype;         /* ipttt_dtype of q, k, the weights and the outputs  */
+  int32_t interleaved;   /* pairs (2i, 2i+1) instead of (i, i + R/2)          */
+  float eps;             /* > 0                                               */
+  int64_t ldq, ldk;      /* token strides of q and k                          */
+  int64_t ldqo, ldko;    /* of the outputs (backward: of their gradients)     */
+  int64_t ldgq, ldgk;    /* backward: of gq and gk                            */
+} ipttt_qk_params;
+
+/* positions: int64 [B, T]; inv_freq: double [R/2] (radians a position); wq, wk: [D]. */
+IPTTT_API ipttt_status ipttt_qk_norm_rope(const ipttt_qk_params* p, const void* q, const void* k, const void* wq,
+                                          const void* wk, const double* inv_freq, const int64_t* positions,
+                                          void* q_out, void* k_out, void* stream);
+/* Gradients of <gqo, q_out> + <gko, k_out>: gq, gk in the call's dtype, gwq and gwk [D]
+ * in fp32.  gq may be gqo itself (same pointer and stride), gk gko. */
+IPTTT_API size_t ipttt_qk_norm_rope_backward_workspace_size(const ipttt_qk_params* p);
+IPTTT_API ipttt_status ipttt_qk_norm_rope_backward(const ipttt_qk_params* p, const void* q, const void* k,
+                                                   const void* wq, const void* wk, const double* inv_freq,
+                                                   const int64_t* positions, const void* gqo, const void* gko,
+                                                   void* gq, void* gk, float* gwq, float* gwk, void* workspace,
+                                                   size_t workspace_bytes, void* stream);
+
+/* Linear attention with a decay for each head.  For every row b and head h, with
+ * gamma_h = exp(log_decay[h]) and head h reading key/value head h / (H / Hkv),
+ *   S_t = (token t starts a document ? 0 : gamma_h S_{t-1}) + k_t v_t^T     [Dk, Dv]
+ *   o_t = scale * q_t S_t,
+ * S_{-1} = S0 (NULL: 0).  log_decay: fp32 [H], <= 0 (0: no decay, -inf: none of the
+ * past); a positive or NaN entry fails on the device (IPTTT_ERR_ARG) and leaves
+ * the outputs unspecified.  doc_starts as for the layer; a row start counts as a
+ * document start only when listed, which matters with S0 alone.  States are fp32
+ * [B, H, Dk, Dv]; S_final_opt may be S0 itself.
+ * Whole sequences are computed by chunks of tokens: the products of a chunk's
+ * queries and keys under the decay, and the state carried over chunks.  A value that
+ * is not finite reaches the other tokens of its chunk, its sequence's later tokens
+ * included, but no other row or head.  bf16 head widths of 64 and 128 run on the
+ * tensor cores with the state and every sum in fp32; other widths (multiples of 8
+ * up to 256) and fp32 run on the CUDA cores. */
+typedef struct {
+  int32_t B, T;             /* sequences, tokens of each                       */
+  int32_t H, Hkv;           /* heads of q and o; heads of k and v (divides H)  */
+  int32_t Dk, Dv;           /* widths of q and k; of v and o                   */
+  int32_t dtype;            /* ipttt_dtype of q, k, v, o and their gradients   */
+  float scale;              /* finite, not 0                                   */
+  int64_t ldq, ldk, ldv;    /* token strides of q, k, v                        */
+  int64_t ldo;              /* of o (backward: of gO)                          */
+  int64_t ldgq, ldgk, ldgv; /* backward: of gq, gk, gv                         */
+} ipttt_linattn_params;
+
+IPTTT_API size_t ipttt_linattn_workspace_size(const ipttt_linattn_params* p);
+IPTTT_API ipttt_status ipttt_linattn_forward(const ipttt_linattn_params* p, const void* q, const void* k,
+                                             const void* v, const float* log_decay, const int32_t* doc_starts,
+                                             int32_t n_doc_starts, const float* S0_opt, void* O,
+                                             float* S_final_opt, void* workspace, size_t workspace_bytes,
+                                             void* stream);
+/* Gradients of <gO, O> + <gS_final, S_final> (gS_final_opt NULL: 0) with respect to q, k,
+ * v (the call's dtype; a shared key/value head's gradient is the fp32 sum over its
+ * heads) and S0 (fp32, NULL to skip).  The decay takes no gradient: it is a
+ * constant of the model. */
+IPTTT_API size_t ipttt_linattn_backward_workspace_size(const ipttt_linattn_params* p);
+IPTTT_API ipttt_status ipttt_linattn_backward(const ipttt_linattn_params* p, const void* q, const void* k,
+                                              const void* v, const float* log_decay, const int32_t* doc_starts,
+                                              int32_t n_doc_starts, const float* S0_opt, const void* gO,
+                                              const float* gS_final_opt, void* gq, void* gk, void* gv,
+                                              float* gS0_opt, void* workspace, size_t workspace_bytes,
+                                              void* stream);
+/* One token of every row (T = 1): the recurrence itself on the fp32 state S [B, H, Dk,
+ * Dv], updated in place.  starts_opt: DEVICE int32 [B], nonzero where the row's
+ * token starts a document (NULL: nowhere).  Captures into a CUDA graph. */
+IPTTT_API ipttt_status ipttt_linattn_step(const ipttt_linattn_params* p, float* S, const void* q, const void* k,
+                                          const void* v, const float* log_decay, const int32_t* starts_opt, void* o,
+                                          void* stream);
+
+/* Softmax cross entropy of a linear head, H [N, d], W [V, d], both in the call's dtype:
+ *   l_n = H_n W^T (fp32),  lse_n = log sum_v exp l_nv,  loss_n = lse_n - l_n[targets_n],
+ * loss and lse fp32 [N].  The logits are formed in pieces of the vocabulary and never
+ * kept.  A target equal to ignore_index leaves its row out: loss 0, no gradient; its
+ * lse is computed all the same.  Any other target outside [0, V) fails on the device
+ * (IPTTT_ERR_ARG) and its row is left out.
+ * The backward takes the forward's lse and gloss = dL/dloss (fp32 [N]) and forms each
+ * piece's logits again: p = (exp(l - lse) - onehot) gloss, gH = p W, gW = p^T H, both in
+ * the call's dtype, summed in fp32; bf16 calls round p to bf16 for the two products.
+ * bf16: d a multiple of 32 (tensor cores); fp32: any d that is a multiple of 4 (CUDA
+ * cores).  Targets, loss, lse and gloss need their element's alignment only.
+ * `piece` is the number of vocabulary rows the backward handles at a time
+ * (its workspace holds their p); 0 picks it. */
+typedef struct {
+  int32_t N, V, d;       /* tokens, vocabulary, width    */
+  int32_t dtype;         /* ipttt_dtype                  */
+  int32_t piece;         /* 0, or a multiple of 256      */
+  int64_t ignore_index;  /* commonly -100                */
+} ipttt_xent_params;
+
+IPTTT_API size_t ipttt_xent_workspace_size(const ipttt_xent_params* p);
+IPTTT_API ipttt_status ipttt_xent_forward(const ipttt_xent_params* p, const void* H, const void* W,
+                                          const int64_t* targets, float* loss, float* lse, void* workspace,
+                                          size_t workspace_bytes, void* stream);
+IPTTT_API size_t ipttt_xent_backward_workspace_size(const ipttt_xent_params* p);
+IPTTT_API ipttt_status ipttt_xent_backward(const ipttt_xent_params* p, const void* H, const void* W,
+                                           const int64_t* targets, const float* lse, const float* gloss, void* gH,
+                                           void* gW, void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
