@@ -401,6 +401,8 @@ bool aligned16(std::initializer_list<const void*> ps) {
   return any % 16 == 0;
 }
 
+bool on_tensor_cores(const ipttt_linattn_params& p) { return p.dtype == IPTTT_BF16 && tc_takes(p.Dk, p.Dv); }
+
 struct Work {
   size_t starts, seg, S0, parts, total;
   long long words;
@@ -416,10 +418,15 @@ Work work_of(const ipttt_linattn_params& p, bool backward) {
     off += al256(bytes);
     return o;
   };
-  w.words = (p.T + 31) / 32;
+  w.words = (p.T + kTcChunk - 1) / kTcChunk * (kTcChunk / 32);
   w.starts = take((size_t)p.B * w.words * 4);
-  w.segs_o = simt_segments(p.B, p.T, p.H, p.Dk, p.Dv, &w.chunks_o);
-  w.segs_q = simt_segments(p.B, p.T, p.H, p.Dv, p.Dk, &w.chunks_q);
+  if (on_tensor_cores(p)) {
+    w.segs_o = w.segs_q = tc_segments(p.B, p.T, p.H, &w.chunks_o);
+    w.chunks_q = w.chunks_o;
+  } else {
+    w.segs_o = simt_segments(p.B, p.T, p.H, p.Dk, p.Dv, &w.chunks_o);
+    w.segs_q = simt_segments(p.B, p.T, p.H, p.Dv, p.Dk, &w.chunks_q);
+  }
   const int segs = backward ? std::max(w.segs_o, w.segs_q) : w.segs_o;
   w.seg = take(segs > 1 ? (size_t)p.B * p.H * segs * p.Dk * p.Dv * 4 : 0);
   w.S0 = take(!backward && segs > 1 ? (size_t)p.B * p.H * p.Dk * p.Dv * 4 : 0);
@@ -428,19 +435,23 @@ Work work_of(const ipttt_linattn_params& p, bool backward) {
   return w;
 }
 
+cudaError_t run_one(const ipttt_linattn_params& p, const Pass& q, cudaStream_t st) {
+  return on_tensor_cores(p) ? run_tc(q, st) : run_simt(q, p.dtype, st);
+}
+
 // A pass, after its segments' own states where the row is cut into segments.
 cudaError_t run_pass(const ipttt_linattn_params& p, Pass q, float* seg, int* launches, cudaStream_t st) {
   if (q.segs > 1) {
     Pass s = q;
     s.out = nullptr;
     s.seg_state = seg;
-    const cudaError_t e = run_simt(s, p.dtype, st);
+    const cudaError_t e = run_one(p, s, st);
     if (e != cudaSuccess) return e;
     ++*launches;
     q.seg_in = seg;
   }
   ++*launches;
-  return run_simt(q, p.dtype, st);
+  return run_one(p, q, st);
 }
 
 // The start bits of the call, or null where no start is listed.

@@ -100,5 +100,11 @@ constexpr int kSimtChunk = 32;
 cudaError_t run_simt(const Pass& p, int dtype, cudaStream_t st);
 int simt_segments(int B, int T, int H, int Da, int Dc, int* seg_chunks);
 
+// The tensor-core pass (bf16 operands, widths of 64 and 128), chunks of 128 tokens.
+constexpr int kTcChunk = 128;
+bool tc_takes(int Da, int Dc);
+cudaError_t run_tc(const Pass& p, cudaStream_t st);
+int tc_segments(int B, int T, int H, int* seg_chunks);
+
 }  // namespace la
 }  // namespace ipttt

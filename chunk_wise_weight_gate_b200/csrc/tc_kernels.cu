@@ -1366,10 +1366,15 @@ static PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 // 128-byte swizzle, zero fill outside the tensor.
 bool make_map_bf16(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows, uint64_t outer,
                    uint32_t box_inner, uint32_t box_rows) {
+  return make_map_bf16_ld(m, base, inner, rows, outer, inner, box_inner, box_rows);
+}
+
+bool make_map_bf16_ld(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows, uint64_t outer, uint64_t ld,
+                      uint32_t box_inner, uint32_t box_rows) {
   auto enc = encode_fn();
   if (!enc) return false;
   cuuint64_t dims[3] = {inner, rows, outer};
-  cuuint64_t strides[2] = {inner * 2, inner * rows * 2};
+  cuuint64_t strides[2] = {ld * 2, ld * rows * 2};
   cuuint32_t box[3] = {box_inner, box_rows, 1};
   cuuint32_t estr[3] = {1, 1, 1};
   CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,

@@ -59,6 +59,9 @@ struct TcParams {
 
 bool make_map_bf16(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows, uint64_t outer,
                    uint32_t box_inner, uint32_t box_rows);
+// As make_map_bf16 for rows `ld` elements apart (a multiple of 8).
+bool make_map_bf16_ld(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows, uint64_t outer, uint64_t ld,
+                      uint32_t box_inner, uint32_t box_rows);
 cudaError_t launch_tc(int fam, const TcParams& p, int num_sms, cudaStream_t st);
 // Whether FAM_ZV2 can run on this device (a cluster of two fits), and the
 // number of CTA pairs resident at once.
