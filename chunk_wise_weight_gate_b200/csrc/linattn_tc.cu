@@ -34,29 +34,38 @@ using namespace ipttt::tc;
 namespace {
 
 constexpr int CH = kTcChunk;
-constexpr int kStateWarp = 6;  // warps 2-5: scores and output; from here: the state
-constexpr int kTcThreads = 14 * 32;
-constexpr int kTab = 256;  // tab[127 + n] = gamma^n for 0 <= n <= 128, 0 below
+constexpr int kOutWarp = 4;  // first of the 8 warps that turn scores into P and write the output
+// Per head: pw[128 + n] = gamma^n for 0 <= n <= 128 and 0 for n < 0, then gamma^{31 - n}, n < 32.
+constexpr int kPw = 260, kTab = kPw + 32;
+
+enum Kind { FORWARD = 0, REVERSE = 1, STATES = 2 };  // STATES: a segment's own state alone, either way
 
 template <int DA, int DC, bool STATE>
 struct Cfg {
-  static constexpr int SLOT = 256 * (DA > DC ? DA : DC);
-  static constexpr int LO = 256 * DA;                // lo half of the scaled B
+  static constexpr int ASLOT = 256 * (DA > DC ? DA : DC);  // an a tile, then the output tile in its place
+  static constexpr int SLOT = 256 * (DA > DC ? DA : DC);   // a b or a c tile
+  static constexpr int NA = STATE ? 0 : 2;
+  static constexpr int LO = 256 * DA;                 // lo half of the scaled B
   static constexpr int FB = STATE ? 0 : DA * DC * 2;  // bf16 state
-  static constexpr int MISC = 2 * kTab * 4 + 512;
-  static constexpr int FIT = (232448 - LO - FB - MISC) / SLOT;
-  static constexpr int NS = FIT < 8 ? FIT : 8;
-  static constexpr int SMEM = NS * SLOT + LO + FB + MISC;
-  static constexpr int NC = DA * DC / 256;           // state columns a thread holds
-  static constexpr int TPC = STATE ? 2 : 3;          // tiles a chunk
+  static constexpr int MISC = 2 * kTab * 4 + 256;
+  static constexpr int FIT = (232448 - NA * ASLOT - LO - FB - MISC) / SLOT;
+  static constexpr int NS = FIT < 6 ? FIT : 6;
+  static constexpr int SMEM = NA * ASLOT + NS * SLOT + LO + FB + MISC;
+  static constexpr int NC = DA * DC / 256;   // state columns a thread holds
+  static constexpr int SW = STATE ? 4 : 12;  // first of the 8 state warps
+  static constexpr int THREADS = 32 * (SW + 8);
 };
+// Registers a thread of the full pass's three groups (640 threads, 96 each at launch): the
+// state's owners need more than an even share, the others less.
+constexpr int kRegsIssue = 64, kRegsOut = 88, kRegsState = 120, kRegsLaunch = 96;
+static_assert(128 * kRegsIssue + 256 * kRegsOut + 256 * kRegsState <= 640 * kRegsLaunch, "register split");
 // TMEM columns
 constexpr int kSC = 0, kO1 = 128;
 __host__ __device__ constexpr int col_o2(int dc) { return 128 + dc; }
 __host__ __device__ constexpr int col_d(int dc) { return 128 + 2 * dc; }
 
 struct TcArgs {
-  CUtensorMap ma, mb, mc;
+  CUtensorMap ma, mb, mc, mo;
   Pass p;
   int items;
 };
@@ -129,29 +138,55 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t two(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint32_t pack2(uint64_t v) {
+  float lo, hi;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+  return pack2(lo, hi);
+}
+__device__ __forceinline__ uint64_t two(const uint32_t* r) { return two(__uint_as_float(r[0]), __uint_as_float(r[1])); }
+
 template <int N>
 __device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&r)[N]) {
   if constexpr (N == 16) tmem_ld16(addr, r);
   else tmem_ld32(addr, r);
 }
 
-template <int DA, int DC, bool STATE>
-__global__ void __launch_bounds__(kTcThreads, 1) k_pass_tc(const __grid_constant__ TcArgs ta) {
+template <int DA, int DC, int KIND>
+__global__ void __launch_bounds__(Cfg<DA, DC, KIND == STATES>::THREADS, 1) k_pass_tc(const __grid_constant__ TcArgs ta) {
+  constexpr bool STATE = KIND == STATES;
   using Cf = Cfg<DA, DC, STATE>;
-  constexpr int NS = Cf::NS, SLOT = Cf::SLOT, TPC = Cf::TPC, NC = Cf::NC;
+  constexpr int NS = Cf::NS, SLOT = Cf::SLOT, ASLOT = Cf::ASLOT, NC = Cf::NC;
   const Pass& p = ta.p;
   extern __shared__ __align__(1024) uint8_t smem[];
-  uint8_t* lo_buf = smem + NS * SLOT;
+  uint8_t* a_buf = smem;                  // [2][ASLOT], chunks in turn
+  uint8_t* ring = smem + Cf::NA * ASLOT;  // [NS][SLOT]: b, c, b, c, ...
+  uint8_t* lo_buf = ring + NS * SLOT;
   uint8_t* f_buf = lo_buf + Cf::LO;
   float* tabs = reinterpret_cast<float*>(f_buf + Cf::FB);
   uint64_t* bars = reinterpret_cast<uint64_t*>(tabs + 2 * kTab);
   uint64_t *full = bars, *empty = bars + NS;
   uint64_t *sc_full = bars + 2 * NS, *p_ready = sc_full + 1, *conv_done = sc_full + 2, *d_full = sc_full + 3;
   uint64_t *f_ready = sc_full + 4, *o_full = sc_full + 5, *o_free = sc_full + 6, *tab_ready = sc_full + 7;
-  uint64_t* drain = sc_full + 8;
+  uint64_t *a_full = sc_full + 8, *a_empty = sc_full + 10, *drain = sc_full + 12;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  uint32_t* issued = tmem_slot + 2;  // tiles whose loads were issued
+  uint32_t* issued = tmem_slot + 2;  // ring tiles and a tiles whose loads were issued
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (smem_u32(smem) % 1024 != 0) {  // the swizzled tiles need it; uniform over the block
@@ -164,20 +199,27 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_pass_tc(const __grid_constant
       mbar_init(&empty[s], 1);
     }
     mbar_init(sc_full, 1);
-    mbar_init(p_ready, 4);
+    mbar_init(p_ready, 8);
     mbar_init(conv_done, 8);
     mbar_init(d_full, 1);
     mbar_init(f_ready, 8);
     mbar_init(o_full, 1);
-    mbar_init(o_free, 4);
-    mbar_init(tab_ready, STATE ? 8 : 12);
+    mbar_init(o_free, 8);
+    mbar_init(tab_ready, STATE ? 8 : 16);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&a_full[s], 1);
+      mbar_init(&a_empty[s], 8);
+    }
     mbar_init(drain, 1);
     *abort_flag = 0;
-    *issued = 0;
+    issued[0] = issued[1] = 0;
     fence_mbar_init();
   }
   if (warp == 0 && lane == 0) {
-    if (!STATE) prefetch_tmap(&ta.ma);
+    if (!STATE) {
+      prefetch_tmap(&ta.ma);
+      prefetch_tmap(&ta.mo);
+    }
     prefetch_tmap(&ta.mb);
     prefetch_tmap(&ta.mc);
   }
@@ -189,6 +231,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_pass_tc(const __grid_constant
   __syncthreads();
   tc_fence_after();
   const uint32_t tm = *tmem_slot;
+  const bool rev = STATE ? p.rev != 0 : KIND == REVERSE;
+  const int step = rev ? -1 : 1;
   bool ok = true;
   // a wait that gives up ends the block's work: every role leaves its loops
 #define LA_WAIT(bar, parity)                                  \
@@ -196,123 +240,126 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_pass_tc(const __grid_constant
     ok = false;                                               \
     break;                                                    \
   }
-
   // of all lanes of a warp alike: what follows are warp-wide TMEM accesses
-#define LA_WAIT_WARP(bar, parity)                                                            \
+#define LA_WAIT_WARP(bar, parity)                                                      \
   if (!__all_sync(0xffffffffu, mbar_wait_or_abort(bar, (parity) & 1u, abort_flag))) { \
-    ok = false;                                                                              \
-    break;                                                                                   \
+    ok = false;                                                                        \
+    break;                                                                             \
   }
 
-  if (warp == 0) {
-    if (lane == 0) {
-      uint32_t tl = 0;
+  if (warp < kOutWarp) {
+    if constexpr (!STATE) regs_dec<kRegsIssue>();
+    if (warp == 0 && lane == 0) {
+      uint32_t tl = 0, cc = 0;
+      auto load = [&](uint8_t* dst, const CUtensorMap* m, uint64_t* bar, int width, int x, int ch, int b) {
+        mbar_arrive_expect_tx(bar, 256 * width);
+        for (int q = 0; q < width / 64; ++q) tma_load_3d(dst + q * 16384, m, bar, x + 64 * q, ch * CH, b);
+      };
       for (int i = blockIdx.x; ok && i < ta.items; i += gridDim.x) {
         const Item it = item_of(p, i);
-        for (int n = 0; ok && n < it.last - it.first; ++n) {
-          const int ch = p.rev ? it.last - 1 - n : it.first + n;
-          for (int k = 0; k < TPC; ++k, ++tl) {
-            const int s = tl % NS;
-            LA_WAIT(&empty[s], (tl / NS) ^ 1u);
-            const bool is_a = !STATE && k == 1, is_c = k == TPC - 1;
-            const CUtensorMap* m = is_a ? &ta.ma : is_c ? &ta.mc : &ta.mb;
-            const int width = is_c ? DC : DA;
-            const int x = it.h / (is_a ? p.ga : is_c ? p.gc : p.gb) * width;
-            mbar_arrive_expect_tx(&full[s], 256 * width);
-            for (int q = 0; q < width / 64; ++q)
-              tma_load_3d(smem + s * SLOT + q * 16384, m, &full[s], x + 64 * q, ch * CH, it.b);
+        for (int n = 0; n < it.last - it.first; ++n, ++cc) {
+          const int ch = rev ? it.last - 1 - n : it.first + n;
+          LA_WAIT(&empty[tl % NS], (tl / NS) ^ 1u);
+          load(ring + tl % NS * SLOT, &ta.mb, &full[tl % NS], DA, it.h / p.gb * DA, ch, it.b);
+          ++tl;
+          if constexpr (!STATE) {
+            LA_WAIT(&a_empty[cc & 1], (cc >> 1) ^ 1u);
+            load(a_buf + (cc & 1) * ASLOT, &ta.ma, &a_full[cc & 1], DA, it.h / p.ga * DA, ch, it.b);
+            issued[1] = cc + 1;
           }
+          LA_WAIT(&empty[tl % NS], (tl / NS) ^ 1u);
+          load(ring + tl % NS * SLOT, &ta.mc, &full[tl % NS], DC, it.h / p.gc * DC, ch, it.b);
+          ++tl;
         }
       }
-      *issued = tl;
-      if (!ok) {
-        *abort_flag = 1;
-        set_status(p.status, IPTTT_ERR_TIMEOUT);
-      }
-    }
-  } else if (warp == 1) {
-    if (lane == 0) {
+      issued[0] = tl;
+    } else if (warp == 1 && lane == 0) {
       constexpr uint32_t id1 = idesc_bf16(128, 128, false, false), id2 = idesc_bf16(128, DC, false, true),
                          id3 = idesc_bf16(128, DC, false, true), id4 = idesc_bf16(128, DC, true, true);
       // width 64: rows 64-127 of (4) repeat rows 0-63 (the second block of 64 is the first)
       constexpr uint32_t lbo4 = DA == 128 ? 16384 : 0;
-      const uint32_t base = smem_u32(smem), lo_addr = smem_u32(lo_buf), f_addr = smem_u32(f_buf);
+      // Descriptors of each tile's first K step; a step adds to the address field (16-byte
+      // units).  Built once: made anew for each MMA they cost the issuing thread some 100
+      // clocks a MMA, where the tensor pipe takes 64.
+      auto k_major = [](const uint8_t* t) { return sdesc_sw128(smem_u32(t), 16, 1024); };
+      auto mn_major = [](const uint8_t* t, uint32_t lbo) { return sdesc_sw128(smem_u32(t), lbo, 1024); };
+      const uint64_t a_k = k_major(a_buf), b_k = k_major(ring), b_mn = mn_major(ring, lbo4), c_mn = mn_major(ring, 16384),
+                     lo_mn = mn_major(lo_buf, lbo4), f_mn = mn_major(f_buf, DA * 128);
       uint32_t tl = 0, cc = 0;
       for (int i = blockIdx.x; ok && i < ta.items; i += gridDim.x) {
         const Item it = item_of(p, i);
-        for (int n = it.first; ok && n < it.last; ++n, ++cc, tl += TPC) {
-          const uint32_t sb = tl % NS, sa = (tl + 1) % NS, sc = (tl + TPC - 1) % NS;
-          const uint32_t ab = base + sb * SLOT, aa = base + sa * SLOT, ac = base + sc * SLOT;
+        for (int n = it.first; n < it.last; ++n, ++cc, tl += 2) {
+          const uint32_t sb = tl % NS, sc = (tl + 1) % NS;
+          const uint64_t da = a_k + (cc & 1) * (ASLOT / 16), db = b_k + sb * (SLOT / 16), dbm = b_mn + sb * (SLOT / 16),
+                         dc = c_mn + sc * (SLOT / 16);
           if constexpr (!STATE) {
             LA_WAIT(&full[sb], tl / NS);
-            LA_WAIT(&full[sa], (tl + 1) / NS);
+            LA_WAIT(&a_full[cc & 1], cc >> 1);
             tc_fence_after();
 #pragma unroll
             for (int k = 0; k < DA / 16; ++k)
-              mma_bf16(tm + kSC, sdesc_sw128(aa + (k / 4) * 16384 + (k % 4) * 32, 16, 1024),
-                       sdesc_sw128(ab + (k / 4) * 16384 + (k % 4) * 32, 16, 1024), id1, k > 0);
+              mma_bf16(tm + kSC, da + (k / 4) * 1024 + (k % 4) * 2, db + (k / 4) * 1024 + (k % 4) * 2, id1, k > 0);
             mma_commit(sc_full);
             LA_WAIT(f_ready, cc);
             LA_WAIT(o_free, cc ^ 1u);
             tc_fence_after();
 #pragma unroll
             for (int k = 0; k < DA / 16; ++k)
-              mma_bf16(tm + kO1, sdesc_sw128(aa + (k / 4) * 16384 + (k % 4) * 32, 16, 1024),
-                       sdesc_sw128(f_addr + k * 2048, DA * 128, 1024), id2, k > 0);
-            mma_commit(&empty[sa]);
+              mma_bf16(tm + kO1, da + (k / 4) * 1024 + (k % 4) * 2, f_mn + k * 128, id2, k > 0);
           }
           LA_WAIT(conv_done, cc);
-          LA_WAIT(&full[sc], (tl + TPC - 1) / NS);
+          LA_WAIT(&full[sc], (tl + 1) / NS);
           tc_fence_after();
 #pragma unroll
-          for (int k = 0; k < CH / 16; ++k)
-            mma_bf16(tm + col_d(DC), sdesc_sw128(ab + k * 2048, lbo4, 1024), sdesc_sw128(ac + k * 2048, 16384, 1024), id4,
-                     k > 0);
+          for (int k = 0; k < CH / 16; ++k) mma_bf16(tm + col_d(DC), dbm + k * 128, dc + k * 128, id4, k > 0);
 #pragma unroll
-          for (int k = 0; k < CH / 16; ++k)
-            mma_bf16(tm + col_d(DC), sdesc_sw128(lo_addr + k * 2048, lbo4, 1024), sdesc_sw128(ac + k * 2048, 16384, 1024),
-                     id4, 1);
+          for (int k = 0; k < CH / 16; ++k) mma_bf16(tm + col_d(DC), lo_mn + k * 128, dc + k * 128, id4, 1);
           mma_commit(&empty[sb]);
           if constexpr (STATE) mma_commit(&empty[sc]);
           mma_commit(d_full);
           if constexpr (!STATE) {
             LA_WAIT(p_ready, cc);
             tc_fence_after();
+            // P lies in columns 0-31 and 64-95 of the scores' place
 #pragma unroll
             for (int k = 0; k < CH / 16; ++k)
-              mma_bf16_ta(tm + col_o2(DC), tm + kSC + 8 * k, sdesc_sw128(ac + k * 2048, 16384, 1024), id3, k > 0);
+              mma_bf16_ta(tm + col_o2(DC), tm + kSC + 8 * k + (k < 4 ? 0 : 32), dc + k * 128, id3, k > 0);
             mma_commit(&empty[sc]);
             mma_commit(o_full);
           }
         }
       }
-      if (!ok) {
-        *abort_flag = 1;
-        set_status(p.status, IPTTT_ERR_TIMEOUT);
-      }
       mma_commit(drain);
       mbar_wait(drain, 0);
     }
-  } else if (warp < kStateWarp) {
+  } else if (warp < Cf::SW) {
     if constexpr (!STATE) {
-      const int quarter = warp & 3, row = quarter * 32 + lane;
+      regs_dec<kRegsOut>();
+      // two warps a quarter of the rows: each has 64 columns of the scores and half of the output's
+      constexpr int HC = DC / 2;
+      const int quarter = warp & 3, half = (warp - kOutWarp) >> 2, row = quarter * 32 + lane;
       const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+      const uint32_t sc_addr = tm + kSC + lanes + 64 * half, o1_addr = tm + kO1 + lanes + HC * half,
+                     o2_addr = tm + col_o2(DC) + lanes + HC * half;
+      const uint64_t s0_2 = two(p.scale, p.scale);
       uint32_t cc = 0, ic = 0;
       for (int i = blockIdx.x; ok && i < ta.items; i += gridDim.x, ++ic) {
         const Item it = item_of(p, i);
-        const float* tab = tabs + (ic & 1) * kTab;
+        const float* pw = tabs + (ic & 1) * kTab + 128;
         if (lane == 0) mbar_arrive(tab_ready);
         LA_WAIT_WARP(tab_ready, ic);
+        Starts next = starts_of(p, it.b, rev ? it.last - 1 : it.first);
         for (int n = 0; n < it.last - it.first; ++n, ++cc) {
-          const int ch = p.rev ? it.last - 1 - n : it.first + n;
+          const int ch = rev ? it.last - 1 - n : it.first + n;
           const int t0 = ch * CH, len = min(CH, p.T - t0);
-          const Starts st = starts_of(p, it.b, ch);
+          const Starts st = next;  // read a chunk ahead
+          if (n + 1 < it.last - it.first) next = starts_of(p, it.b, ch + step);
           const bool any = st.any();
-          // the tokens the row looks at: [from, to)
-          int from = p.rev ? row : 0, to = p.rev ? CH : row + 1;
+          // the tokens the row looks at: [from, to); whether the state before the chunk reaches it
+          int from = rev ? row : 0, to = rev ? CH : row + 1;
           bool in = true;
           if (any) {
-            if (p.rev) {
+            if (rev) {
               to = st.from(row + 1).first();
               in = row >= st.last();
             } else {
@@ -321,84 +368,119 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_pass_tc(const __grid_constant
             }
           }
           LA_WAIT_WARP(sc_full, cc);
+          if (cc > 0 && lane == 0) {  // the last chunk's output has left the a tile's place
+            bulk_wait_read<0>();
+            mbar_arrive(&a_empty[(cc - 1) & 1]);
+          }
+          __syncwarp();
           tc_fence_after();
-          const float* wt = tab + 127 + (p.rev ? -row : row);
-          const int dir = p.rev ? 1 : -1;
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
+          // 32 columns at a time; P takes the place of scores already read.  (Loops stay rolled:
+          // unrolled, the roles' code overran the instruction caches, a third of all stalls.)
+#pragma unroll 1
+          for (int q = 0; q < 2; ++q) {
+            const int block = 2 * half + q;
             uint32_t w[16];
-            if (p.rev ? q < quarter : q > quarter) {  // wholly on the other side of every row of the warp
+            if (rev ? block < quarter : block > quarter) {  // on the other side of every row of the warp
 #pragma unroll
               for (int e = 0; e < 16; ++e) w[e] = 0u;
             } else {
-              uint32_t r[32];
-              tmem_ld32(tm + kSC + lanes + 32 * q, r);
-              tmem_ld_wait();
+              uint32_t v[32];
+              tmem_ld32(sc_addr + 32 * q, v);
+              if (block == quarter) {  // the diagonal: gamma^|row - j|, 0 on the far side
+                const float* wt = pw + (rev ? -lane : lane);
+                tmem_ld_wait();
 #pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                const int j = 32 * q + 2 * e;
-                float x = __uint_as_float(r[2 * e]) * wt[dir * j], y = __uint_as_float(r[2 * e + 1]) * wt[dir * (j + 1)];
-                x = j >= from && j < to ? x : 0.0f;
-                y = j + 1 >= from && j + 1 < to ? y : 0.0f;
-                w[e] = pack2(x, y);
+                for (int e = 0; e < 16; ++e)
+                  w[e] = pack2(mul2(two(v + 2 * e), rev ? two(wt[2 * e], wt[2 * e + 1]) : two(wt[-2 * e], wt[-2 * e - 1])));
+              } else {  // a factor of the column times one of the row, neither above 1
+                const float rf = rev ? pw[32 * block - row] : pw[row - 32 * block - 31];
+                const uint64_t rf2 = two(rf, rf);
+                const ulonglong2* col = reinterpret_cast<const ulonglong2*>(rev ? pw : pw - 128 + kPw);
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                  const ulonglong2 c2 = col[e];
+                  w[2 * e] = pack2(mul2(mul2(two(v + 4 * e), c2.x), rf2));
+                  w[2 * e + 1] = pack2(mul2(mul2(two(v + 4 * e + 2), c2.y), rf2));
+                }
+              }
+              if (any) {
+                // bit j of the mask: column j of the block is in the row's document and on its side
+                const int lo = min(max(from - 32 * block, 0), 32), hi = min(max(to - 32 * block, 0), 32);
+                const uint32_t below_hi = hi == 32 ? 0xffffffffu : (1u << hi) - 1u;
+                const uint32_t mask = lo == 32 ? 0u : below_hi & (0xffffffffu << lo);
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                  w[e] &= (mask >> (2 * e) & 1u ? 0x0000ffffu : 0u) | (mask >> (2 * e) & 2u ? 0xffff0000u : 0u);
               }
             }
-            tmem_st16(tm + kSC + lanes + 16 * q, w);
+            tmem_st16(sc_addr + 16 * q, w);
           }
           tmem_st_wait();
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(p_ready);
 
-          const int lag = p.rev && t0 + len == p.T ? 1 : 0;
+          const int lag = rev && t0 + len == p.T ? 1 : 0;
           const bool write = row < len;
-          const float win = in && write ? tab[127 + (p.rev ? len - row - lag : row + 1)] : 0.0f;
+          const float win = in && write ? pw[rev ? len - row - lag : row + 1] : 0.0f;
           const float s1 = win * p.scale;
-          const long long at = ((long long)it.b * p.T + t0 + row) * p.ldo + (long long)it.h * DC;
+          const uint64_t s1_2 = two(s1, s1);
+          // the output goes out through the a tile's place: (1) and (2) are done with it
+          uint8_t* stage = a_buf + (cc & 1) * ASLOT + half * (256 * HC);
           LA_WAIT_WARP(o_full, cc);
           tc_fence_after();
-#pragma unroll
-          for (int q = 0; q < DC / 32; ++q) {
-            uint32_t x[32], y[32];
-            tmem_ld32(tm + col_o2(DC) + lanes + 32 * q, x);
-            tmem_ld32(tm + kO1 + lanes + 32 * q, y);
+#pragma unroll 1
+          for (int q = 0; q < HC / 16; ++q) {
+            uint32_t x[16], y[16];
+            tmem_ld16(o2_addr + 16 * q, x);
+            tmem_ld16(o1_addr + 16 * q, y);
             tmem_ld_wait();
-            if (q == DC / 32 - 1) {  // the last read: the accumulators are free
-              tc_fence_before();
+            uint64_t o[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              // rows of another document take nothing of the state, whatever is in it
+              const uint64_t s = win != 0.0f ? two(y + 2 * e) : 0ull;
+              o[e] = fma2(s1_2, s, mul2(s0_2, two(x + 2 * e)));
+            }
+            if (p.out_f32) {
+              if (write) {
+                ulonglong2* g = reinterpret_cast<ulonglong2*>(
+                    static_cast<float*>(p.out) + ((long long)it.b * p.T + t0 + row) * p.ldo + (long long)it.h * DC +
+                    HC * half + 16 * q);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) g[e] = make_ulonglong2(o[2 * e], o[2 * e + 1]);
+              }
               __syncwarp();
-              if (lane == 0) mbar_arrive(o_free);
-            }
-            if (write) {
+            } else {  // rows of HC columns, swizzled as the store's map is
 #pragma unroll
-              for (int e = 0; e < 32; ++e) {
-                const float o = p.scale * __uint_as_float(x[e]);
-                x[e] = __float_as_uint(win != 0.0f ? fmaf(s1, __uint_as_float(y[e]), o) : o);
-              }
-              if (p.out_f32) {
-                uint4* o = reinterpret_cast<uint4*>(static_cast<float*>(p.out) + at + 32 * q);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) o[e] = make_uint4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
-              } else {
-                uint4* o = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + at + 32 * q);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  const float* f = reinterpret_cast<const float*>(x) + 8 * e;
-                  o[e] = make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
-                }
+              for (int e = 0; e < 2; ++e) {
+                const int unit = (2 * q + e) ^ (HC == 64 ? row & 7 : (row >> 1) & 3);
+                *reinterpret_cast<uint4*>(stage + row * (2 * HC) + unit * 16) =
+                    make_uint4(pack2(o[4 * e]), pack2(o[4 * e + 1]), pack2(o[4 * e + 2]), pack2(o[4 * e + 3]));
               }
             }
+          }
+          tc_fence_before();  // the accumulators are free
+          __syncwarp();
+          if (lane == 0) mbar_arrive(o_free);
+          if (!p.out_f32) {
+            fence_proxy_async_smem();
             __syncwarp();
+            const int t = t0 + 32 * quarter;  // rows past T are left out by the map
+            if (lane == 0 && t < p.T) {
+              tma_store_3d(&ta.mo, stage + quarter * (64 * HC), it.h * DC + HC * half, t, it.b);
+              bulk_commit();
+            }
           }
         }
       }
-      if (!ok) {
-        *abort_flag = 1;
-        set_status(p.status, IPTTT_ERR_TIMEOUT);
-      }
+      if (lane == 0) bulk_wait<0>();
     }
   } else {
-    const int tid = threadIdx.x - kStateWarp * 32;
-    const int quarter = warp & 3, half = (warp - kStateWarp) >> 2;
+    if constexpr (!STATE) regs_inc<kRegsState>();
+    const int tid = threadIdx.x - Cf::SW * 32;
+    const int quarter = warp & 3, half = (warp - Cf::SW) >> 2;
     const int row = DA == 128 ? quarter * 32 + lane : (quarter & 1) * 32 + lane;
     const int c0 = (DA == 128 ? half : half * 2 + (quarter >> 1)) * NC;  // its columns: [c0, c0 + NC)
     const uint32_t d_addr = tm + col_d(DC) + ((uint32_t)(quarter * 32) << 16) + c0;
@@ -409,30 +491,18 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_pass_tc(const __grid_constant
       const size_t bh = (size_t)it.b * p.H + it.h;
       const float g = p.log_decay[it.h];
       if (tid == 0 && !(g <= 0.0f)) set_status(p.status, IPTTT_ERR_ARG);
-      float* tab = tabs + (ic & 1) * kTab;
-      tab[tid] = tid < 127 ? 0.0f : decay_pow(g, tid - 127);
+      float* pw = tabs + (ic & 1) * kTab + 128;
+      pw[tid - 128] = tid < 128 ? 0.0f : decay_pow(g, tid - 128);
+      if (tid < 32) pw[kPw - 128 + tid] = decay_pow(g, 31 - tid);
+      if (tid == 32) pw[128] = decay_pow(g, 128);
       __syncwarp();
       if (lane == 0) mbar_arrive(tab_ready);
       const int lo = it.first * CH, hi = min(p.T, it.last * CH);
 
-      // the state the segment starts from, and its operand copy
-      auto store_f = [&]() {
-        uint8_t* fb = f_buf + (c0 / 64) * (DA * 128) + row * 128;
-#pragma unroll
-        for (int e = 0; e < NC / 8; ++e) {
-          const int unit = (c0 % 64) / 8 + e;
-          *reinterpret_cast<uint4*>(fb + ((unit ^ (row & 7)) * 16)) =
-              make_uint4(pack2(f[8 * e], f[8 * e + 1]), pack2(f[8 * e + 2], f[8 * e + 3]),
-                         pack2(f[8 * e + 4], f[8 * e + 5]), pack2(f[8 * e + 6], f[8 * e + 7]));
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(f_ready);
-      };
 #pragma unroll
       for (int e = 0; e < NC; ++e) f[e] = 0.0f;
       if constexpr (!STATE) {
-        const int start = p.init || p.segs > 1 ? nearest_start_warp(p, it.b, p.rev ? hi : lo, lane) : 0;
+        const int start = p.init || p.segs > 1 ? nearest_start_warp(p, it.b, rev ? hi : lo, lane) : 0;
         auto add = [&](const float* src, int transposed, float w) {
           if (w == 0.0f) return;
           if (transposed) {
@@ -450,47 +520,74 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_pass_tc(const __grid_constant
           }
         };
         if (p.init) add(p.init + bh * DA * DC, p.init_t, p.init_mul * reach(p, g, -1, lo, hi, start, CH));
-        const int s0 = p.rev ? it.seg + 1 : 0, s1 = p.rev ? p.segs : it.seg;
+        const int s0 = rev ? it.seg + 1 : 0, s1 = rev ? p.segs : it.seg;
         for (int s = s0; s < s1; ++s)
           add(p.seg_in + (bh * p.segs + s) * DA * DC, p.seg_t, reach(p, g, s, lo, hi, start, CH));
-        store_f();
       }
       LA_WAIT_WARP(tab_ready, ic);
 
-      for (int n = 0; n < it.last - it.first; ++n, ++cc, tl += TPC) {
-        const int ch = p.rev ? it.last - 1 - n : it.first + n;
+      Starts next = starts_of(p, it.b, rev ? it.last - 1 : it.first);
+      for (int n = 0; n < it.last - it.first; ++n, ++cc, tl += 2) {
+        const int ch = rev ? it.last - 1 - n : it.first + n;
         const int t0 = ch * CH, len = min(CH, p.T - t0);
-        const Starts st = starts_of(p, it.b, ch);
+        const Starts st = next;  // read a chunk ahead
+        if (n + 1 < it.last - it.first) next = starts_of(p, it.b, ch + step);
         const bool any = st.any();
-        const int lag = p.rev && t0 + len == p.T ? 1 : 0;
+        const int lag = rev && t0 + len == p.T ? 1 : 0;
         // rows that reach the state at the chunk's far end
-        const int out_from = p.rev ? 0 : st.last(), out_to = p.rev ? min(len, st.first()) : len;
+        const int out_from = rev ? 0 : st.last(), out_to = rev ? min(len, st.first()) : len;
         const uint32_t sb = tl % NS;
-        LA_WAIT_WARP(&full[sb], tl / NS);
-        uint8_t* bt = smem + sb * SLOT + tid * 16;
-        uint8_t* lt = lo_buf + tid * 16;
-        uint4 v[DA / 16];
+        if constexpr (!STATE) {
+          // the operand copy of the state, [Dc / 64][Da][64] in 128-byte swizzled rows; the last
+          // chunk's (2) has read the old one: its d_full came after it
+          uint8_t* fb = f_buf + (c0 / 64) * (DA * 128) + row * 128;
 #pragma unroll
-        for (int m = 0; m < DA / 16; ++m) v[m] = *reinterpret_cast<const uint4*>(bt + m * 4096);
-        if constexpr (!STATE) LA_WAIT_WARP(sc_full, cc);  // (1) has read B: it may be overwritten
-#pragma unroll
-        for (int m = 0; m < DA / 16; ++m) {
-          const int j = (tid >> 3) + 32 * (m & 3);  // the token of this 16-byte unit
-          const bool on = j >= out_from && j < out_to;
-          const float w = tab[127 + (on ? (p.rev ? j : len - 1 - j) : 0)];
-          const uint32_t u[4] = {v[m].x, v[m].y, v[m].z, v[m].w};
-          uint32_t hi4[4], lo4[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float2 x = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u[e]));
-            x.x = on ? x.x * w : 0.0f;
-            x.y = on ? x.y * w : 0.0f;
-            hi4[e] = pack2(x.x, x.y);
-            const float2 h2 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&hi4[e]));
-            lo4[e] = pack2(x.x - h2.x, x.y - h2.y);
+          for (int e = 0; e < NC / 8; ++e) {
+            const int unit = (c0 % 64) / 8 + e;
+            *reinterpret_cast<uint4*>(fb + ((unit ^ (row & 7)) * 16)) =
+                make_uint4(pack2(f[8 * e], f[8 * e + 1]), pack2(f[8 * e + 2], f[8 * e + 3]),
+                           pack2(f[8 * e + 4], f[8 * e + 5]), pack2(f[8 * e + 6], f[8 * e + 7]));
           }
-          *reinterpret_cast<uint4*>(bt + m * 4096) = make_uint4(hi4[0], hi4[1], hi4[2], hi4[3]);
-          *reinterpret_cast<uint4*>(lt + m * 4096) = make_uint4(lo4[0], lo4[1], lo4[2], lo4[3]);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(f_ready);
+        }
+        // each row's weight as wh + wl (bf16 each); a thread's units lie in four rows
+        __nv_bfloat162 wh[4], wl[4];
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          const int j = (tid >> 3) + 32 * m;
+          const float w = j >= out_from && j < out_to ? pw[rev ? j : len - 1 - j] : 0.0f;
+          const __nv_bfloat16 x = __float2bfloat16_rn(w);
+          wh[m] = __bfloat162bfloat162(x);
+          wl[m] = __float2bfloat162_rn(w - __bfloat162float(x));
+        }
+        LA_WAIT_WARP(&full[sb], tl / NS);
+        uint8_t* bt = ring + sb * SLOT + tid * 16;
+        uint8_t* lt = lo_buf + tid * 16;
+        uint4 v[4];
+#pragma unroll
+        for (int m = 0; m < 4; ++m) v[m] = *reinterpret_cast<const uint4*>(bt + m * 4096);
+        if constexpr (!STATE) LA_WAIT_WARP(sc_full, cc);  // (1) has read B: it may be overwritten
+        // hi = bf16(b wh); b wh - hi is a bf16 number, so lo = bf16(b wl + (b wh - hi)) loses 2^-9 of lo alone
+#pragma unroll 1
+        for (int k = 0; k < DA / 64; ++k) {
+#pragma unroll
+          for (int m = 0; m < 4; ++m) {
+            uint32_t hi4[4], lo4[4];
+            const uint32_t u[4] = {v[m].x, v[m].y, v[m].z, v[m].w};
+            if (k + 1 < DA / 64) v[m] = *reinterpret_cast<const uint4*>(bt + (m + 4) * 4096);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const __nv_bfloat162 x = *reinterpret_cast<const __nv_bfloat162*>(&u[e]);
+              const __nv_bfloat162 h2 = __hmul2(x, wh[m]);
+              const __nv_bfloat162 l2 = __hfma2(x, wl[m], __hfma2(x, wh[m], __hneg2(h2)));
+              hi4[e] = *reinterpret_cast<const uint32_t*>(&h2);
+              lo4[e] = *reinterpret_cast<const uint32_t*>(&l2);
+            }
+            *reinterpret_cast<uint4*>(bt + (m + 4 * k) * 4096) = make_uint4(hi4[0], hi4[1], hi4[2], hi4[3]);
+            *reinterpret_cast<uint4*>(lt + (m + 4 * k) * 4096) = make_uint4(lo4[0], lo4[1], lo4[2], lo4[3]);
+          }
         }
         fence_proxy_async_smem();
         tc_fence_before();  // the last chunk's D has been read
@@ -499,21 +596,19 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_pass_tc(const __grid_constant
 
         LA_WAIT_WARP(d_full, cc);
         tc_fence_after();
-        const float keep = any ? 0.0f : tab[127 + len - lag];
-        constexpr int STEP = NC < 32 ? NC : 32;
+        const float keep = any ? 0.0f : pw[len - lag];
+        if (keep == 0.0f) {
 #pragma unroll
-        for (int q = 0; q < NC / STEP; ++q) {
-          uint32_t r[STEP];
-          tmem_load<STEP>(d_addr + STEP * q, r);
-          tmem_ld_wait();
-#pragma unroll
-          for (int e = 0; e < STEP; ++e) {
-            float& x = f[STEP * q + e];
-            x = keep != 0.0f ? fmaf(keep, x, __uint_as_float(r[e])) : __uint_as_float(r[e]);
-          }
+          for (int e = 0; e < NC; ++e) f[e] = 0.0f;
         }
-        if constexpr (!STATE) {
-          if (n + 1 < it.last - it.first) store_f();  // (2) of this chunk has read the old copy: d_full came after it
+        uint32_t r[2][16];
+        tmem_ld16(d_addr, r[0]);
+#pragma unroll
+        for (int q = 0; q < NC / 16; ++q) {
+          tmem_ld_wait();
+          if (q + 1 < NC / 16) tmem_ld16(d_addr + 16 * (q + 1), r[(q + 1) & 1]);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) f[16 * q + e] = fmaf(keep, f[16 * q + e], __uint_as_float(r[q & 1][e]));
         }
       }
       if (!ok) break;
@@ -521,7 +616,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_pass_tc(const __grid_constant
       float mul = 1.0f;
       if constexpr (STATE) {
         dst = p.seg_state + (bh * p.segs + it.seg) * DA * DC;
-      } else if (p.fin && (p.rev ? it.seg == 0 : it.seg == p.segs - 1)) {
+      } else if (p.fin && (rev ? it.seg == 0 : it.seg == p.segs - 1)) {
         dst = p.fin + bh * DA * DC;
         if (p.fin_scale) mul = p.scale * decay_pow(g, 1);
       }
@@ -532,19 +627,20 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_pass_tc(const __grid_constant
               make_float4(mul * f[e], mul * f[e + 1], mul * f[e + 2], mul * f[e + 3]);
       }
     }
-    if (!ok) {
-      *abort_flag = 1;
-      set_status(p.status, IPTTT_ERR_TIMEOUT);
-    }
   }
 #undef LA_WAIT
 #undef LA_WAIT_WARP
+  if (!ok) {
+    *abort_flag = 1;
+    set_status(p.status, IPTTT_ERR_TIMEOUT);
+  }
 
   __syncthreads();
   if (*abort_flag && threadIdx.x == 0) {
     // copies that were issued land before the block's shared memory is given back
-    const uint32_t n = *issued;
+    const uint32_t n = issued[0], na = issued[1];
     for (uint32_t t = n > (uint32_t)NS ? n - NS : 0; t < n; ++t) mbar_wait(&full[t % NS], (t / NS) & 1);
+    for (uint32_t t = na > 2 ? na - 2 : 0; t < na; ++t) mbar_wait(&a_full[t & 1], (t >> 1) & 1);
   }
   tc_fence_before();
   __syncthreads();
@@ -554,20 +650,27 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_pass_tc(const __grid_constant
   }
 }
 
-template <int DA, int DC, bool STATE>
+template <int DA, int DC, int KIND>
 cudaError_t launch(const TcArgs& a, cudaStream_t st) {
-  constexpr int smem = Cfg<DA, DC, STATE>::SMEM;
-  static_assert(smem <= 232448 && Cfg<DA, DC, STATE>::NS >= 2 * Cfg<DA, DC, STATE>::TPC - 1, "ring");
-  const cudaError_t e =
-      cudaFuncSetAttribute(k_pass_tc<DA, DC, STATE>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  using Cf = Cfg<DA, DC, KIND == STATES>;
+  static_assert(Cf::SMEM <= 232448 && Cf::NS >= 3, "ring");
+  cudaError_t e = cudaFuncSetAttribute(k_pass_tc<DA, DC, KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cf::SMEM);
   if (e != cudaSuccess) return e;
-  k_pass_tc<DA, DC, STATE><<<std::min(a.items, device_sms()), kTcThreads, smem, st>>>(a);
+  if (KIND != STATES) {
+    // the register split takes what the launch gives: with less, the state's warps would wait for good
+    cudaFuncAttributes at;
+    e = cudaFuncGetAttributes(&at, k_pass_tc<DA, DC, KIND>);
+    if (e != cudaSuccess) return e;
+    if (at.numRegs < kRegsLaunch) return cudaErrorInvalidConfiguration;
+  }
+  k_pass_tc<DA, DC, KIND><<<std::min(a.items, device_sms()), Cf::THREADS, Cf::SMEM, st>>>(a);
   return cudaGetLastError();
 }
 
 template <int DA, int DC>
 cudaError_t launch(const TcArgs& a, cudaStream_t st) {
-  return a.p.out ? launch<DA, DC, false>(a, st) : launch<DA, DC, true>(a, st);
+  if (!a.p.out) return launch<DA, DC, STATES>(a, st);
+  return a.p.rev ? launch<DA, DC, REVERSE>(a, st) : launch<DA, DC, FORWARD>(a, st);
 }
 
 }  // namespace
@@ -600,6 +703,9 @@ cudaError_t run_tc(const Pass& p, cudaStream_t st) {
     return tck::make_map_bf16_ld(m, base, (uint64_t)(p.H / g) * width, p.T, p.B, ld, 64, CH);
   };
   if (p.out && !map(&a.ma, p.a, p.lda, p.ga, p.Da)) return cudaErrorInvalidValue;
+  if (p.out && !p.out_f32 &&
+      !tck::make_map_bf16_ld(&a.mo, p.out, (uint64_t)p.H * p.Dc, p.T, p.B, p.ldo, p.Dc / 2, 32, p.Dc == 64))
+    return cudaErrorInvalidValue;
   if (!map(&a.mb, p.b, p.ldb, p.gb, p.Da) || !map(&a.mc, p.c, p.ldc, p.gc, p.Dc)) return cudaErrorInvalidValue;
   if (p.Da == 128) return p.Dc == 128 ? launch<128, 128>(a, st) : launch<128, 64>(a, st);
   return p.Dc == 128 ? launch<64, 128>(a, st) : launch<64, 64>(a, st);

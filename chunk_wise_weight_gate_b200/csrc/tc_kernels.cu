@@ -1370,7 +1370,7 @@ bool make_map_bf16(CUtensorMap* m, const void* base, uint64_t inner, uint64_t ro
 }
 
 bool make_map_bf16_ld(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows, uint64_t outer, uint64_t ld,
-                      uint32_t box_inner, uint32_t box_rows) {
+                      uint32_t box_inner, uint32_t box_rows, bool swizzle64) {
   auto enc = encode_fn();
   if (!enc) return false;
   cuuint64_t dims[3] = {inner, rows, outer};
@@ -1378,7 +1378,9 @@ bool make_map_bf16_ld(CUtensorMap* m, const void* base, uint64_t inner, uint64_t
   cuuint32_t box[3] = {box_inner, box_rows, 1};
   cuuint32_t estr[3] = {1, 1, 1};
   CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
-                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   swizzle64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }

@@ -59,9 +59,10 @@ struct TcParams {
 
 bool make_map_bf16(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows, uint64_t outer,
                    uint32_t box_inner, uint32_t box_rows);
-// As make_map_bf16 for rows `ld` elements apart (a multiple of 8).
+// As make_map_bf16 for rows `ld` elements apart (a multiple of 8); swizzle64: 64-byte swizzle
+// (boxes 32 elements wide).
 bool make_map_bf16_ld(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows, uint64_t outer, uint64_t ld,
-                      uint32_t box_inner, uint32_t box_rows);
+                      uint32_t box_inner, uint32_t box_rows, bool swizzle64 = false);
 cudaError_t launch_tc(int fam, const TcParams& p, int num_sms, cudaStream_t st);
 // Whether FAM_ZV2 can run on this device (a cluster of two fits), and the
 // number of CTA pairs resident at once.
