@@ -408,6 +408,7 @@ struct Work {
   long long words;
   int segs_o, chunks_o;  // passes whose output is Dv wide (O, gv)
   int segs_q, chunks_q;  // passes whose output is Dk wide (gq, gk)
+  int whole;             // (row, head) pairs that are not cut
 };
 
 Work work_of(const ipttt_linattn_params& p, bool backward) {
@@ -421,7 +422,7 @@ Work work_of(const ipttt_linattn_params& p, bool backward) {
   w.words = (p.T + kTcChunk - 1) / kTcChunk * (kTcChunk / 32);
   w.starts = take((size_t)p.B * w.words * 4);
   if (on_tensor_cores(p)) {
-    w.segs_o = w.segs_q = tc_segments(p.B, p.T, p.H, &w.chunks_o);
+    w.segs_o = w.segs_q = tc_segments(p.B, p.T, p.H, &w.chunks_o, &w.whole);
     w.chunks_q = w.chunks_o;
   } else {
     w.segs_o = simt_segments(p.B, p.T, p.H, p.Dk, p.Dv, &w.chunks_o);
@@ -439,17 +440,18 @@ cudaError_t run_one(const ipttt_linattn_params& p, const Pass& q, cudaStream_t s
   return on_tensor_cores(p) ? run_tc(q, st) : run_simt(q, p.dtype, st);
 }
 
-// A pass, after its segments' own states where the row is cut into segments.
-cudaError_t run_pass(const ipttt_linattn_params& p, Pass q, float* seg, int* launches, cudaStream_t st) {
-  if (q.segs > 1) {
+// A pass, after its segments' own states where the row is cut into segments (have: they are in
+// `seg` already).
+cudaError_t run_pass(const ipttt_linattn_params& p, Pass q, float* seg, bool have, int* launches, cudaStream_t st) {
+  if (q.segs > 1 && !have) {
     Pass s = q;
     s.out = nullptr;
     s.seg_state = seg;
     const cudaError_t e = run_one(p, s, st);
     if (e != cudaSuccess) return e;
     ++*launches;
-    q.seg_in = seg;
   }
+  q.seg_in = seg;
   ++*launches;
   return run_one(p, q, st);
 }
@@ -528,13 +530,14 @@ ipttt_status ipttt_linattn_forward(const ipttt_linattn_params* pp, const void* q
   a.fin = S_final_opt;
   a.segs = w.segs_o;
   a.seg_chunks = w.chunks_o;
+  a.whole = w.whole;
   cudaError_t e = mark_starts(p, w, ws, doc_starts, n_doc_starts, status, &a.starts, &launches, st);
   if (e == cudaSuccess && S0_opt && S0_opt == S_final_opt && a.segs > 1) {
     // the last segment may write the final state before the others have read the first
     a.init = reinterpret_cast<const float*>(ws + w.S0);
     e = cudaMemcpyAsync(ws + w.S0, S0_opt, (size_t)p.B * p.H * p.Dk * p.Dv * 4, cudaMemcpyDeviceToDevice, st);
   }
-  if (e == cudaSuccess) e = run_pass(p, a, reinterpret_cast<float*>(ws + w.seg), &launches, st);
+  if (e == cudaSuccess) e = run_pass(p, a, reinterpret_cast<float*>(ws + w.seg), false, &launches, st);
   if (e != cudaSuccess) return cuda_fail("linattn_forward", e);
   count_launches(launches);
   return IPTTT_OK;
@@ -568,6 +571,7 @@ ipttt_status ipttt_linattn_backward(const ipttt_linattn_params* pp, const void* 
   base.log_decay = log_decay;
   base.words = w.words;
   base.scale = p.scale;
+  base.whole = w.whole;
   base.status = status;
   cudaError_t e = mark_starts(p, w, ws, doc_starts, n_doc_starts, status, &base.starts, &launches, st);
 
@@ -595,19 +599,19 @@ ipttt_status ipttt_linattn_backward(const ipttt_linattn_params* pp, const void* 
     return s;
   };
   // a gradient of k or v: straight to the output, or per head in fp32 and then summed over the group
-  auto shared = [&](Pass s, void* out, long long ldo, int D) {
+  auto shared = [&](Pass s, void* out, long long ldo, int D, bool have) {
     s.rev = 1;
     s.init = gS_final_opt;
     s.init_mul = 1.0f / p.scale;
     if (G == 1) {
       s.out = out;
       s.ldo = ldo;
-      return run_pass(p, s, seg, &launches, st);
+      return run_pass(p, s, seg, have, &launches, st);
     }
     s.out = parts;
     s.out_f32 = 1;
     s.ldo = (long long)p.H * D;
-    const cudaError_t err = run_pass(p, s, seg, &launches, st);
+    const cudaError_t err = run_pass(p, s, seg, have, &launches, st);
     if (err != cudaSuccess) return err;
     const long long tokens = (long long)p.B * p.T, n = tokens * p.Hkv * (D / 4);
     const unsigned grid = (unsigned)std::min<long long>((n + kThreads - 1) / kThreads, 148 * 16);
@@ -626,18 +630,21 @@ ipttt_status ipttt_linattn_backward(const ipttt_linattn_params* pp, const void* 
     s.init_t = 1;
     s.out = gq;
     s.ldo = p.ldgq;
-    e = run_pass(p, s, seg, &launches, st);
+    e = run_pass(p, s, seg, false, &launches, st);
   }
   if (e == cudaSuccess) {
     Pass s = pass_of(xk, xq, xg, p.Dk, p.Dv);  // gv, and R's last value gives gS0
     s.fin = gS0_opt;
     s.fin_scale = 1;
-    e = shared(s, gv, p.ldgv, p.Dv);
+    e = shared(s, gv, p.ldgv, p.Dv, false);
   }
   if (e == cudaSuccess) {
     Pass s = pass_of(xv, xg, xq, p.Dv, p.Dk);  // gk, R transposed
     s.init_t = 1;
-    e = shared(s, gk, p.ldgk, p.Dk);
+    // where both passes cut the rows alike, the segments' R of the pass for gv serve here too
+    const bool have = s.segs > 1 && w.segs_o == w.segs_q && w.chunks_o == w.chunks_q;
+    s.seg_t = have;
+    e = shared(s, gk, p.ldgk, p.Dk, have);
   }
   if (e != cudaSuccess) return cuda_fail("linattn_backward", e);
   count_launches(launches);

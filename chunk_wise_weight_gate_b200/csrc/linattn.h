@@ -40,6 +40,7 @@ struct Pass {
   const float* seg_in;           // [B][H][segs][Da][Dc]: the segments' own states (segs > 1)
   float* seg_state;              // the same array, written when out is null
   int segs, seg_chunks;          // segments of a row, chunks of each (the last may have fewer)
+  int whole;                     // (row, head) pairs b * H + h below this are not cut into segments
   int B, T, H, Da, Dc;
   int rev;
   float scale;
@@ -104,7 +105,7 @@ int simt_segments(int B, int T, int H, int Da, int Dc, int* seg_chunks);
 constexpr int kTcChunk = 128;
 bool tc_takes(int Da, int Dc);
 cudaError_t run_tc(const Pass& p, cudaStream_t st);
-int tc_segments(int B, int T, int H, int* seg_chunks);
+int tc_segments(int B, int T, int H, int* seg_chunks, int* whole);
 
 }  // namespace la
 }  // namespace ipttt

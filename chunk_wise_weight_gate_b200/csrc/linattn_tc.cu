@@ -45,7 +45,7 @@ struct Cfg {
   static constexpr int ASLOT = 256 * (DA > DC ? DA : DC);  // an a tile, then the output tile in its place
   static constexpr int SLOT = 256 * (DA > DC ? DA : DC);   // a b or a c tile
   static constexpr int NA = STATE ? 0 : 2;
-  static constexpr int LO = 256 * DA;                 // lo half of the scaled B
+  static constexpr int LO = 256 * DA * (STATE ? 2 : 1);  // lo half of the scaled B (STATES: of two chunks in turn)
   static constexpr int FB = STATE ? 0 : DA * DC * 2;  // bf16 state
   static constexpr int MISC = 2 * kTab * 4 + 256;
   static constexpr int FIT = (232448 - NA * ASLOT - LO - FB - MISC) / SLOT;
@@ -71,20 +71,32 @@ struct TcArgs {
 };
 
 struct Item {
-  int b, h, seg, first, last;  // chunks [first, last)
+  int b, h, seg, segs, first, last;  // chunks [first, last) of segment seg out of segs
 };
 
+// Work items: the (row, head) pairs that are not cut, then the segments of the others, the
+// pairs fastest (heads side by side in memory are walked at the same time).
 __device__ __forceinline__ Item item_of(const Pass& p, int i) {
   Item t;
-  t.h = i % p.H;
-  const int r = i / p.H;
-  // a pass for states alone leaves out the segment that nothing follows
-  const int segs = p.out ? p.segs : p.segs - 1;
-  t.seg = r % segs + (!p.out && p.rev ? 1 : 0);
-  t.b = r / segs;
   const int n = (p.T + CH - 1) / CH;
-  t.first = t.seg * p.seg_chunks;
-  t.last = min(n, t.first + p.seg_chunks);
+  int bh;
+  if (p.out && i < p.whole) {
+    bh = i;
+    t.seg = 0;
+    t.segs = 1;
+    t.first = 0;
+    t.last = n;
+  } else {
+    const int j = p.out ? i - p.whole : i, cut = p.B * p.H - p.whole;
+    bh = p.whole + j % cut;
+    // a pass for states alone leaves out the segment that nothing follows
+    t.seg = j / cut + (!p.out && p.rev ? 1 : 0);
+    t.segs = p.segs;
+    t.first = t.seg * p.seg_chunks;
+    t.last = min(n, t.first + p.seg_chunks);
+  }
+  t.b = bh / p.H;
+  t.h = bh % p.H;
   return t;
 }
 
@@ -161,10 +173,16 @@ __device__ __forceinline__ uint32_t pack2(uint64_t v) {
 }
 __device__ __forceinline__ uint64_t two(const uint32_t* r) { return two(__uint_as_float(r[0]), __uint_as_float(r[1])); }
 
-template <int N>
-__device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&r)[N]) {
-  if constexpr (N == 16) tmem_ld16(addr, r);
-  else tmem_ld32(addr, r);
+// mbar_wait_or_abort in few instructions: there are some twenty waits in the kernel.
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  bool done = mbar_try_wait(bar, parity);
+  if (!done) {
+    const uint64_t t0 = global_timer_ns();
+#pragma unroll 1
+    do done = mbar_try_wait(bar, parity);
+    while (!done && !*abort && global_timer_ns() - t0 < kWaitLimitNs);
+  }
+  return done;
 }
 
 template <int DA, int DC, int KIND>
@@ -184,7 +202,8 @@ __global__ void __launch_bounds__(Cfg<DA, DC, KIND == STATES>::THREADS, 1) k_pas
   uint64_t *sc_full = bars + 2 * NS, *p_ready = sc_full + 1, *conv_done = sc_full + 2, *d_full = sc_full + 3;
   uint64_t *f_ready = sc_full + 4, *o_full = sc_full + 5, *o_free = sc_full + 6, *tab_ready = sc_full + 7;
   uint64_t *a_full = sc_full + 8, *a_empty = sc_full + 10, *drain = sc_full + 12;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  uint64_t* d_odd = sc_full + 13;  // STATES: d_full of the odd chunks (its waiters are a chunk behind)
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(d_odd + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   uint32_t* issued = tmem_slot + 2;  // ring tiles and a tiles whose loads were issued
 
@@ -202,6 +221,7 @@ __global__ void __launch_bounds__(Cfg<DA, DC, KIND == STATES>::THREADS, 1) k_pas
     mbar_init(p_ready, 8);
     mbar_init(conv_done, 8);
     mbar_init(d_full, 1);
+    mbar_init(d_odd, 1);
     mbar_init(f_ready, 8);
     mbar_init(o_full, 1);
     mbar_init(o_free, 8);
@@ -233,16 +253,18 @@ __global__ void __launch_bounds__(Cfg<DA, DC, KIND == STATES>::THREADS, 1) k_pas
   const uint32_t tm = *tmem_slot;
   const bool rev = STATE ? p.rev != 0 : KIND == REVERSE;
   const int step = rev ? -1 : 1;
+  // STATES has room for two chunks' lo halves and D, so that a chunk's scaling runs beside the last one's (4)
+  constexpr uint32_t d_col = STATE ? 0 : col_d(DC), two_col = STATE ? DC : 0, two_lo = STATE ? 256 * DA / 16 : 0;
   bool ok = true;
   // a wait that gives up ends the block's work: every role leaves its loops
 #define LA_WAIT(bar, parity)                                  \
-  if (!mbar_wait_or_abort(bar, (parity) & 1u, abort_flag)) { \
+  if (!wait_for(bar, (parity) & 1u, abort_flag)) {           \
     ok = false;                                               \
     break;                                                    \
   }
   // of all lanes of a warp alike: what follows are warp-wide TMEM accesses
 #define LA_WAIT_WARP(bar, parity)                                                      \
-  if (!__all_sync(0xffffffffu, mbar_wait_or_abort(bar, (parity) & 1u, abort_flag))) { \
+  if (!__all_sync(0xffffffffu, wait_for(bar, (parity) & 1u, abort_flag))) {           \
     ok = false;                                                                        \
     break;                                                                             \
   }
@@ -311,12 +333,13 @@ __global__ void __launch_bounds__(Cfg<DA, DC, KIND == STATES>::THREADS, 1) k_pas
           LA_WAIT(&full[sc], (tl + 1) / NS);
           tc_fence_after();
 #pragma unroll
-          for (int k = 0; k < CH / 16; ++k) mma_bf16(tm + col_d(DC), dbm + k * 128, dc + k * 128, id4, k > 0);
+          for (int k = 0; k < CH / 16; ++k) mma_bf16(tm + d_col + two_col * (cc & 1), dbm + k * 128, dc + k * 128, id4, k > 0);
 #pragma unroll
-          for (int k = 0; k < CH / 16; ++k) mma_bf16(tm + col_d(DC), lo_mn + k * 128, dc + k * 128, id4, 1);
+          for (int k = 0; k < CH / 16; ++k)
+            mma_bf16(tm + d_col + two_col * (cc & 1), lo_mn + (cc & 1) * two_lo + k * 128, dc + k * 128, id4, 1);
           mma_commit(&empty[sb]);
           if constexpr (STATE) mma_commit(&empty[sc]);
-          mma_commit(d_full);
+          mma_commit(STATE && (cc & 1) ? d_odd : d_full);
           if constexpr (!STATE) {
             LA_WAIT(p_ready, cc);
             tc_fence_after();
@@ -483,7 +506,7 @@ __global__ void __launch_bounds__(Cfg<DA, DC, KIND == STATES>::THREADS, 1) k_pas
     const int quarter = warp & 3, half = (warp - Cf::SW) >> 2;
     const int row = DA == 128 ? quarter * 32 + lane : (quarter & 1) * 32 + lane;
     const int c0 = (DA == 128 ? half : half * 2 + (quarter >> 1)) * NC;  // its columns: [c0, c0 + NC)
-    const uint32_t d_addr = tm + col_d(DC) + ((uint32_t)(quarter * 32) << 16) + c0;
+    const uint32_t d_addr = tm + d_col + ((uint32_t)(quarter * 32) << 16) + c0;
     uint32_t tl = 0, cc = 0, ic = 0;
     float f[NC];
     for (int i = blockIdx.x; ok && i < ta.items; i += gridDim.x, ++ic) {
@@ -502,7 +525,7 @@ __global__ void __launch_bounds__(Cfg<DA, DC, KIND == STATES>::THREADS, 1) k_pas
 #pragma unroll
       for (int e = 0; e < NC; ++e) f[e] = 0.0f;
       if constexpr (!STATE) {
-        const int start = p.init || p.segs > 1 ? nearest_start_warp(p, it.b, rev ? hi : lo, lane) : 0;
+        const int start = p.init || it.segs > 1 ? nearest_start_warp(p, it.b, rev ? hi : lo, lane) : 0;
         auto add = [&](const float* src, int transposed, float w) {
           if (w == 0.0f) return;
           if (transposed) {
@@ -520,12 +543,31 @@ __global__ void __launch_bounds__(Cfg<DA, DC, KIND == STATES>::THREADS, 1) k_pas
           }
         };
         if (p.init) add(p.init + bh * DA * DC, p.init_t, p.init_mul * reach(p, g, -1, lo, hi, start, CH));
-        const int s0 = rev ? it.seg + 1 : 0, s1 = rev ? p.segs : it.seg;
+        const int s0 = rev ? it.seg + 1 : 0, s1 = rev ? it.segs : it.seg;
         for (int s = s0; s < s1; ++s)
           add(p.seg_in + (bh * p.segs + s) * DA * DC, p.seg_t, reach(p, g, s, lo, hi, start, CH));
       }
       LA_WAIT_WARP(tab_ready, ic);
 
+      // f <- keep f + D of chunk number c
+      auto advance = [&](float keep, uint32_t c) {
+        tc_fence_after();
+        const uint32_t addr = d_addr + two_col * (c & 1);
+        if (keep == 0.0f) {  // whatever f holds
+#pragma unroll
+          for (int e = 0; e < NC; ++e) f[e] = 0.0f;
+        }
+        uint32_t r[2][16];
+        tmem_ld16(addr, r[0]);
+#pragma unroll
+        for (int q = 0; q < NC / 16; ++q) {
+          tmem_ld_wait();
+          if (q + 1 < NC / 16) tmem_ld16(addr + 16 * (q + 1), r[(q + 1) & 1]);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) f[16 * q + e] = fmaf(keep, f[16 * q + e], __uint_as_float(r[q & 1][e]));
+        }
+      };
+      float keep = 0.0f;
       Starts next = starts_of(p, it.b, rev ? it.last - 1 : it.first);
       for (int n = 0; n < it.last - it.first; ++n, ++cc, tl += 2) {
         const int ch = rev ? it.last - 1 - n : it.first + n;
@@ -564,7 +606,7 @@ __global__ void __launch_bounds__(Cfg<DA, DC, KIND == STATES>::THREADS, 1) k_pas
         }
         LA_WAIT_WARP(&full[sb], tl / NS);
         uint8_t* bt = ring + sb * SLOT + tid * 16;
-        uint8_t* lt = lo_buf + tid * 16;
+        uint8_t* lt = lo_buf + (cc & 1) * (two_lo * 16) + tid * 16;
         uint4 v[4];
 #pragma unroll
         for (int m = 0; m < 4; ++m) v[m] = *reinterpret_cast<const uint4*>(bt + m * 4096);
@@ -594,29 +636,29 @@ __global__ void __launch_bounds__(Cfg<DA, DC, KIND == STATES>::THREADS, 1) k_pas
         __syncwarp();
         if (lane == 0) mbar_arrive(conv_done);
 
-        LA_WAIT_WARP(d_full, cc);
-        tc_fence_after();
-        const float keep = any ? 0.0f : pw[len - lag];
-        if (keep == 0.0f) {
-#pragma unroll
-          for (int e = 0; e < NC; ++e) f[e] = 0.0f;
+        const float keep_now = any ? 0.0f : pw[len - lag];
+        if constexpr (STATE) {
+          if (n > 0) {
+            LA_WAIT_WARP(cc & 1 ? d_full : d_odd, (cc - 1) >> 1);
+            advance(keep, cc - 1);
+          }
+          keep = keep_now;
+        } else {
+          LA_WAIT_WARP(d_full, cc);
+          advance(keep_now, cc);
         }
-        uint32_t r[2][16];
-        tmem_ld16(d_addr, r[0]);
-#pragma unroll
-        for (int q = 0; q < NC / 16; ++q) {
-          tmem_ld_wait();
-          if (q + 1 < NC / 16) tmem_ld16(d_addr + 16 * (q + 1), r[(q + 1) & 1]);
-#pragma unroll
-          for (int e = 0; e < 16; ++e) f[16 * q + e] = fmaf(keep, f[16 * q + e], __uint_as_float(r[q & 1][e]));
-        }
+      }
+      if (!ok) break;
+      if constexpr (STATE) {
+        LA_WAIT_WARP(cc & 1 ? d_full : d_odd, (cc - 1) >> 1);
+        advance(keep, cc - 1);
       }
       if (!ok) break;
       float* dst = nullptr;
       float mul = 1.0f;
       if constexpr (STATE) {
         dst = p.seg_state + (bh * p.segs + it.seg) * DA * DC;
-      } else if (p.fin && (rev ? it.seg == 0 : it.seg == p.segs - 1)) {
+      } else if (p.fin && (rev ? it.seg == 0 : it.seg == it.segs - 1)) {
         dst = p.fin + bh * DA * DC;
         if (p.fin_scale) mul = p.scale * decay_pow(g, 1);
       }
@@ -677,27 +719,37 @@ cudaError_t launch(const TcArgs& a, cudaStream_t st) {
 
 bool tc_takes(int Da, int Dc) { return (Da == 64 || Da == 128) && (Dc == 64 || Dc == 128); }
 
-int tc_segments(int B, int T, int H, int* seg_chunks) {
+int tc_segments(int B, int T, int H, int* seg_chunks, int* whole) {
   const int n = (T + CH - 1) / CH;
-  const long long bh = (long long)B * H;
-  // Chunks the busiest SM walks, in the pass and (at two thirds of the time) in the pass for
-  // the segments' states, with two more an item for its start; the fewest win.
-  auto cost = [&](int segs) {
-    const long long each = (n + segs - 1) / segs;
-    const long long waves = (bh * segs + 147) / 148, waves_s = (bh * (segs - 1) + 147) / 148;
-    return waves * (each + 2) * 3 + (segs > 1 ? waves_s * (each + 2) * 2 + 6 : 0);
+  const long long bh = (long long)B * H, sms = 148;
+  // Time in quarters of a chunk of the full pass: what the busiest SM walks, an item's start
+  // taken as 1.5 chunks, the pass for the segments' states at half the time a chunk, and
+  // its launch as one chunk.  Pairs that fill the SMs evenly stay whole; the rest
+  // are cut into the number of segments that comes out fastest.
+  auto cost = [&](long long uncut, int segs) {
+    const long long cut = bh - uncut, each = (n + segs - 1) / segs;
+    const long long waves = (cut * segs + sms - 1) / sms, waves_s = (cut * (segs - 1) + sms - 1) / sms;
+    return (uncut + sms - 1) / sms * (4 * n + 6) + waves * (4 * each + 6) + (segs > 1 && cut ? waves_s * (2 * each + 6) + 4 : 0);
   };
-  int best = 1;
+  const long long even = bh / sms * sms;
+  long long best = cost(0, 1);
+  int segs = 1;
+  *whole = 0;
   for (int s = 2; s <= std::min(n, 148); ++s)
-    if (cost(s) < cost(best)) best = s;
-  *seg_chunks = (n + best - 1) / best;
+    for (long long u : {0ll, even})
+      if (u < bh && cost(u, s) < best) {
+        best = cost(u, s);
+        segs = s;
+        *whole = (int)u;
+      }
+  *seg_chunks = (n + segs - 1) / segs;
   return (n + *seg_chunks - 1) / *seg_chunks;
 }
 
 cudaError_t run_tc(const Pass& p, cudaStream_t st) {
   TcArgs a;
   a.p = p;
-  a.items = p.B * p.H * (p.out ? p.segs : p.segs - 1);
+  a.items = (p.B * p.H - p.whole) * (p.out ? p.segs : p.segs - 1) + (p.out ? p.whole : 0);
   if (a.items <= 0) return cudaSuccess;
   auto map = [&](CUtensorMap* m, const void* base, long long ld, int g, int width) {
     return tck::make_map_bf16_ld(m, base, (uint64_t)(p.H / g) * width, p.T, p.B, ld, 64, CH);
