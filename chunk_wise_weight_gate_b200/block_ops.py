@@ -10,7 +10,6 @@ projection): heads and width packed, any token stride that is a multiple of 8 el
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 from dataclasses import dataclass
 
@@ -19,6 +18,7 @@ import torch
 from .ipttt import BF16, F32, LinattnParams, QKParams, XentParams, _check, lib
 
 _DTYPES = {"bf16": (BF16, torch.bfloat16), "f32": (F32, torch.float32)}
+_byref = ctypes.byref
 
 
 def _dtype(name: str):
@@ -27,42 +27,55 @@ def _dtype(name: str):
     return _DTYPES[name]
 
 
-@contextlib.contextmanager
-def _on(t: torch.Tensor, stream):
-    """Runs the block on t's device and on `stream`; yields the stream's handle."""
-    if not t.is_cuda:
-        raise ValueError("the tensors must be CUDA tensors")
-    if stream is None:
-        if t.device.index == torch.cuda.current_device():
-            yield torch.cuda.current_stream().cuda_stream
-        else:
-            with torch.cuda.device(t.device):
-                yield torch.cuda.current_stream().cuda_stream
-        return
-    if stream.device != t.device:
-        raise ValueError(f"stream of {stream.device}, tensors on {t.device}")
-    with torch.cuda.device(t.device), torch.cuda.stream(stream):  # what is allocated inside belongs to `stream`
-        yield stream.cuda_stream
+class _On:
+    """Runs its block on t's device and on `stream` (default: that device's current one), so that what
+    is allocated inside belongs to that stream; gives the stream's handle."""
+    __slots__ = ("device", "stream", "inner")
+
+    def __init__(self, t: torch.Tensor, stream):
+        if not t.is_cuda:
+            raise ValueError("the tensors must be CUDA tensors")
+        self.device, self.stream, self.inner = t.device, stream, ()
+        if stream is not None and stream.device != self.device:
+            raise ValueError(f"stream of {stream.device}, tensors on {self.device}")
+
+    def __enter__(self):
+        index = self.device.index
+        if self.stream is not None:
+            self.inner = (torch.cuda.device(index), torch.cuda.stream(self.stream))
+        elif index != torch._C._cuda_getDevice():
+            self.inner = (torch.cuda.device(index),)
+        for c in self.inner:
+            c.__enter__()
+        return self.stream.cuda_stream if self.stream is not None else torch._C._cuda_getCurrentRawStream(index)
+
+    def __exit__(self, *error):
+        for c in reversed(self.inner):
+            c.__exit__(*error)
+
+
+def _mismatch(t, name, shape, dtype, device):
+    return ValueError(f"{name}: {tuple(t.shape)} {t.dtype} on {t.device}, expected {shape} {dtype} on {device}")
 
 
 def _flat(t, name, shape, dtype, device):
     """Pointer of a packed tensor (None: None)."""
     if t is None:
         return None
-    if t.dtype != dtype or t.device != device or tuple(t.shape) != shape:
-        raise ValueError(f"{name}: {tuple(t.shape)} {t.dtype} on {t.device}, expected {shape} {dtype} on {device}")
+    if t.dtype is not dtype or t.shape != shape or t.device != device:
+        raise _mismatch(t, name, shape, dtype, device)
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
 
 
 def _tokens(t, name, shape, dtype, device):
-    """(pointer, token stride) of a token tensor [B, T, heads, width]."""
-    if t.dtype != dtype or t.device != device or tuple(t.shape) != shape:
-        raise ValueError(f"{name}: {tuple(t.shape)} {t.dtype} on {t.device}, expected {shape} {dtype} on {device}")
-    B, T, H, D = shape
+    """(pointer, token stride) of a token tensor [B, T, heads, width]; stride 0: packed."""
+    if t.dtype is not dtype or t.shape != shape or t.device != device:
+        raise _mismatch(t, name, shape, dtype, device)
     if t.is_contiguous():
-        return t.data_ptr(), H * D
+        return t.data_ptr(), 0
+    B, T, H, D = shape
     sb, st, sh, sd = t.stride()
     ld = st if T > 1 else sb if B > 1 else H * D
     if (sd != 1 and D > 1) or (sh != D and H > 1) or (B > 1 and sb != T * ld) or ld < H * D or ld % 8:
@@ -89,7 +102,7 @@ def _workspace(workspace, need, device):
 
 
 def _size(fn, params, what):
-    n = int(fn(ctypes.byref(params)))
+    n = fn(_byref(params))
     if n == 0:
         raise ValueError(f"invalid configuration {what}")
     return n
@@ -111,38 +124,37 @@ class QKNormRopeConfig:
     interleaved: bool = False
     dtype: str = "bf16"
 
-    def params(self, **ld) -> QKParams:
+    def params(self, ldq=0, ldk=0, ldqo=0, ldko=0, ldgq=0, ldgk=0) -> QKParams:
         return QKParams(self.B, self.T, self.Hq, self.Hk, self.D, self.R, _dtype(self.dtype)[0], int(self.interleaved),
-                        float(self.eps), *(int(ld.get(n, 0)) for n in ("ldq", "ldk", "ldqo", "ldko", "ldgq", "ldgk")))
+                        self.eps, ldq, ldk, ldqo, ldko, ldgq, ldgk)
 
 
 def _qk_inputs(cfg, q, k, wq, wk, inv_freq, positions):
     dt, dev = _dtype(cfg.dtype)[1], q.device
-    pq, ldq = _tokens(q, "q", (cfg.B, cfg.T, cfg.Hq, cfg.D), dt, dev)
-    pk, ldk = _tokens(k, "k", (cfg.B, cfg.T, cfg.Hk, cfg.D), dt, dev)
-    ptrs = [pq, pk, _flat(wq, "wq", (cfg.D,), dt, dev), _flat(wk, "wk", (cfg.D,), dt, dev)]
-    if cfg.R:
-        ptrs += [_flat(inv_freq, "inv_freq", (cfg.R // 2,), torch.float64, dev),
-                 _flat(positions, "positions", (cfg.B, cfg.T), torch.int64, dev)]
-    else:
-        ptrs += [None, None]
-    return ptrs, ldq, ldk, dt, dev
+    B, T, D = cfg.B, cfg.T, cfg.D
+    sq, sk = (B, T, cfg.Hq, D), (B, T, cfg.Hk, D)
+    pq, ldq = _tokens(q, "q", sq, dt, dev)
+    pk, ldk = _tokens(k, "k", sk, dt, dev)
+    turned = (_flat(inv_freq, "inv_freq", (cfg.R // 2,), torch.float64, dev),
+              _flat(positions, "positions", (B, T), torch.int64, dev)) if cfg.R else (None, None)
+    return (pq, pk, _flat(wq, "wq", (D,), dt, dev), _flat(wk, "wk", (D,), dt, dev), *turned), ldq, ldk, sq, sk, dt, dev
 
 
 def qk_norm_rope(cfg: QKNormRopeConfig, q, k, wq, wk, inv_freq, positions, *, q_out=None, k_out=None, stream=None):
     """RMS norm of every head of q [B,T,Hq,D] and k [B,T,Hk,D] with weights wq, wk [D], then
     the rotation by positions [B,T] (int64) * inv_freq [R/2] (float64, radians a
     position).  Returns (q_out, k_out), packed unless given; q_out may be q, k_out k."""
-    (*ptrs,), ldq, ldk, dt, dev = _qk_inputs(cfg, q, k, wq, wk, inv_freq, positions)
-    with _on(q, stream) as st:
+    ptrs, ldq, ldk, sq, sk, dt, dev = _qk_inputs(cfg, q, k, wq, wk, inv_freq, positions)
+    with _On(q, stream) as st:
         if q_out is None:
-            q_out = torch.empty(cfg.B, cfg.T, cfg.Hq, cfg.D, dtype=dt, device=dev)
+            q_out = torch.empty(sq, dtype=dt, device=dev)
         if k_out is None:
-            k_out = torch.empty(cfg.B, cfg.T, cfg.Hk, cfg.D, dtype=dt, device=dev)
-        po, ldqo = _tokens(q_out, "q_out", (cfg.B, cfg.T, cfg.Hq, cfg.D), dt, dev)
-        pk, ldko = _tokens(k_out, "k_out", (cfg.B, cfg.T, cfg.Hk, cfg.D), dt, dev)
-        p = cfg.params(ldq=ldq, ldk=ldk, ldqo=ldqo, ldko=ldko)
-        _check(lib().ipttt_qk_norm_rope(ctypes.byref(p), *ptrs, po, pk, st), "ipttt_qk_norm_rope")
+            k_out = torch.empty(sk, dtype=dt, device=dev)
+        pq, ldqo = _tokens(q_out, "q_out", sq, dt, dev)
+        pk, ldko = _tokens(k_out, "k_out", sk, dt, dev)
+        rc = lib().ipttt_qk_norm_rope(_byref(cfg.params(ldq, ldk, ldqo, ldko)), *ptrs, pq, pk, st)
+        if rc:
+            _check(rc, "ipttt_qk_norm_rope")
     return q_out, k_out
 
 
@@ -150,19 +162,18 @@ def qk_norm_rope_backward(cfg: QKNormRopeConfig, q, k, wq, wk, inv_freq, positio
                           gk=None, workspace=None, stream=None):
     """Gradients of <gq_out, q_out> + <gk_out, k_out>: a dict with q and k (the call's dtype,
     packed unless gq, gk are given; they may be gq_out, gk_out) and wq, wk (fp32)."""
-    (*ptrs,), ldq, ldk, dt, dev = _qk_inputs(cfg, q, k, wq, wk, inv_freq, positions)
-    sq, sk = (cfg.B, cfg.T, cfg.Hq, cfg.D), (cfg.B, cfg.T, cfg.Hk, cfg.D)
+    ptrs, ldq, ldk, sq, sk, dt, dev = _qk_inputs(cfg, q, k, wq, wk, inv_freq, positions)
     pgq, ldqo = _tokens(gq_out, "gq_out", sq, dt, dev)
     pgk, ldko = _tokens(gk_out, "gk_out", sk, dt, dev)
-    with _on(q, stream) as st:
-        gq = torch.empty(*sq, dtype=dt, device=dev) if gq is None else gq
-        gk = torch.empty(*sk, dtype=dt, device=dev) if gk is None else gk
+    with _On(q, stream) as st:
+        gq = torch.empty(sq, dtype=dt, device=dev) if gq is None else gq
+        gk = torch.empty(sk, dtype=dt, device=dev) if gk is None else gk
         po, ldgq = _tokens(gq, "gq", sq, dt, dev)
         pk, ldgk = _tokens(gk, "gk", sk, dt, dev)
         gw = torch.empty(2, cfg.D, dtype=torch.float32, device=dev)
-        p = cfg.params(ldq=ldq, ldk=ldk, ldqo=ldqo, ldko=ldko, ldgq=ldgq, ldgk=ldgk)
+        p = cfg.params(ldq, ldk, ldqo, ldko, ldgq, ldgk)
         ws = _workspace(workspace, _size(lib().ipttt_qk_norm_rope_backward_workspace_size, p, cfg), dev)
-        _check(lib().ipttt_qk_norm_rope_backward(ctypes.byref(p), *ptrs, pgq, pgk, po, pk, gw.data_ptr(),
+        _check(lib().ipttt_qk_norm_rope_backward(_byref(p), *ptrs, pgq, pgk, po, pk, gw.data_ptr(),
                                                  gw.data_ptr() + 4 * cfg.D, ws.data_ptr(), ws.numel(), st),
                "ipttt_qk_norm_rope_backward")
     return {"q": gq, "k": gk, "wq": gw[0], "wk": gw[1]}
@@ -182,10 +193,9 @@ class LinearAttentionConfig:
     scale: float
     dtype: str = "bf16"
 
-    def params(self, **ld) -> LinattnParams:
-        return LinattnParams(self.B, self.T, self.H, self.Hkv, self.Dk, self.Dv, _dtype(self.dtype)[0],
-                             float(self.scale),
-                             *(int(ld.get(n, 0)) for n in ("ldq", "ldk", "ldv", "ldo", "ldgq", "ldgk", "ldgv")))
+    def params(self, ldq=0, ldk=0, ldv=0, ldo=0, ldgq=0, ldgk=0, ldgv=0, T=None) -> LinattnParams:
+        return LinattnParams(self.B, self.T if T is None else T, self.H, self.Hkv, self.Dk, self.Dv,
+                             _dtype(self.dtype)[0], self.scale, ldq, ldk, ldv, ldo, ldgq, ldgk, ldgv)
 
     def shapes(self):
         B, T = self.B, self.T
@@ -212,15 +222,15 @@ def linear_attention(cfg: LinearAttentionConfig, q, k, v, log_decay, doc_starts=
     pv, ldv = _tokens(v, "v", sh["v"], dt, dev)
     pd = _flat(log_decay, "log_decay", (cfg.H,), f32, dev)
     p0 = _flat(S0, "S0", sh["S"], f32, dev)
-    with _on(q, stream) as st:
+    with _On(q, stream) as st:
         if O is None:
-            O = torch.empty(*sh["O"], dtype=dt, device=dev)
-        Sf = torch.empty(*sh["S"], dtype=f32, device=dev) if S_final is True else S_final if S_final is not False else None
+            O = torch.empty(sh["O"], dtype=dt, device=dev)
+        Sf = torch.empty(sh["S"], dtype=f32, device=dev) if S_final is True else S_final if S_final is not False else None
         po, ldo = _tokens(O, "O", sh["O"], dt, dev)
-        p = cfg.params(ldq=ldq, ldk=ldk, ldv=ldv, ldo=ldo)
+        p = cfg.params(ldq, ldk, ldv, ldo)
         ws = _workspace(workspace, _size(lib().ipttt_linattn_workspace_size, p, cfg), dev)
         dp, nd, keep = _starts(doc_starts, dev)
-        _check(lib().ipttt_linattn_forward(ctypes.byref(p), pq, pk, pv, pd, dp, nd, p0, po,
+        _check(lib().ipttt_linattn_forward(_byref(p), pq, pk, pv, pd, dp, nd, p0, po,
                                            _flat(Sf, "S_final", sh["S"], f32, dev), ws.data_ptr(), ws.numel(), st),
                "ipttt_linattn_forward")
     return O if Sf is None else (O, Sf)
@@ -239,18 +249,28 @@ def linear_attention_backward(cfg: LinearAttentionConfig, q, k, v, log_decay, do
     pd = _flat(log_decay, "log_decay", (cfg.H,), f32, dev)
     p0 = _flat(S0, "S0", sh["S"], f32, dev)
     ps = _flat(gS_final, "gS_final", sh["S"], f32, dev)
-    with _on(q, stream) as st:
-        out = {n: torch.empty(*sh[n], dtype=dt, device=dev) for n in ("q", "k", "v")}
+    with _On(q, stream) as st:
+        out = {n: torch.empty(sh[n], dtype=dt, device=dev) for n in ("q", "k", "v")}
         if S0 is not None:
-            out["S0"] = torch.empty(*sh["S"], dtype=f32, device=dev)
-        p = cfg.params(ldq=ldq, ldk=ldk, ldv=ldv, ldo=ldo)
+            out["S0"] = torch.empty(sh["S"], dtype=f32, device=dev)
+        p = cfg.params(ldq, ldk, ldv, ldo)
         ws = _workspace(workspace, _size(lib().ipttt_linattn_backward_workspace_size, p, cfg), dev)
         dp, nd, keep = _starts(doc_starts, dev)
-        _check(lib().ipttt_linattn_backward(ctypes.byref(p), pq, pk, pv, pd, dp, nd, p0, pg, ps, out["q"].data_ptr(),
+        _check(lib().ipttt_linattn_backward(_byref(p), pq, pk, pv, pd, dp, nd, p0, pg, ps, out["q"].data_ptr(),
                                             out["k"].data_ptr(), out["v"].data_ptr(),
                                             out["S0"].data_ptr() if S0 is not None else None, ws.data_ptr(),
                                             ws.numel(), st), "ipttt_linattn_backward")
     return out
+
+
+def _rows(t, name, shape, dtype, device):
+    """_tokens for one token a row: t [B, heads, width]."""
+    if t.dtype is not dtype or t.shape != shape or t.device != device:
+        raise _mismatch(t, name, shape, dtype, device)
+    if t.is_contiguous():
+        return t.data_ptr(), 0
+    B, H, D = shape
+    return _tokens(t.unsqueeze(1), name, (B, 1, H, D), dtype, device)
 
 
 def linear_attention_step(cfg: LinearAttentionConfig, S, q, k, v, log_decay, starts=None, *, o=None, stream=None):
@@ -260,26 +280,21 @@ def linear_attention_step(cfg: LinearAttentionConfig, S, q, k, v, log_decay, sta
     dt, dev = _dtype(cfg.dtype)[1], q.device
     B, H, Hkv, Dk, Dv = cfg.B, cfg.H, cfg.Hkv, cfg.Dk, cfg.Dv
 
-    def rows(t, name, heads, width):
-        if t.dim() != 3:
-            raise ValueError(f"{name}: {tuple(t.shape)}, expected {(B, heads, width)}")
-        return _tokens(t.unsqueeze(1), name, (B, 1, heads, width), dt, dev)
-
-    pq, ldq = rows(q, "q", H, Dk)
-    pk, ldk = rows(k, "k", Hkv, Dk)
-    pv, ldv = rows(v, "v", Hkv, Dv)
+    pq, ldq = _rows(q, "q", (B, H, Dk), dt, dev)
+    pk, ldk = _rows(k, "k", (B, Hkv, Dk), dt, dev)
+    pv, ldv = _rows(v, "v", (B, Hkv, Dv), dt, dev)
     ps = _flat(S, "S", (B, H, Dk, Dv), torch.float32, dev)
     pd = _flat(log_decay, "log_decay", (H,), torch.float32, dev)
     pn = _flat(starts, "starts", (B,), torch.int32, dev)
     if ps is None:
         raise ValueError("S is missing")
-    with _on(q, stream) as st:
+    with _On(q, stream) as st:
         if o is None:
-            o = torch.empty(B, H, Dv, dtype=dt, device=dev)
-        po, ldo = rows(o, "o", H, Dv)
-        p = cfg.params(ldq=ldq, ldk=ldk, ldv=ldv, ldo=ldo)
-        p.T = 1
-        _check(lib().ipttt_linattn_step(ctypes.byref(p), ps, pq, pk, pv, pd, pn, po, st), "ipttt_linattn_step")
+            o = torch.empty((B, H, Dv), dtype=dt, device=dev)
+        po, ldo = _rows(o, "o", (B, H, Dv), dt, dev)
+        rc = lib().ipttt_linattn_step(_byref(cfg.params(ldq, ldk, ldv, ldo, T=1)), ps, pq, pk, pv, pd, pn, po, st)
+        if rc:
+            _check(rc, "ipttt_linattn_step")
     return o
 
 
@@ -311,11 +326,11 @@ def cross_entropy(cfg: CrossEntropyConfig, H, W, targets, *, workspace=None, str
     dt, dev, f32 = _dtype(cfg.dtype)[1], H.device, torch.float32
     ptrs = [_flat(H, "H", (cfg.N, cfg.d), dt, dev), _flat(W, "W", (cfg.V, cfg.d), dt, dev),
             _flat(targets, "targets", (cfg.N,), torch.int64, dev)]
-    with _on(H, stream) as st:
+    with _On(H, stream) as st:
         loss, lse = torch.empty(cfg.N, dtype=f32, device=dev), torch.empty(cfg.N, dtype=f32, device=dev)
         ws = _workspace(workspace, cross_entropy_workspace_size(cfg), dev)
         p = cfg.params()
-        _check(lib().ipttt_xent_forward(ctypes.byref(p), *ptrs, loss.data_ptr(), lse.data_ptr(), ws.data_ptr(),
+        _check(lib().ipttt_xent_forward(_byref(p), *ptrs, loss.data_ptr(), lse.data_ptr(), ws.data_ptr(),
                                         ws.numel(), st), "ipttt_xent_forward")
     return loss, lse
 
@@ -328,12 +343,12 @@ def cross_entropy_backward(cfg: CrossEntropyConfig, H, W, targets, lse, gloss, *
     ptrs = [_flat(H, "H", (cfg.N, cfg.d), dt, dev), _flat(W, "W", (cfg.V, cfg.d), dt, dev),
             _flat(targets, "targets", (cfg.N,), torch.int64, dev), _flat(lse, "lse", (cfg.N,), f32, dev),
             _flat(gloss, "gloss", (cfg.N,), f32, dev)]
-    with _on(H, stream) as st:
+    with _On(H, stream) as st:
         gH = torch.empty(cfg.N, cfg.d, dtype=dt, device=dev) if gH is None else gH
         gW = torch.empty(cfg.V, cfg.d, dtype=dt, device=dev) if gW is None else gW
         ws = _workspace(workspace, cross_entropy_workspace_size(cfg, backward=True), dev)
         p = cfg.params()
-        _check(lib().ipttt_xent_backward(ctypes.byref(p), *ptrs, _flat(gH, "gH", (cfg.N, cfg.d), dt, dev),
+        _check(lib().ipttt_xent_backward(_byref(p), *ptrs, _flat(gH, "gH", (cfg.N, cfg.d), dt, dev),
                                          _flat(gW, "gW", (cfg.V, cfg.d), dt, dev), ws.data_ptr(), ws.numel(), st),
                "ipttt_xent_backward")
     return {"H": gH, "W": gW}
