@@ -185,7 +185,89 @@ __device__ __forceinline__ bool keep_row(const Args& a, const Tile& t, int m) {
   return a.rows == GR_LAST ? tok >= cm.last_start : (cm.cont && tok < cm.first_end);
 }
 
-template <bool PAIR>
+constexpr float kLog2e = 1.4426950408889634f;
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// The softmax epilogues of one row's 128 accumulator columns from `tacc` on (all lanes of the
+// warp; m, n: the row and first column of this thread's part of the output).
+template <int EPI>
+__device__ __forceinline__ void row_epilogue(const Args& a, uint32_t tacc, int m, int n) {
+  const Softmax& s = a.softmax;
+  const bool on = m < a.M;
+  const int64_t t = on ? s.targets[m] : s.ignore;
+  const bool part = on && t != s.ignore && t >= 0 && t < s.V;
+  const int hit = part && t >= s.v0 + n && t < s.v0 + n + 128 ? (int)(t - s.v0 - n) : -1;  // the target's column here
+  if (EPI == 1) {
+    // running maximum and sum, 32 columns at a time
+    float mx = -INFINITY, sum = 0.0f, tl = 0.0f;
+#pragma unroll 1
+    for (int q = 0; q < 4; ++q) {
+      uint32_t r[32];
+      tmem_ld32(tacc + 32 * q, r);
+      tmem_ld_wait();
+      const int left = s.cols - n - 32 * q;  // columns that exist
+      if (left <= 0) continue;
+      if (left < 32) {
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+          if (e >= left) r[e] = 0xff800000u;  // -inf
+      }
+      if ((hit >> 5) == q) {
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+          if (e == (hit & 31)) tl = __uint_as_float(r[e]);
+      }
+      float top = mx;
+#pragma unroll
+      for (int e = 0; e < 32; ++e) top = fmaxf(top, __uint_as_float(r[e]));
+      const float base = top == -INFINITY ? 0.0f : top;  // no logit above -inf yet: every term is 0
+      float acc[4] = {};
+#pragma unroll
+      for (int e = 0; e < 32; ++e) acc[e & 3] += exp2_fast((__uint_as_float(r[e]) - base) * kLog2e);
+      sum = sum * exp2_fast((mx - base) * kLog2e) + ((acc[0] + acc[1]) + (acc[2] + acc[3]));
+      mx = top;
+    }
+    if (on && n < s.cols) s.part[(long long)((s.v0 + n) / 128) * a.M + m] = make_float2(mx, sum);
+    if (hit >= 0) s.target_logit[m] = tl;
+  } else {
+    const float lse = part ? s.lse[m] : 0.0f, g = part ? s.gloss[m] : 0.0f;
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + (long long)m * a.ldo + n;
+#pragma unroll 1
+    for (int q = 0; q < 4; ++q) {
+      uint32_t r[32];
+      tmem_ld32(tacc + 32 * q, r);
+      tmem_ld_wait();
+      if (!on || n + 32 * q >= a.N) continue;
+      const int left = s.cols - n - 32 * q;
+      const int at = (hit >> 5) == q ? hit & 31 : -1;
+      uint4* o = reinterpret_cast<uint4*>(out + 32 * q);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        uint32_t w[4];
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          float v[2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int c = 8 * e + 2 * h + k;
+            const float x = exp2_fast((__uint_as_float(r[c]) - lse) * kLog2e) - (c == at ? 1.0f : 0.0f);
+            v[k] = part && c < left ? x * g : 0.0f;
+          }
+          const __nv_bfloat162 pr = __floats2bfloat162_rn(v[0], v[1]);
+          w[h] = *reinterpret_cast<const uint32_t*>(&pr);
+        }
+        o[e] = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
+  }
+}
+
+// EPI: 0 the outputs of GO_F32, GO_F32_ADD and GO_BF16, 1 GO_ROW_STATS, 2 GO_ROW_GRAD.
+template <bool PAIR, int EPI>
 __global__ void __launch_bounds__(THREADS, 1) gemm_kernel(const __grid_constant__ KArgs ka) {
   using Cf = Cfg<PAIR>;
   constexpr int TK = Cf::TK;
@@ -336,8 +418,9 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_kernel(const __grid_constant_
       if (a.mode == GM_PLAIN) base = (long long)t.slice * a.osz + (long long)m * a.ldo;
       else if (a.mode == GM_CHUNK_ROWS) base = (long long)t.b * a.osz + (long long)(t.t0 + m) * a.ldo;
       else base = ((long long)(t.chunk - a.chunk_base) * a.B + t.b) * a.osz + (long long)m * a.ldo;
+      if constexpr (EPI != 0) row_epilogue<EPI>(a, tacc, m, t.n0 + 128 * half);
 #pragma unroll 1
-      for (int q = 0; q < 4; ++q) {
+      for (int q = 0; q < (EPI == 0 ? 4 : 0); ++q) {
         uint32_t r[32];
         tmem_ld32(tacc + 32 * q, r);
         tmem_ld_wait();
@@ -400,7 +483,24 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_kernel(const __grid_constant_
   }
 }
 
-// Clusters of two that can be resident at once (0: the pair form cannot run).
+cudaLaunchConfig_t pair_config(int grid, cudaStream_t st, cudaLaunchAttribute* attr) {
+  cudaLaunchConfig_t cfg = {};
+  attr->id = cudaLaunchAttributeClusterDimension;
+  attr->val.clusterDim.x = 2;
+  attr->val.clusterDim.y = 1;
+  attr->val.clusterDim.z = 1;
+  cfg.gridDim = dim3((unsigned)grid, 1, 1);
+  cfg.blockDim = dim3(THREADS, 1, 1);
+  cfg.dynamicSmemBytes = Cfg<true>::SMEM;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cfg;
+}
+
+// Clusters of two that can be resident at once (0: the pair form cannot run).  Every build of
+// the pair kernel has the same threads and shared memory, and one block a SM, so the
+// plain one's number holds for all.
 int pair_workers(cudaStream_t st) {
   static int cached[64];
   static bool have[64];
@@ -409,25 +509,32 @@ int pair_workers(cudaStream_t st) {
   if (have[dev]) return cached[dev];
   int n = 0;
   constexpr int smem = Cfg<true>::SMEM;
-  if (cudaFuncSetAttribute(gemm_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) == cudaSuccess) {
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.gridDim = dim3(2, 1, 1);
-    cfg.blockDim = dim3(THREADS, 1, 1);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(&n, gemm_kernel<true>, &cfg) != cudaSuccess) n = 0;
+  if (cudaFuncSetAttribute(gemm_kernel<true, 0>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) == cudaSuccess &&
+      cudaFuncSetAttribute(gemm_kernel<true, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) == cudaSuccess &&
+      cudaFuncSetAttribute(gemm_kernel<true, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) == cudaSuccess) {
+    cudaLaunchAttribute attr;
+    const cudaLaunchConfig_t cfg = pair_config(2, st, &attr);
+    if (cudaOccupancyMaxActiveClusters(&n, gemm_kernel<true, 0>, &cfg) != cudaSuccess) n = 0;
   }
   cudaGetLastError();
   cached[dev] = n;
   have[dev] = true;
   return n;
+}
+
+template <int EPI>
+cudaError_t launch(const KArgs& ka, int np, long long tiles, int num_sms, cudaStream_t st) {
+  if (np > 0) {
+    cudaLaunchAttribute attr;
+    const cudaLaunchConfig_t cfg = pair_config((int)(2 * std::max(1LL, std::min(tiles, (long long)np))), st, &attr);
+    return cudaLaunchKernelEx(&cfg, gemm_kernel<true, EPI>, ka);
+  }
+  constexpr int smem = Cfg<false>::SMEM;
+  const cudaError_t e = cudaFuncSetAttribute(gemm_kernel<false, EPI>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  const int grid = (int)std::max(1LL, std::min(tiles, (long long)num_sms));
+  gemm_kernel<false, EPI><<<grid, THREADS, smem, st>>>(ka);
+  return cudaGetLastError();
 }
 
 long long tiles_of(const Args& a, int tm) {
@@ -440,7 +547,8 @@ long long tiles_of(const Args& a, int tm) {
 }  // namespace
 
 cudaError_t run(const Args& a, int num_sms, cudaStream_t st) {
-  if (a.N <= 0 || a.N % 32 != 0 || !a.out || !a.A.base || !a.Bop.base) return cudaErrorInvalidValue;
+  const bool stats = a.out_kind == GO_ROW_STATS;
+  if (a.N <= 0 || a.N % 32 != 0 || (!a.out && !stats) || !a.A.base || !a.Bop.base) return cudaErrorInvalidValue;
   if (a.mode == GM_PLAIN) {
     // every slice holds at least one K block of either form (64 or 128 K)
     if (a.M <= 0 || a.K <= 0 || a.ksplit < 0 || (a.ksplit > 1 && a.ksplit > a.K / 128)) return cudaErrorInvalidValue;
@@ -452,6 +560,10 @@ cudaError_t run(const Args& a, int num_sms, cudaStream_t st) {
     if (a.mode == GM_CHUNK_K && a.M <= 0) return cudaErrorInvalidValue;
     if (a.mode == GM_CHUNK_ROWS && a.rows != GR_ALL && !a.meta) return cudaErrorInvalidValue;
   }
+  if (a.out_kind >= GO_ROW_STATS &&
+      (a.mode != GM_PLAIN || a.ksplit > 1 || !a.softmax.targets || a.softmax.v0 % 256 != 0 || a.softmax.cols > a.N ||
+       (stats ? !a.softmax.part || !a.softmax.target_logit : !a.softmax.lse || !a.softmax.gloss)))
+    return cudaErrorInvalidValue;
   // Pairs where a 256-row tile is not mostly padding: M of at least 256; in the
   // per-chunk-rows form chunks of a multiple of 256 tokens; in the per-chunk-K
   // form chunks of a multiple of the pair's 128 K per stage.
@@ -464,35 +576,15 @@ cudaError_t run(const Args& a, int num_sms, cudaStream_t st) {
   const bool bmn = a.mode == GM_CHUNK_K || a.b_mn;
   KArgs ka;
   ka.a = a;
-  if (!tck::make_map_bf16(&ka.amap, a.A.base, a.A.inner, a.A.rows, a.A.outer, 64, amn ? tk : 128) ||
-      !tck::make_map_bf16(&ka.bmap, a.Bop.base, a.Bop.inner, a.Bop.rows, a.Bop.outer, 64, bmn ? tk : 128))
-    return cudaErrorInvalidValue;
-  if (np > 0) {
-    const long long tiles = tiles_of(a, 256);
-    if (tiles <= 0 || tiles > 0x7fffffffLL) return cudaErrorInvalidValue;
-    constexpr int smem = Cfg<true>::SMEM;
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.gridDim = dim3((unsigned)(2 * std::max(1LL, std::min(tiles, (long long)np))), 1, 1);
-    cfg.blockDim = dim3(THREADS, 1, 1);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, gemm_kernel<true>, ka);
-  }
-  const long long tiles = tiles_of(a, 128);
+  auto map = [](CUtensorMap* m, const Operand& o, int box_rows) {
+    return tck::make_map_bf16_ld(m, o.base, o.inner, o.rows, o.outer, o.ld ? o.ld : o.inner, 64, box_rows);
+  };
+  if (!map(&ka.amap, a.A, amn ? tk : 128) || !map(&ka.bmap, a.Bop, bmn ? tk : 128)) return cudaErrorInvalidValue;
+  const long long tiles = tiles_of(a, np > 0 ? 256 : 128);
   if (tiles <= 0 || tiles > 0x7fffffffLL) return cudaErrorInvalidValue;
-  constexpr int smem = Cfg<false>::SMEM;
-  cudaError_t e = cudaFuncSetAttribute(gemm_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  const int grid = (int)std::max(1LL, std::min(tiles, (long long)num_sms));
-  gemm_kernel<false><<<grid, THREADS, smem, st>>>(ka);
-  return cudaGetLastError();
+  if (a.out_kind == GO_ROW_STATS) return launch<1>(ka, np, tiles, num_sms, st);
+  if (a.out_kind == GO_ROW_GRAD) return launch<2>(ka, np, tiles, num_sms, st);
+  return launch<0>(ka, np, tiles, num_sms, st);
 }
 
 }  // namespace gemm

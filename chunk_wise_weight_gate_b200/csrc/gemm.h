@@ -29,12 +29,30 @@ enum Mode { GM_PLAIN = 0, GM_CHUNK_ROWS = 1, GM_CHUNK_K = 2 };
 // Rows of a chunk an GM_CHUNK_ROWS output keeps: all, the chunk's last document
 // segment, or its first segment when it continues the previous chunk's document.
 enum Rows { GR_ALL = 0, GR_LAST = 1, GR_FIRST = 2 };
-enum Out { GO_F32 = 0, GO_F32_ADD = 1, GO_BF16 = 2 };
+// GO_ROW_STATS, GO_ROW_GRAD (PLAIN; a tile's columns are a row's logits, never stored): see Softmax.
+enum Out { GO_F32 = 0, GO_F32_ADD = 1, GO_BF16 = 2, GO_ROW_STATS = 3, GO_ROW_GRAD = 4 };
 
-// A bf16 operand: a row-major {outer, rows, inner} array (inner contiguous).
+// What the softmax epilogues take: the product's row m is the logits l of token m over the
+// vocabulary's entries [v0, v0 + cols).
+//   GO_ROW_STATS: part[2 (v0 + n) / 256 + half][m] = (max l, sum exp(l - max)) over each 128 columns, and
+//                 target_logit[m] = l at the token's target, where it lies here
+//   GO_ROW_GRAD : out (bf16) = (exp(l - lse[m]) - [the target]) gloss[m]; 0 in rows left out
+// A token takes part when its target is not `ignore` and lies in [0, V).
+struct Softmax {
+  const int64_t* targets;
+  int64_t ignore;
+  int V, v0, cols;
+  float2* part;
+  float* target_logit;
+  const float* lse;
+  const float* gloss;
+};
+
+// A bf16 operand: a row-major {outer, rows, inner} array (inner contiguous), its rows `ld`
+// elements apart (0: inner).
 struct Operand {
   const void* base;
-  uint64_t inner, rows, outer;
+  uint64_t inner, rows, outer, ld;
 };
 
 struct Args {
@@ -54,6 +72,7 @@ struct Args {
   int rows;              // Rows
   int ksplit;            // PLAIN: K in this many slices (0 or 1: one), slice s written at out + s * osz
   int* status;           // device status word (timeouts)
+  Softmax softmax;       // GO_ROW_STATS, GO_ROW_GRAD
   int chunk_base;        // CHUNK_K: chunk i's matrices go to index i - chunk_base of out
 };
 

@@ -1,10 +1,14 @@
 // Softmax cross entropy of a linear head in pieces of the vocabulary
 // (ipttt_xent_forward, ipttt_xent_backward).
 //
-// Mathematics: the logits l = H W^T of a piece are formed, folded into each row's
-// running maximum m and sum s = sum exp(l - m), and dropped; lse = m + log s and
-// loss = lse - l[target].  Backward: the piece's logits again, p = (exp(l - lse) -
+// Mathematics: each row's logits l = H W^T are folded into maxima m and sums s = sum
+// exp(l - m) as they are formed, and dropped; lse = m + log s and loss = lse - l[target].
+// Backward, by pieces of the vocabulary: the piece's logits again, p = (exp(l - lse) -
 // onehot) gloss, then gH += p W_piece and gW_piece = p^T H.
+// bf16: tensor-core GEMMs (gemm.cu) whose epilogues do the softmax's part on the
+// accumulators: the forward's leaves (m, s) for each 128 columns of a row, the
+// backward's writes p in bf16.  Bound by the tensor cores: 2 N V d operations forwards,
+// 6 N V d backwards (2 N V d of them to form the logits again).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -150,8 +154,19 @@ __device__ __forceinline__ float2 block_merge(float2 v, float2* sh) {
   return v;
 }
 
-// One block a row: the piece's logits into the row's running maximum and sum, and
-// its target's logit.  The last piece writes lse and loss.
+// A row's lse, and its loss where it takes part.
+__device__ __forceinline__ void finish_row(int n, float2 v, float target_logit, int V, const int64_t* targets, int64_t ignore,
+                                           float* loss, float* lse, int* status) {
+  const int64_t t = targets[n];
+  const float s = v.x + logf(v.y);
+  lse[n] = s;
+  const bool out = t < 0 || t >= V;
+  if (out && t != ignore) set_status(status, IPTTT_ERR_ARG);
+  loss[n] = out || t == ignore ? 0.0f : s - target_logit;
+}
+
+// fp32: one block a row: the piece's logits into the row's running maximum and sum, and its
+// target's logit.  The last piece writes lse and loss.
 __global__ void __launch_bounds__(kThreads) k_row_stats(const float* l, long long ld, int v0, int cols, int V, int last,
                                                       const int64_t* targets, int64_t ignore, float2* run, float* tl,
                                                       float* loss, float* lse, int* status) {
@@ -166,17 +181,34 @@ __global__ void __launch_bounds__(kThreads) k_row_stats(const float* l, long lon
   run[n] = v;
   const int64_t t = targets[n];
   if (t >= v0 && t < v0 + cols) tl[n] = x[t - v0];
-  if (!last) return;
-  const float s = v.x + logf(v.y);
-  lse[n] = s;
-  const bool out = t < 0 || t >= V;
-  if (out && t != ignore) set_status(status, IPTTT_ERR_ARG);
-  loss[n] = out || t == ignore ? 0.0f : s - tl[n];
+  if (last) finish_row(n, v, tl[n], V, targets, ignore, loss, lse, status);
 }
 
-// p = (exp(l - lse) - onehot) gloss for the piece's columns; 0 in the padding.
-template <typename T>
-__global__ void __launch_bounds__(kThreads) k_row_grad(const float* l, T* p, long long ld, int v0, int cols, int padded, int V,
+// bf16: the GEMM's (maximum, sum) of every 128 columns, part[parts][N], into lse and loss.
+// 32 rows a block, 8 threads a row.
+__global__ void __launch_bounds__(kThreads) k_row_join(const float2* part, int parts, int N, int V, const int64_t* targets,
+                                                     int64_t ignore, const float* tl, float* loss, float* lse,
+                                                     int* status) {
+  __shared__ float2 sh[8][32];
+  const int n = blockIdx.x * 32 + threadIdx.x % 32, k = threadIdx.x / 32;
+  float2 v = make_float2(-INFINITY, 0.0f);
+  if (n < N)
+    for (int i = k; i < parts; i += 8) v = merge(v, part[(long long)i * N + n]);
+  sh[k][threadIdx.x % 32] = v;
+  __syncthreads();
+  if (k != 0 || n >= N) return;
+  for (int i = 1; i < 8; ++i) v = merge(v, sh[i][threadIdx.x]);
+  finish_row(n, v, tl[n], V, targets, ignore, loss, lse, status);
+}
+
+// Reports targets that are neither in the vocabulary nor the one to leave out.
+__global__ void k_check_targets(const int64_t* targets, int N, int V, int64_t ignore, int* status) {
+  const int n = blockIdx.x * blockDim.x + threadIdx.x;
+  if (n < N && (targets[n] < 0 || targets[n] >= V) && targets[n] != ignore) set_status(status, IPTTT_ERR_ARG);
+}
+
+// fp32: p = (exp(l - lse) - onehot) gloss for the piece's columns; 0 in the padding.
+__global__ void __launch_bounds__(kThreads) k_row_grad(float* l, long long ld, int v0, int cols, int padded, int V,
                                                      const int64_t* targets, int64_t ignore, const float* lse,
                                                      const float* gloss, int* status) {
   const int n = blockIdx.x;
@@ -188,7 +220,7 @@ __global__ void __launch_bounds__(kThreads) k_row_grad(const float* l, T* p, lon
   for (int i = threadIdx.x; i < padded; i += kThreads) {
     float v = 0.0f;
     if (on && i < cols) v = (expf(l[(long long)n * ld + i] - s) - (t - v0 == i ? 1.0f : 0.0f)) * g;
-    p[(long long)n * ld + i] = from_f<T>(v);
+    l[(long long)n * ld + i] = v;
   }
 }
 
@@ -206,7 +238,7 @@ __global__ void __launch_bounds__(kThreads) k_sum_slices(const float* part, T* o
 
 size_t al256(size_t x) { return (x + 255) & ~size_t(255); }
 
-constexpr size_t kPieceBytes = size_t(512) << 20;  // of a piece's logits and p
+constexpr size_t kPieceBytes = size_t(256) << 20;  // of a piece's p (fp32: of its logits, p in their place)
 
 ipttt_status check(const ipttt_xent_params* p) {
   if (!p) return IPTTT_ERR_ARG;
@@ -220,7 +252,7 @@ ipttt_status check(const ipttt_xent_params* p) {
 struct Work {
   int piece;  // vocabulary rows at a time, a multiple of 256
   int slices; // partial sums of gH: slices of a piece's columns
-  size_t logits, p, run, tl, gH, total;
+  size_t p, part, tl, gH, total;  // p: fp32 logits and p, or bf16 p
 };
 
 Work work_of(const ipttt_xent_params& p, bool backward) {
@@ -232,15 +264,15 @@ Work work_of(const ipttt_xent_params& p, bool backward) {
     return o;
   };
   const long long all = ((long long)p.V + 255) / 256 * 256;
-  const long long row = (long long)p.N * 4;
-  w.piece = p.piece ? p.piece : (int)std::max<long long>(256, (long long)(kPieceBytes / row) / 256 * 256);
+  const bool tc = p.dtype == IPTTT_BF16;
+  const long long row = (long long)p.N * (tc ? 2 : 4);
+  w.piece = p.piece ? p.piece : (int)std::max<long long>(256, std::min<long long>(all, kPieceBytes / row / 256 * 256));
   w.piece = (int)std::min<long long>(w.piece, all);
-  w.logits = take((size_t)p.N * w.piece * 4);
+  if (!(tc && !backward)) w.p = take(row * w.piece);
   if (!backward) {
-    w.run = take((size_t)p.N * sizeof(float2));
+    w.part = take((size_t)p.N * sizeof(float2) * (tc ? all / 128 : 1));
     w.tl = take((size_t)p.N * 4);
   } else {
-    w.p = p.dtype == IPTTT_BF16 ? take((size_t)p.N * w.piece * 2) : w.logits;
     // enough slices of K for gH's product to fill the SMs twice, each of at least 256 columns
     const long long tiles = (long long)((p.N + 127) / 128) * ((p.d + 127) / 128);
     w.slices = (int)std::max<long long>(1, std::min<long long>({(296 + tiles - 1) / tiles, w.piece / 256, 32}));
@@ -250,14 +282,16 @@ Work work_of(const ipttt_xent_params& p, bool backward) {
   return w;
 }
 
-// The logits of vocabulary rows [v0, v0 + cols).
+// The logits of vocabulary rows [v0, v0 + cols), fp32.
 cudaError_t logits_of(const ipttt_xent_params& p, const void* H, const void* W, int v0, int cols, float* out, long long ld,
                       cudaStream_t st) {
-  if (p.dtype == IPTTT_F32) {
-    Sgemm g{static_cast<const float*>(H), static_cast<const float*>(W) + (long long)v0 * p.d, out, p.d, p.d, ld, 0,
-            p.N, cols, p.d, 1, 0, 0};
-    return sgemm<true, true>(g, st);
-  }
+  Sgemm g{static_cast<const float*>(H), static_cast<const float*>(W) + (long long)v0 * p.d, out, p.d, p.d, ld, 0,
+          p.N, cols, p.d, 1, 0, 0, 0};
+  return sgemm<true, true>(g, st);
+}
+
+// H W^T over vocabulary rows [v0, v0 + cols), bf16, with a softmax epilogue.
+gemm::Args logits_args(const ipttt_xent_params& p, const void* H, const void* W, const int64_t* targets, int v0, int cols) {
   gemm::Args a{};
   a.A = {H, (uint64_t)p.d, (uint64_t)p.N, 1};
   a.Bop = {static_cast<const __nv_bfloat16*>(W) + (long long)v0 * p.d, (uint64_t)p.d, (uint64_t)cols, 1};
@@ -265,11 +299,13 @@ cudaError_t logits_of(const ipttt_xent_params& p, const void* H, const void* W, 
   a.M = p.N;
   a.N = (cols + 31) / 32 * 32;
   a.K = p.d;
-  a.out_kind = gemm::GO_F32;
-  a.out = out;
-  a.ldo = ld;
+  a.softmax.targets = targets;
+  a.softmax.ignore = p.ignore_index;
+  a.softmax.V = p.V;
+  a.softmax.v0 = v0;
+  a.softmax.cols = cols;
   a.status = device_status();
-  return gemm::run(a, device_sms(), st);
+  return a;
 }
 
 bool aligned(std::initializer_list<const void*> ps, unsigned bytes) {
@@ -280,14 +316,27 @@ bool aligned(std::initializer_list<const void*> ps, unsigned bytes) {
 
 cudaError_t forward(const ipttt_xent_params& p, const Work& w, const void* H, const void* W, const int64_t* targets,
                     float* loss, float* lse, uint8_t* ws, int* launches, cudaStream_t st) {
-  float* l = reinterpret_cast<float*>(ws + w.logits);
+  float2* part = reinterpret_cast<float2*>(ws + w.part);
+  float* tl = reinterpret_cast<float*>(ws + w.tl);
+  if (p.dtype == IPTTT_BF16) {
+    gemm::Args a = logits_args(p, H, W, targets, 0, p.V);
+    a.out_kind = gemm::GO_ROW_STATS;
+    a.softmax.part = part;
+    a.softmax.target_logit = tl;
+    const cudaError_t e = gemm::run(a, device_sms(), st);
+    if (e != cudaSuccess) return e;
+    k_row_join<<<(p.N + 31) / 32, kThreads, 0, st>>>(part, (p.V + 127) / 128, p.N, p.V, targets, p.ignore_index, tl, loss,
+                                                     lse, device_status());
+    *launches += 2;
+    return cudaGetLastError();
+  }
+  float* l = reinterpret_cast<float*>(ws + w.p);
   for (int v0 = 0; v0 < p.V; v0 += w.piece) {
     const int cols = std::min(w.piece, p.V - v0);
     const cudaError_t e = logits_of(p, H, W, v0, cols, l, w.piece, st);
     if (e != cudaSuccess) return e;
     k_row_stats<<<p.N, kThreads, 0, st>>>(l, w.piece, v0, cols, p.V, v0 + cols == p.V, targets, p.ignore_index,
-                                          reinterpret_cast<float2*>(ws + w.run), reinterpret_cast<float*>(ws + w.tl),
-                                          loss, lse, device_status());
+                                          part, tl, loss, lse, device_status());
     *launches += 2;
   }
   return cudaGetLastError();
@@ -296,65 +345,79 @@ cudaError_t forward(const ipttt_xent_params& p, const Work& w, const void* H, co
 cudaError_t backward(const ipttt_xent_params& p, const Work& w, const void* H, const void* W, const int64_t* targets,
                      const float* lse, const float* gloss, void* gH, void* gW, uint8_t* ws, int* launches,
                      cudaStream_t st) {
-  float* l = reinterpret_cast<float*>(ws + w.logits);
   float* acc = reinterpret_cast<float*>(ws + w.gH);
   const long long nd = (long long)p.N * p.d;
-  int slices = 0, all_slices = 0;
+  const bool tc = p.dtype == IPTTT_BF16;
+  if (tc) {
+    k_check_targets<<<(p.N + kThreads - 1) / kThreads, kThreads, 0, st>>>(targets, p.N, p.V, p.ignore_index,
+                                                                           device_status());
+    ++*launches;
+  }
+  int all_slices = 0;
   for (int v0 = 0; v0 < p.V; v0 += w.piece) {
     const int cols = std::min(w.piece, p.V - v0);
-    slices = std::max(1, std::min(w.slices, cols / 256));
+    const int slices = std::max(1, std::min(w.slices, cols / 256));
     if (v0 == 0) all_slices = slices;  // a shorter last piece adds to the first ones
-    cudaError_t e = logits_of(p, H, W, v0, cols, l, w.piece, st);
-    if (e != cudaSuccess) return e;
-    if (p.dtype == IPTTT_F32) {
-      k_row_grad<<<p.N, kThreads, 0, st>>>(l, l, w.piece, v0, cols, w.piece, p.V, targets, p.ignore_index, lse, gloss,
+    cudaError_t e;
+    if (!tc) {
+      float* l = reinterpret_cast<float*>(ws + w.p);
+      const float* Wf = static_cast<const float*>(W) + (long long)v0 * p.d;
+      e = logits_of(p, H, W, v0, cols, l, w.piece, st);
+      if (e != cudaSuccess) return e;
+      k_row_grad<<<p.N, kThreads, 0, st>>>(l, w.piece, v0, cols, w.piece, p.V, targets, p.ignore_index, lse, gloss,
                                            device_status());
-      Sgemm a{l, static_cast<const float*>(W) + (long long)v0 * p.d, acc, w.piece, p.d, p.d, nd,
-              p.N, p.d, cols, slices, 0, p.d, v0 > 0};
       // p's columns past the vocabulary are zero, and W's rows past it are not read
+      Sgemm a{l, Wf, acc, w.piece, p.d, p.d, nd, p.N, p.d, cols, slices, 0, p.d, v0 > 0};
       e = sgemm<true, false>(a, st);
       if (e != cudaSuccess) return e;
       Sgemm b{l, static_cast<const float*>(H), static_cast<float*>(gW) + (long long)v0 * p.d, w.piece, p.d, p.d, 0,
-              cols, p.d, p.N, 1, w.piece, p.d};
+              cols, p.d, p.N, 1, w.piece, p.d, 0};
       e = sgemm<false, false>(b, st);
       if (e != cudaSuccess) return e;
-    } else {
-      __nv_bfloat16* pb = reinterpret_cast<__nv_bfloat16*>(ws + w.p);
-      k_row_grad<<<p.N, kThreads, 0, st>>>(l, pb, w.piece, v0, cols, w.piece, p.V, targets, p.ignore_index, lse, gloss,
-                                           device_status());
-      gemm::Args a{};
-      a.A = {pb, (uint64_t)w.piece, (uint64_t)p.N, 1};
-      a.Bop = {static_cast<const __nv_bfloat16*>(W) + (long long)v0 * p.d, (uint64_t)p.d, (uint64_t)cols, 1};
-      a.b_mn = 1;
-      a.mode = gemm::GM_PLAIN;
-      a.M = p.N;
-      a.N = p.d;
-      a.K = cols;
-      a.out_kind = v0 > 0 ? gemm::GO_F32_ADD : gemm::GO_F32;
-      a.out = acc;
-      a.ldo = p.d;
-      a.osz = nd;
-      a.ksplit = slices;
-      a.status = device_status();
-      e = gemm::run(a, device_sms(), st);
-      if (e != cudaSuccess) return e;
-      gemm::Args b{};
-      b.A = {pb, (uint64_t)w.piece, (uint64_t)p.N, 1};
-      b.a_mn = 1;
-      b.Bop = {H, (uint64_t)p.d, (uint64_t)p.N, 1};
-      b.b_mn = 1;
-      b.mode = gemm::GM_PLAIN;
-      b.M = cols;
-      b.N = p.d;
-      b.K = p.N;
-      b.out_kind = gemm::GO_BF16;
-      b.out = static_cast<__nv_bfloat16*>(gW) + (long long)v0 * p.d;
-      b.ldo = p.d;
-      b.status = device_status();
-      e = gemm::run(b, device_sms(), st);
-      if (e != cudaSuccess) return e;
+      *launches += 4;
+      continue;
     }
-    *launches += 4;
+    __nv_bfloat16* pb = reinterpret_cast<__nv_bfloat16*>(ws + w.p);
+    gemm::Args l = logits_args(p, H, W, targets, v0, cols);
+    l.out_kind = gemm::GO_ROW_GRAD;
+    l.out = pb;
+    l.ldo = w.piece;
+    l.softmax.lse = lse;
+    l.softmax.gloss = gloss;
+    e = gemm::run(l, device_sms(), st);
+    if (e != cudaSuccess) return e;
+    gemm::Args a{};
+    a.A = {pb, (uint64_t)cols, (uint64_t)p.N, 1, (uint64_t)w.piece};
+    a.Bop = {static_cast<const __nv_bfloat16*>(W) + (long long)v0 * p.d, (uint64_t)p.d, (uint64_t)cols, 1};
+    a.b_mn = 1;
+    a.mode = gemm::GM_PLAIN;
+    a.M = p.N;
+    a.N = p.d;
+    a.K = cols;
+    a.out_kind = v0 > 0 ? gemm::GO_F32_ADD : gemm::GO_F32;
+    a.out = acc;
+    a.ldo = p.d;
+    a.osz = nd;
+    a.ksplit = slices;
+    a.status = device_status();
+    e = gemm::run(a, device_sms(), st);
+    if (e != cudaSuccess) return e;
+    gemm::Args b{};
+    b.A = {pb, (uint64_t)cols, (uint64_t)p.N, 1, (uint64_t)w.piece};
+    b.a_mn = 1;
+    b.Bop = {H, (uint64_t)p.d, (uint64_t)p.N, 1};
+    b.b_mn = 1;
+    b.mode = gemm::GM_PLAIN;
+    b.M = cols;
+    b.N = p.d;
+    b.K = p.N;
+    b.out_kind = gemm::GO_BF16;
+    b.out = static_cast<__nv_bfloat16*>(gW) + (long long)v0 * p.d;
+    b.ldo = p.d;
+    b.status = device_status();
+    e = gemm::run(b, device_sms(), st);
+    if (e != cudaSuccess) return e;
+    *launches += 3;
   }
   const unsigned grid = (unsigned)std::min<long long>((nd + kThreads - 1) / kThreads, 148 * 16);
   if (p.dtype == IPTTT_F32) k_sum_slices<<<grid, kThreads, 0, st>>>(acc, static_cast<float*>(gH), nd, all_slices);
