@@ -5,15 +5,18 @@
 // z = xh w; each pair of z's first R elements turns by position * inv_freq.  Backward:
 // gz = the pairs of gy turned back, gw = sum gz xh, gx = r (gz w - xh mean(gz w xh)).
 //
-// Bound by HBM: 16 bytes in and 16 out per 8 bf16 elements, some 100 instructions.
-// Layout: a lane holds 8 elements of a vector as two quads, chosen so that both
-// halves of a pair lie in the same lane: elements 4l.. and R/2 + 4l.. (pairs
-// (i, i + R/2)), or 8l..8l+7 (pairs (2i, 2i+1)); lanes from R/8 on hold the elements
-// that do not turn, 8 in a row.  So the rotation needs no exchange between lanes,
-// and the norm one reduction over the 8, 16 or 32 lanes of a vector.  A block takes
-// a few tokens with all their heads, so that the sines and cosines (one per
-// token and pair: angle reduced to a turn in 64 bits, sincospif of the rest)
-// are computed once and shared by the heads through shared memory.
+// Bound by HBM (each element read and written once) as long as the instructions keep up: a first
+// form with 8 elements a lane took 256 instructions for 512 bytes in and out of a warp, and
+// ran at the rate those issue (172 us for 32768 tokens of 32 + 8 heads of 128, bf16, where
+// the bytes take 103).  So a lane holds 16 elements of a vector where the widths allow
+// (8 elsewhere), in two strips chosen so that both halves of every pair lie in the same
+// lane: the rotation needs no exchange between lanes, the norm one sum over the 4 to
+// 32 lanes of a vector, and the arithmetic goes two elements an instruction.  Strips: elements
+// from E/2 l and from R/2 + E/2 l on (pairs (i, i + R/2)), or E l.. and E l + E/2.. (pairs
+// (2i, 2i+1), and elements that do not turn).  A block takes up to four tokens with
+// all their heads; a group of lanes stays with one token, whose sines and cosines
+// (angle reduced to a turn in 64 bits, sincospif of the rest) are computed once for
+// all heads and then stay in registers.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -42,40 +45,128 @@ struct QkArgs {
   float eps;
 };
 
-// Four consecutive elements as fp32.
-__device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
-__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
-  const uint2 v = *reinterpret_cast<const uint2*>(p);
-  const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&v.x));
-  const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&v.y));
-  return make_float4(a.x, a.y, b.x, b.y);
+// Two fp32 numbers in one register pair, and operations on both at once.
+__device__ __forceinline__ uint64_t two(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
 }
-__device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
-__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
-  const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
-  uint2 u;
-  u.x = *reinterpret_cast<const uint32_t*>(&a);
-  u.y = *reinterpret_cast<const uint32_t*>(&b);
-  *reinterpret_cast<uint2*>(p) = u;
+__device__ __forceinline__ float2 apart(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ float sum2(uint64_t v) {
+  const float2 f = apart(v);
+  return f.x + f.y;
 }
 
-__device__ __forceinline__ float dot4(float4 a, float4 b) { return a.x * b.x + a.y * b.y + a.z * b.z + a.w * b.w; }
-__device__ __forceinline__ float4 mul4(float4 a, float4 b) {
-  return make_float4(a.x * b.x, a.y * b.y, a.z * b.z, a.w * b.w);
-}
-__device__ __forceinline__ float4 scale4(float4 a, float s) { return make_float4(a.x * s, a.y * s, a.z * s, a.w * s); }
-
-// Turns the four pairs held in (a, b) by the angles whose cosines and sines are c and s.
-__device__ __forceinline__ void turn(float4& a, float4& b, float4 c, float4 s, bool interleaved) {
-  const float4 x = a, y = b;
-  if (interleaved) {  // pairs (x.x, x.y), (x.z, x.w), (y.x, y.y), (y.z, y.w)
-    a = make_float4(x.x * c.x - x.y * s.x, x.y * c.x + x.x * s.x, x.z * c.y - x.w * s.y, x.w * c.y + x.z * s.y);
-    b = make_float4(y.x * c.z - y.y * s.z, y.y * c.z + y.x * s.z, y.z * c.w - y.w * s.w, y.w * c.w + y.z * s.w);
-  } else {
-    a = make_float4(x.x * c.x - y.x * s.x, x.y * c.y - y.y * s.y, x.z * c.z - y.z * s.z, x.w * c.w - y.w * s.w);
-    b = make_float4(y.x * c.x + x.x * s.x, y.y * c.y + x.y * s.y, y.z * c.z + x.z * s.z, y.w * c.w + x.w * s.w);
+// N elements (4 or 8) as they lie in memory, as pairs of fp32, and back.
+template <typename T, int N> struct Strip;
+template <int N> struct Strip<float, N> {
+  float4 v[N / 4];
+  __device__ __forceinline__ void load(const float* p) {
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) v[i] = reinterpret_cast<const float4*>(p)[i];
   }
-}
+  __device__ __forceinline__ void unpack(uint64_t* x) const {
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
+      x[2 * i] = two(v[i].x, v[i].y);
+      x[2 * i + 1] = two(v[i].z, v[i].w);
+    }
+  }
+  static __device__ __forceinline__ void store(float* p, const uint64_t* x) {
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
+      const float2 a = apart(x[2 * i]), b = apart(x[2 * i + 1]);
+      reinterpret_cast<float4*>(p)[i] = make_float4(a.x, a.y, b.x, b.y);
+    }
+  }
+};
+template <int N> struct Strip<__nv_bfloat16, N> {
+  uint32_t v[N / 2];
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+    if constexpr (N == 8) *reinterpret_cast<uint4*>(v) = *reinterpret_cast<const uint4*>(p);
+    else *reinterpret_cast<uint2*>(v) = *reinterpret_cast<const uint2*>(p);
+  }
+  __device__ __forceinline__ void unpack(uint64_t* x) const {
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) x[i] = two(__uint_as_float(v[i] << 16), __uint_as_float(v[i] & 0xffff0000u));
+  }
+  static __device__ __forceinline__ void store(__nv_bfloat16* p, const uint64_t* x) {
+    uint32_t w[N / 2];
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+      const float2 f = apart(x[i]);
+      const __nv_bfloat162 b = __floats2bfloat162_rn(f.x, f.y);
+      w[i] = *reinterpret_cast<const uint32_t*>(&b);
+    }
+    if constexpr (N == 8) *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(w);
+    else *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(w);
+  }
+};
+
+// A lane's E elements of a vector: two strips of E/2.
+template <typename T, int E> struct Piece {
+  Strip<T, E / 2> a, b;
+  __device__ __forceinline__ void load(const T* p, int o0, int o1) {
+    a.load(p + o0);
+    b.load(p + o1);
+  }
+  __device__ __forceinline__ void unpack(uint64_t* x) const {
+    a.unpack(x);
+    b.unpack(x + E / 4);
+  }
+  static __device__ __forceinline__ void store(T* p, int o0, int o1, const uint64_t* x) {
+    Strip<T, E / 2>::store(p + o0, x);
+    Strip<T, E / 2>::store(p + o1, x + E / 4);
+  }
+};
+
+// The cosines and sines of a lane's E/2 pairs (in order), read once for its token.
+template <int E> struct Turn {
+  uint64_t c[E / 4], s[E / 4];
+  __device__ __forceinline__ void read(const float* cs, const float* sn) {
+#pragma unroll
+    for (int i = 0; i < E / 8; ++i) {
+      const float4 x = reinterpret_cast<const float4*>(cs)[i], y = reinterpret_cast<const float4*>(sn)[i];
+      c[2 * i] = two(x.x, x.y);
+      c[2 * i + 1] = two(x.z, x.w);
+      s[2 * i] = two(y.x, y.y);
+      s[2 * i + 1] = two(y.z, y.w);
+    }
+  }
+  // sign 1: by the angle; -1: back
+  __device__ __forceinline__ void apply(uint64_t* x, bool interleaved, float sign) const {
+    const uint64_t plus = two(sign, sign), minus = two(-sign, -sign);
+    if (!interleaved) {  // strip 0 holds the first halves, strip 1 the second
+#pragma unroll
+      for (int i = 0; i < E / 4; ++i) {
+        const uint64_t a = x[i], b = x[E / 4 + i];
+        x[i] = fma2(mul2(b, minus), s[i], mul2(a, c[i]));
+        x[E / 4 + i] = fma2(mul2(a, plus), s[i], mul2(b, c[i]));
+      }
+    } else {  // a pair is one register pair
+#pragma unroll
+      for (int i = 0; i < E / 2; ++i) {
+        const float2 ci = apart(c[i / 2]), si = apart(s[i / 2]), v = apart(x[i]);
+        const float cc = i % 2 ? ci.y : ci.x, ss = (i % 2 ? si.y : si.x) * sign;
+        x[i] = two(v.x * cc - v.y * ss, v.y * cc + v.x * ss);
+      }
+    }
+  }
+};
 
 // The sum over the G lanes of a vector (all lanes of the warp take part).
 template <int G>
@@ -85,19 +176,20 @@ __device__ __forceinline__ float group_sum(float v) {
   return v;
 }
 
-// A lane's two quads within a vector, and its first pair.
+// Where a lane's strips lie within a vector, and its first pair.
 struct LanePlace {
   int o0, o1, pair;
   bool rotates, used;
 };
+template <int E>
 __device__ __forceinline__ LanePlace place_of(const QkArgs& a, int l) {
   LanePlace p;
-  p.used = 8 * l < a.D;
-  p.rotates = 8 * l < a.R;
-  p.pair = 4 * l;
+  p.used = E * l < a.D;
+  p.rotates = E * l < a.R;
+  p.pair = E / 2 * l;
   const bool halves = p.rotates && !a.interleaved;
-  p.o0 = halves ? 4 * l : 8 * l;
-  p.o1 = halves ? a.R / 2 + 4 * l : 8 * l + 4;
+  p.o0 = halves ? E / 2 * l : E * l;
+  p.o1 = halves ? a.R / 2 + E / 2 * l : E * l + E / 2;
   return p;
 }
 
@@ -114,154 +206,170 @@ __device__ __forceinline__ void fill_angles(const QkArgs& a, long long t0, int n
   }
 }
 
-template <typename T, int G>
-__device__ __forceinline__ void forward_heads(const QkArgs& a, const LanePlace& lp, long long t0, int n, int H,
-                                              const T* x, long long ldx, const T* w, T* y, long long ldy,
-                                              const float* cs, const float* sn) {
-  constexpr int kVecs = kThreads / G;  // vectors a block has in hand
-  const float4 zero = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  const float4 w0 = lp.used ? load4(w + lp.o0) : zero, w1 = lp.used ? load4(w + lp.o1) : zero;
-  const int total = n * H;
-  // every lane of a warp runs the same number of steps: the sums need them all
-  for (int v0 = 0; v0 < total; v0 += kVecs) {
-    const int v = v0 + threadIdx.x / G;
-    const bool on = v < total && lp.used;
-    const int t = on ? v / H : 0, h = on ? v % H : 0;
-    float4 x0 = zero, x1 = zero;
-    if (on) {
-      const T* xp = x + (t0 + t) * ldx + (long long)h * a.D;
-      x0 = load4(xp + lp.o0);
-      x1 = load4(xp + lp.o1);
+// The heads of one operand for a group of lanes and its token: heads first, first + step, ...  Every
+// lane of a warp runs the same number of rounds (`rounds` of two heads): the sums need them all.
+template <typename T, int E, int G>
+__device__ __forceinline__ void forward_heads(const QkArgs& a, const LanePlace& lp, const Turn<E>& turn, bool token, int H,
+                                              int first, int step, const T* x, const T* w, T* y) {
+  uint64_t wv[E / 2];
+#pragma unroll
+  for (int i = 0; i < E / 2; ++i) wv[i] = 0ull;
+  if (lp.used) {
+    Piece<T, E> pw;
+    pw.load(w, lp.o0, lp.o1);
+    pw.unpack(wv);
+  }
+  const bool on = token && lp.used;
+  const float inv_d = 1.0f / (float)a.D;
+  for (int h0 = 0; h0 < H; h0 += 2 * step) {
+    Piece<T, E> raw[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int h = h0 + u * step + first;
+      raw[u] = Piece<T, E>{};
+      if (on && h < H) raw[u].load(x + h * a.D, lp.o0, lp.o1);
     }
-    const float r = rsqrtf(group_sum<G>(dot4(x0, x0) + dot4(x1, x1)) / a.D + a.eps);
-    if (!on) continue;
-    float4 y0 = mul4(scale4(x0, r), w0), y1 = mul4(scale4(x1, r), w1);
-    if (lp.rotates) {
-      const float4 c = *reinterpret_cast<const float4*>(cs + t * (kMaxD / 2) + lp.pair);
-      const float4 s = *reinterpret_cast<const float4*>(sn + t * (kMaxD / 2) + lp.pair);
-      turn(y0, y1, c, s, a.interleaved);
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int h = h0 + u * step + first;
+      uint64_t v[E / 2], ss = 0ull;
+      raw[u].unpack(v);
+#pragma unroll
+      for (int i = 0; i < E / 2; ++i) {
+        ss = fma2(v[i], v[i], ss);
+        v[i] = mul2(v[i], wv[i]);
+      }
+      const float r = rsqrtf(group_sum<G>(sum2(ss)) * inv_d + a.eps);
+      const uint64_t r2 = two(r, r);
+      if (lp.rotates) turn.apply(v, a.interleaved, 1.0f);
+#pragma unroll
+      for (int i = 0; i < E / 2; ++i) v[i] = mul2(v[i], r2);
+      if (on && h < H) Piece<T, E>::store(y + h * a.D, lp.o0, lp.o1, v);
     }
-    T* yp = y + (t0 + t) * ldy + (long long)h * a.D;
-    store4(yp + lp.o0, y0);
-    store4(yp + lp.o1, y1);
   }
 }
 
-template <typename T, int G>
-__global__ void __launch_bounds__(kThreads) k_qk_forward(const QkArgs a) {
+template <typename T, int E, int G>
+__global__ void __launch_bounds__(kThreads, 3) k_qk_forward(const QkArgs a) {
+  constexpr int kGroups = kThreads / G;
   __shared__ __align__(16) float cs[kTokens * kMaxD / 2], sn[kTokens * kMaxD / 2];
-  const LanePlace lp = place_of(a, threadIdx.x % G);
+  const LanePlace lp = place_of<E>(a, threadIdx.x % G);
   const long long t0 = (long long)blockIdx.x * a.tile;
   const int n = (int)min((long long)a.tile, a.tokens - t0);
   fill_angles(a, t0, n, cs, sn);
   __syncthreads();
-  forward_heads<T, G>(a, lp, t0, n, a.Hq, static_cast<const T*>(a.q), a.ldq, static_cast<const T*>(a.wq),
-                      static_cast<T*>(a.qo), a.ldqo, cs, sn);
-  forward_heads<T, G>(a, lp, t0, n, a.Hk, static_cast<const T*>(a.k), a.ldk, static_cast<const T*>(a.wk),
-                      static_cast<T*>(a.ko), a.ldko, cs, sn);
+  const int grp = threadIdx.x / G, t = grp % a.tile, first = grp / a.tile, step = kGroups / a.tile;
+  Turn<E> turn{};
+  if (lp.rotates && t < n) turn.read(cs + t * (kMaxD / 2) + lp.pair, sn + t * (kMaxD / 2) + lp.pair);
+  const long long tok = t0 + t;
+  forward_heads<T, E, G>(a, lp, turn, t < n, a.Hq, first, step, static_cast<const T*>(a.q) + tok * a.ldq,
+                         static_cast<const T*>(a.wq), static_cast<T*>(a.qo) + tok * a.ldqo);
+  forward_heads<T, E, G>(a, lp, turn, t < n, a.Hk, first, step, static_cast<const T*>(a.k) + tok * a.ldk,
+                         static_cast<const T*>(a.wk), static_cast<T*>(a.ko) + tok * a.ldko);
 }
 
-// As forward_heads; the lane's share of the weight gradient is added to g0, g1.
-template <typename T, int G>
-__device__ __forceinline__ void backward_heads(const QkArgs& a, const LanePlace& lp, long long t0, int n, int H,
-                                               const T* x, long long ldx, const T* w, const T* gy, long long ldgy,
-                                               T* gx, long long ldgx, const float* cs, const float* sn, float4& g0,
-                                               float4& g1) {
-  constexpr int kVecs = kThreads / G;
-  const float4 zero = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  const float4 w0 = lp.used ? load4(w + lp.o0) : zero, w1 = lp.used ? load4(w + lp.o1) : zero;
-  const int total = n * H;
-  for (int v0 = 0; v0 < total; v0 += kVecs) {
-    const int v = v0 + threadIdx.x / G;
-    const bool on = v < total && lp.used;
-    const int t = on ? v / H : 0, h = on ? v % H : 0;
-    float4 x0 = zero, x1 = zero, z0 = zero, z1 = zero;
-    if (on) {
-      const T* xp = x + (t0 + t) * ldx + (long long)h * a.D;
-      const T* gp = gy + (t0 + t) * ldgy + (long long)h * a.D;
-      x0 = load4(xp + lp.o0);
-      x1 = load4(xp + lp.o1);
-      z0 = load4(gp + lp.o0);
-      z1 = load4(gp + lp.o1);
-      if (lp.rotates) {  // back: the same pairs by the opposite angle
-        const float4 c = *reinterpret_cast<const float4*>(cs + t * (kMaxD / 2) + lp.pair);
-        const float4 s = *reinterpret_cast<const float4*>(sn + t * (kMaxD / 2) + lp.pair);
-        turn(z0, z1, c, scale4(s, -1.0f), a.interleaved);
-      }
+// As forward_heads; the lane's share of the weight gradient is added to gw.
+template <typename T, int E, int G>
+__device__ __forceinline__ void backward_heads(const QkArgs& a, const LanePlace& lp, const Turn<E>& turn, bool token, int H,
+                                               int first, int step, const T* x, const T* w, const T* gy, T* gx,
+                                               uint64_t* gw) {
+  uint64_t wv[E / 2];
+#pragma unroll
+  for (int i = 0; i < E / 2; ++i) wv[i] = 0ull;
+  if (lp.used) {
+    Piece<T, E> pw;
+    pw.load(w, lp.o0, lp.o1);
+    pw.unpack(wv);
+  }
+  const bool on = token && lp.used;
+  const float inv_d = 1.0f / (float)a.D;
+  for (int h0 = 0; h0 < H; h0 += step) {
+    const int h = h0 + first;
+    Piece<T, E> rx{}, rg{};
+    if (on && h < H) {
+      rx.load(x + h * a.D, lp.o0, lp.o1);
+      rg.load(gy + h * a.D, lp.o0, lp.o1);
     }
-    const float4 u0 = mul4(z0, w0), u1 = mul4(z1, w1);
-    const float ss = group_sum<G>(dot4(x0, x0) + dot4(x1, x1));
-    const float ux = group_sum<G>(dot4(u0, x0) + dot4(u1, x1));
-    if (!on) continue;
-    const float r = rsqrtf(ss / a.D + a.eps);
-    x0 = scale4(x0, r);
-    x1 = scale4(x1, r);
-    const float m = ux * r / a.D;  // mean(u xh)
-    T* op = gx + (t0 + t) * ldgx + (long long)h * a.D;
-    store4(op + lp.o0, make_float4(r * (u0.x - x0.x * m), r * (u0.y - x0.y * m), r * (u0.z - x0.z * m),
-                                   r * (u0.w - x0.w * m)));
-    store4(op + lp.o1, make_float4(r * (u1.x - x1.x * m), r * (u1.y - x1.y * m), r * (u1.z - x1.z * m),
-                                   r * (u1.w - x1.w * m)));
-    g0 = make_float4(fmaf(z0.x, x0.x, g0.x), fmaf(z0.y, x0.y, g0.y), fmaf(z0.z, x0.z, g0.z), fmaf(z0.w, x0.w, g0.w));
-    g1 = make_float4(fmaf(z1.x, x1.x, g1.x), fmaf(z1.y, x1.y, g1.y), fmaf(z1.z, x1.z, g1.z), fmaf(z1.w, x1.w, g1.w));
+    uint64_t v[E / 2], z[E / 2], ss = 0ull, ux = 0ull;
+    rx.unpack(v);
+    rg.unpack(z);
+    if (lp.rotates) turn.apply(z, a.interleaved, -1.0f);
+#pragma unroll
+    for (int i = 0; i < E / 2; ++i) {
+      ss = fma2(v[i], v[i], ss);
+      ux = fma2(mul2(z[i], wv[i]), v[i], ux);
+    }
+    const float r = rsqrtf(group_sum<G>(sum2(ss)) * inv_d + a.eps);
+    const float m = group_sum<G>(sum2(ux)) * r * inv_d;  // mean(gz w xh)
+    const uint64_t r2 = two(r, r), m2 = two(-m, -m);
+#pragma unroll
+    for (int i = 0; i < E / 2; ++i) {
+      v[i] = mul2(v[i], r2);
+      gw[i] = fma2(z[i], v[i], gw[i]);
+      z[i] = mul2(fma2(v[i], m2, mul2(z[i], wv[i])), r2);
+    }
+    if (on && h < H) Piece<T, E>::store(gx + h * a.D, lp.o0, lp.o1, z);
   }
 }
 
 // The block's sum of every element's weight gradient, in the order of its groups of lanes.
-template <int G>
-__device__ __forceinline__ void store_parts(const LanePlace& lp, float4 g0, float4 g1, float* sh, float* out, int D) {
-  constexpr int kVecs = kThreads / G;
+template <int E, int G>
+__device__ __forceinline__ void store_parts(const LanePlace& lp, const uint64_t* gw, float* sh, float* out, int D) {
+  constexpr int kGroups = kThreads / G;
   __syncthreads();  // sh's last readers
-  if (lp.used) {
-    float* s = sh + (threadIdx.x / G) * kMaxD;
-    *reinterpret_cast<float4*>(s + lp.o0) = g0;
-    *reinterpret_cast<float4*>(s + lp.o1) = g1;
-  }
+  if (lp.used) Piece<float, E>::store(sh + (threadIdx.x / G) * (G * E), lp.o0, lp.o1, gw);
   __syncthreads();
   for (int e = threadIdx.x; e < D; e += kThreads) {
     float sum = 0.0f;
-    for (int q = 0; q < kVecs; ++q) sum += sh[q * kMaxD + e];
+    for (int q = 0; q < kGroups; ++q) sum += sh[q * (G * E) + e];
     out[e] = sum;
   }
 }
 
-template <typename T, int G>
-__global__ void __launch_bounds__(kThreads) k_qk_backward(const QkArgs a) {
+template <typename T, int E, int G>
+__global__ void __launch_bounds__(kThreads, 2) k_qk_backward(const QkArgs a) {
+  constexpr int kGroups = kThreads / G;
   __shared__ __align__(16) float cs[kTokens * kMaxD / 2], sn[kTokens * kMaxD / 2];
-  extern __shared__ __align__(16) float sh[];  // [kThreads / G][kMaxD]
-  const LanePlace lp = place_of(a, threadIdx.x % G);
-  const float4 zero = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  float4 q0 = zero, q1 = zero, k0 = zero, k1 = zero;
+  __shared__ __align__(16) float sh[kThreads * E];  // [kGroups][G E]
+  const LanePlace lp = place_of<E>(a, threadIdx.x % G);
+  const int grp = threadIdx.x / G, t = grp % a.tile, first = grp / a.tile, step = kGroups / a.tile;
+  uint64_t gq[E / 2] = {}, gk[E / 2] = {};
   const long long tiles = (a.tokens + a.tile - 1) / a.tile;
   for (long long i = blockIdx.x; i < tiles; i += gridDim.x) {
-    const long long t0 = i * a.tile;
+    const long long t0 = i * a.tile, tok = t0 + t;
     const int n = (int)min((long long)a.tile, a.tokens - t0);
     __syncthreads();  // the last tile's angles have been read
     fill_angles(a, t0, n, cs, sn);
     __syncthreads();
-    backward_heads<T, G>(a, lp, t0, n, a.Hq, static_cast<const T*>(a.q), a.ldq, static_cast<const T*>(a.wq),
-                         static_cast<const T*>(a.gqo), a.ldqo, static_cast<T*>(a.qo), a.ldgq, cs, sn, q0, q1);
-    backward_heads<T, G>(a, lp, t0, n, a.Hk, static_cast<const T*>(a.k), a.ldk, static_cast<const T*>(a.wk),
-                         static_cast<const T*>(a.gko), a.ldko, static_cast<T*>(a.ko), a.ldgk, cs, sn, k0, k1);
+    Turn<E> turn{};
+    if (lp.rotates && t < n) turn.read(cs + t * (kMaxD / 2) + lp.pair, sn + t * (kMaxD / 2) + lp.pair);
+    backward_heads<T, E, G>(a, lp, turn, t < n, a.Hq, first, step, static_cast<const T*>(a.q) + tok * a.ldq,
+                            static_cast<const T*>(a.wq), static_cast<const T*>(a.gqo) + tok * a.ldqo,
+                            static_cast<T*>(a.qo) + tok * a.ldgq, gq);
+    backward_heads<T, E, G>(a, lp, turn, t < n, a.Hk, first, step, static_cast<const T*>(a.k) + tok * a.ldk,
+                            static_cast<const T*>(a.wk), static_cast<const T*>(a.gko) + tok * a.ldko,
+                            static_cast<T*>(a.ko) + tok * a.ldgk, gk);
   }
-  store_parts<G>(lp, q0, q1, sh, a.parts + (size_t)blockIdx.x * a.D, a.D);
-  store_parts<G>(lp, k0, k1, sh, a.parts + (size_t)(gridDim.x + blockIdx.x) * a.D, a.D);
+  store_parts<E, G>(lp, gq, sh, a.parts + (size_t)blockIdx.x * a.D, a.D);
+  store_parts<E, G>(lp, gk, sh, a.parts + (size_t)(gridDim.x + blockIdx.x) * a.D, a.D);
 }
 
-// gw[e] = the blocks' partial sums in block order, in 64 bits; one block of 32 x 8
+// gw[e] = the blocks' partial sums, in 64 bits and a fixed order; one block of 32 x 32
 // threads takes 32 elements of gwq (y = 0) or gwk (y = 1).
-__global__ void k_qk_weight_grad(const float* parts, float* gwq, float* gwk, int blocks, int D) {
-  __shared__ double sh[8][32];
+__global__ void __launch_bounds__(1024) k_qk_weight_grad(const float* parts, float* gwq, float* gwk, int blocks, int D) {
+  __shared__ double sh[32][33];
   const int e = blockIdx.x * 32 + threadIdx.x;
   double s = 0.0;
   if (e < D)
-    for (int i = threadIdx.y; i < blocks; i += 8) s += parts[((size_t)blockIdx.y * blocks + i) * D + e];
-  sh[threadIdx.y][threadIdx.x] = s;
+    for (int i = threadIdx.y; i < blocks; i += 32) s += parts[((size_t)blockIdx.y * blocks + i) * D + e];
+  sh[threadIdx.x][threadIdx.y] = s;
   __syncthreads();
-  if (threadIdx.y == 0 && e < D) {
-    for (int q = 1; q < 8; ++q) s += sh[q][threadIdx.x];
-    (blockIdx.y == 0 ? gwq : gwk)[e] = (float)s;
-  }
+  // warp y sums element y
+  s = sh[threadIdx.y][threadIdx.x];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  const int out = blockIdx.x * 32 + threadIdx.y;
+  if (threadIdx.x == 0 && out < D) (blockIdx.y == 0 ? gwq : gwk)[out] = (float)s;
 }
 
 ipttt_status check(const ipttt_qk_params* p) {
@@ -301,30 +409,34 @@ QkArgs args_of(const ipttt_qk_params& p) {
   return a;
 }
 
-int lanes_of(int D) { return D <= 64 ? 8 : D <= 128 ? 16 : 32; }
-
 int grad_blocks(const QkArgs& a) {
   return (int)std::min<long long>(kGradBlocks, (a.tokens + a.tile - 1) / a.tile);
 }
 
-template <typename T>
-cudaError_t launch_forward(const QkArgs& a, cudaStream_t st) {
-  const unsigned grid = (unsigned)((a.tokens + a.tile - 1) / a.tile);
-  switch (lanes_of(a.D)) {
-    case 8: k_qk_forward<T, 8><<<grid, kThreads, 0, st>>>(a); break;
-    case 16: k_qk_forward<T, 16><<<grid, kThreads, 0, st>>>(a); break;
-    default: k_qk_forward<T, 32><<<grid, kThreads, 0, st>>>(a); break;
+struct Forward {
+  template <typename T, int E, int G>
+  static void launch(const QkArgs& a, cudaStream_t st) {
+    k_qk_forward<T, E, G><<<(unsigned)((a.tokens + a.tile - 1) / a.tile), kThreads, 0, st>>>(a);
   }
-  return cudaGetLastError();
-}
+};
+struct Backward {
+  template <typename T, int E, int G>
+  static void launch(const QkArgs& a, cudaStream_t st) {
+    k_qk_backward<T, E, G><<<(unsigned)grad_blocks(a), kThreads, 0, st>>>(a);
+  }
+};
 
-template <typename T>
-cudaError_t launch_backward(const QkArgs& a, cudaStream_t st) {
-  const unsigned grid = (unsigned)grad_blocks(a);
-  switch (lanes_of(a.D)) {
-    case 8: k_qk_backward<T, 8><<<grid, kThreads, (kThreads / 8) * kMaxD * 4, st>>>(a); break;
-    case 16: k_qk_backward<T, 16><<<grid, kThreads, (kThreads / 16) * kMaxD * 4, st>>>(a); break;
-    default: k_qk_backward<T, 32><<<grid, kThreads, (kThreads / 32) * kMaxD * 4, st>>>(a); break;
+// 16 elements a lane where D and R are multiples of 16, else 8; the fewest lanes that hold D.
+template <typename K, typename T>
+cudaError_t launch(const QkArgs& a, cudaStream_t st) {
+  if (a.D % 16 == 0 && a.R % 16 == 0) {
+    if (a.D <= 64) K::template launch<T, 16, 4>(a, st);
+    else if (a.D <= 128) K::template launch<T, 16, 8>(a, st);
+    else K::template launch<T, 16, 16>(a, st);
+  } else {
+    if (a.D <= 64) K::template launch<T, 8, 8>(a, st);
+    else if (a.D <= 128) K::template launch<T, 8, 16>(a, st);
+    else K::template launch<T, 8, 32>(a, st);
   }
   return cudaGetLastError();
 }
@@ -363,7 +475,7 @@ ipttt_status ipttt_qk_norm_rope(const ipttt_qk_params* p, const void* q, const v
   a.qo = q_out;
   a.ko = k_out;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = p->dtype == IPTTT_BF16 ? launch_forward<__nv_bfloat16>(a, st) : launch_forward<float>(a, st);
+  const cudaError_t e = p->dtype == IPTTT_BF16 ? launch<Forward, __nv_bfloat16>(a, st) : launch<Forward, float>(a, st);
   if (e != cudaSuccess) return cuda_fail("qk_norm_rope", e);
   count_launches(1);
   return IPTTT_OK;
@@ -403,9 +515,9 @@ ipttt_status ipttt_qk_norm_rope_backward(const ipttt_qk_params* p, const void* q
   a.ko = gk;
   a.parts = static_cast<float*>(workspace);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  cudaError_t e = p->dtype == IPTTT_BF16 ? launch_backward<__nv_bfloat16>(a, st) : launch_backward<float>(a, st);
+  cudaError_t e = p->dtype == IPTTT_BF16 ? launch<Backward, __nv_bfloat16>(a, st) : launch<Backward, float>(a, st);
   if (e == cudaSuccess) {
-    k_qk_weight_grad<<<dim3((a.D + 31) / 32, 2), dim3(32, 8), 0, st>>>(a.parts, gwq, gwk, grad_blocks(a), a.D);
+    k_qk_weight_grad<<<dim3((a.D + 31) / 32, 2), dim3(32, 32), 0, st>>>(a.parts, gwq, gwk, grad_blocks(a), a.D);
     e = cudaGetLastError();
   }
   if (e != cudaSuccess) return cuda_fail("qk_norm_rope_backward", e);

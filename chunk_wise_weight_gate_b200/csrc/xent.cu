@@ -185,20 +185,24 @@ __global__ void __launch_bounds__(kThreads) k_row_stats(const float* l, long lon
 }
 
 // bf16: the GEMM's (maximum, sum) of every 128 columns, part[parts][N], into lse and loss.
-// 32 rows a block, 8 threads a row.
+// 8 rows a block, 32 threads a row.
 __global__ void __launch_bounds__(kThreads) k_row_join(const float2* part, int parts, int N, int V, const int64_t* targets,
                                                      int64_t ignore, const float* tl, float* loss, float* lse,
                                                      int* status) {
-  __shared__ float2 sh[8][32];
-  const int n = blockIdx.x * 32 + threadIdx.x % 32, k = threadIdx.x / 32;
+  __shared__ float2 sh[8][33];
+  const int r = threadIdx.x % 8, k = threadIdx.x / 8, n = blockIdx.x * 8 + r;
   float2 v = make_float2(-INFINITY, 0.0f);
   if (n < N)
-    for (int i = k; i < parts; i += 8) v = merge(v, part[(long long)i * N + n]);
-  sh[k][threadIdx.x % 32] = v;
+    for (int i = k; i < parts; i += 32) v = merge(v, part[(long long)i * N + n]);
+  sh[r][k] = v;
   __syncthreads();
-  if (k != 0 || n >= N) return;
-  for (int i = 1; i < 8; ++i) v = merge(v, sh[i][threadIdx.x]);
-  finish_row(n, v, tl[n], V, targets, ignore, loss, lse, status);
+  // warp w joins row w
+  const int row = threadIdx.x / 32, at = blockIdx.x * 8 + row;
+  v = sh[row][threadIdx.x % 32];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    v = merge(v, make_float2(__shfl_xor_sync(0xffffffffu, v.x, o), __shfl_xor_sync(0xffffffffu, v.y, o)));
+  if (threadIdx.x % 32 == 0 && at < N) finish_row(at, v, tl[at], V, targets, ignore, loss, lse, status);
 }
 
 // Reports targets that are neither in the vocabulary nor the one to leave out.
@@ -325,7 +329,7 @@ cudaError_t forward(const ipttt_xent_params& p, const Work& w, const void* H, co
     a.softmax.target_logit = tl;
     const cudaError_t e = gemm::run(a, device_sms(), st);
     if (e != cudaSuccess) return e;
-    k_row_join<<<(p.N + 31) / 32, kThreads, 0, st>>>(part, (p.V + 127) / 128, p.N, p.V, targets, p.ignore_index, tl, loss,
+    k_row_join<<<(p.N + 7) / 8, kThreads, 0, st>>>(part, (p.V + 127) / 128, p.N, p.V, targets, p.ignore_index, tl, loss,
                                                      lse, device_status());
     *launches += 2;
     return cudaGetLastError();
