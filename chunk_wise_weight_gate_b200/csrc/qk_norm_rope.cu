@@ -206,34 +206,40 @@ __device__ __forceinline__ void fill_angles(const QkArgs& a, long long t0, int n
   }
 }
 
-// The heads of one operand for a group of lanes and its token: heads first, first + step, ...  Every
-// lane of a warp runs the same number of rounds (`rounds` of two heads): the sums need them all.
-template <typename T, int E, int G>
-__device__ __forceinline__ void forward_heads(const QkArgs& a, const LanePlace& lp, const Turn<E>& turn, bool token, int H,
-                                              int first, int step, const T* x, const T* w, T* y) {
-  uint64_t wv[E / 2];
-#pragma unroll
-  for (int i = 0; i < E / 2; ++i) wv[i] = 0ull;
-  if (lp.used) {
-    Piece<T, E> pw;
-    pw.load(w, lp.o0, lp.o1);
-    pw.unpack(wv);
+// A group of lanes takes the heads first, first + step, ... of its token of one operand.
+template <typename T, int E> struct Heads {
+  const T* x;
+  int H, first, step;
+  bool on;  // the lane holds elements, and the token is there
+  __device__ __forceinline__ void load(Piece<T, E>& raw, const LanePlace& lp, int D, int h0) const {
+    if (on && h0 + first < H) raw.load(x + (h0 + first) * D, lp.o0, lp.o1);
+    else raw = Piece<T, E>{};
   }
-  const bool on = token && lp.used;
+};
+
+template <typename T, int E>
+__device__ __forceinline__ void load_weight(uint64_t* wv, const T* w, const LanePlace& lp) {
+  Piece<T, E> pw{};
+  if (lp.used) pw.load(w, lp.o0, lp.o1);
+  pw.unpack(wv);
+}
+
+// Every lane of a warp runs the same number of rounds: the sums need them all.  raw holds the
+// first two rounds' elements; a round's place is filled again, two rounds ahead, once it
+// has been read.
+template <typename T, int E, int G>
+__device__ __forceinline__ void forward_heads(const QkArgs& a, const LanePlace& lp, const Turn<E>& turn,
+                                              const Heads<T, E>& hd, Piece<T, E> (&raw)[2], const T* w, T* y) {
+  uint64_t wv[E / 2];
+  load_weight<T, E>(wv, w, lp);
   const float inv_d = 1.0f / (float)a.D;
-  for (int h0 = 0; h0 < H; h0 += 2 * step) {
-    Piece<T, E> raw[2];
+  for (int h0 = 0; h0 < hd.H; h0 += 2 * hd.step) {
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      const int h = h0 + u * step + first;
-      raw[u] = Piece<T, E>{};
-      if (on && h < H) raw[u].load(x + h * a.D, lp.o0, lp.o1);
-    }
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int h = h0 + u * step + first;
+      const int h = h0 + u * hd.step + hd.first;
       uint64_t v[E / 2], ss = 0ull;
       raw[u].unpack(v);
+      hd.load(raw[u], lp, a.D, h0 + (u + 2) * hd.step);
 #pragma unroll
       for (int i = 0; i < E / 2; ++i) {
         ss = fma2(v[i], v[i], ss);
@@ -244,7 +250,7 @@ __device__ __forceinline__ void forward_heads(const QkArgs& a, const LanePlace& 
       if (lp.rotates) turn.apply(v, a.interleaved, 1.0f);
 #pragma unroll
       for (int i = 0; i < E / 2; ++i) v[i] = mul2(v[i], r2);
-      if (on && h < H) Piece<T, E>::store(y + h * a.D, lp.o0, lp.o1, v);
+      if (hd.on && h < hd.H) Piece<T, E>::store(y + h * a.D, lp.o0, lp.o1, v);
     }
   }
 }
@@ -256,43 +262,42 @@ __global__ void __launch_bounds__(kThreads, 3) k_qk_forward(const QkArgs a) {
   const LanePlace lp = place_of<E>(a, threadIdx.x % G);
   const long long t0 = (long long)blockIdx.x * a.tile;
   const int n = (int)min((long long)a.tile, a.tokens - t0);
-  fill_angles(a, t0, n, cs, sn);
-  __syncthreads();
   const int grp = threadIdx.x / G, t = grp % a.tile, first = grp / a.tile, step = kGroups / a.tile;
+  const long long tok = t0 + t;
+  const bool on = t < n && lp.used;
+  const Heads<T, E> hq{static_cast<const T*>(a.q) + tok * a.ldq, a.Hq, first, step, on};
+  const Heads<T, E> hk{static_cast<const T*>(a.k) + tok * a.ldk, a.Hk, first, step, on};
+  Piece<T, E> raw[2];
+  hq.load(raw[0], lp, a.D, 0);
+  hq.load(raw[1], lp, a.D, step);
+  fill_angles(a, t0, n, cs, sn);  // while the first elements are on their way
+  __syncthreads();
   Turn<E> turn{};
   if (lp.rotates && t < n) turn.read(cs + t * (kMaxD / 2) + lp.pair, sn + t * (kMaxD / 2) + lp.pair);
-  const long long tok = t0 + t;
-  forward_heads<T, E, G>(a, lp, turn, t < n, a.Hq, first, step, static_cast<const T*>(a.q) + tok * a.ldq,
-                         static_cast<const T*>(a.wq), static_cast<T*>(a.qo) + tok * a.ldqo);
-  forward_heads<T, E, G>(a, lp, turn, t < n, a.Hk, first, step, static_cast<const T*>(a.k) + tok * a.ldk,
-                         static_cast<const T*>(a.wk), static_cast<T*>(a.ko) + tok * a.ldko);
+  forward_heads<T, E, G>(a, lp, turn, hq, raw, static_cast<const T*>(a.wq), static_cast<T*>(a.qo) + tok * a.ldqo);
+  hk.load(raw[0], lp, a.D, 0);
+  hk.load(raw[1], lp, a.D, step);
+  forward_heads<T, E, G>(a, lp, turn, hk, raw, static_cast<const T*>(a.wk), static_cast<T*>(a.ko) + tok * a.ldko);
 }
 
-// As forward_heads; the lane's share of the weight gradient is added to gw.
+// As forward_heads, a round of x and gy ahead; the lane's share of the weight gradient is added to gw.
 template <typename T, int E, int G>
-__device__ __forceinline__ void backward_heads(const QkArgs& a, const LanePlace& lp, const Turn<E>& turn, bool token, int H,
-                                               int first, int step, const T* x, const T* w, const T* gy, T* gx,
+__device__ __forceinline__ void backward_heads(const QkArgs& a, const LanePlace& lp, const Turn<E>& turn,
+                                               const Heads<T, E>& hx, const Heads<T, E>& hg, const T* w, T* gx,
                                                uint64_t* gw) {
   uint64_t wv[E / 2];
-#pragma unroll
-  for (int i = 0; i < E / 2; ++i) wv[i] = 0ull;
-  if (lp.used) {
-    Piece<T, E> pw;
-    pw.load(w, lp.o0, lp.o1);
-    pw.unpack(wv);
-  }
-  const bool on = token && lp.used;
+  load_weight<T, E>(wv, w, lp);
   const float inv_d = 1.0f / (float)a.D;
-  for (int h0 = 0; h0 < H; h0 += step) {
-    const int h = h0 + first;
-    Piece<T, E> rx{}, rg{};
-    if (on && h < H) {
-      rx.load(x + h * a.D, lp.o0, lp.o1);
-      rg.load(gy + h * a.D, lp.o0, lp.o1);
-    }
+  Piece<T, E> rx, rg;
+  hx.load(rx, lp, a.D, 0);
+  hg.load(rg, lp, a.D, 0);
+  for (int h0 = 0; h0 < hx.H; h0 += hx.step) {
+    const int h = h0 + hx.first;
     uint64_t v[E / 2], z[E / 2], ss = 0ull, ux = 0ull;
     rx.unpack(v);
     rg.unpack(z);
+    hx.load(rx, lp, a.D, h0 + hx.step);
+    hg.load(rg, lp, a.D, h0 + hx.step);
     if (lp.rotates) turn.apply(z, a.interleaved, -1.0f);
 #pragma unroll
     for (int i = 0; i < E / 2; ++i) {
@@ -308,7 +313,7 @@ __device__ __forceinline__ void backward_heads(const QkArgs& a, const LanePlace&
       gw[i] = fma2(z[i], v[i], gw[i]);
       z[i] = mul2(fma2(v[i], m2, mul2(z[i], wv[i])), r2);
     }
-    if (on && h < H) Piece<T, E>::store(gx + h * a.D, lp.o0, lp.o1, z);
+    if (hx.on && h < hx.H) Piece<T, E>::store(gx + h * a.D, lp.o0, lp.o1, z);
   }
 }
 
@@ -343,12 +348,13 @@ __global__ void __launch_bounds__(kThreads, 2) k_qk_backward(const QkArgs a) {
     __syncthreads();
     Turn<E> turn{};
     if (lp.rotates && t < n) turn.read(cs + t * (kMaxD / 2) + lp.pair, sn + t * (kMaxD / 2) + lp.pair);
-    backward_heads<T, E, G>(a, lp, turn, t < n, a.Hq, first, step, static_cast<const T*>(a.q) + tok * a.ldq,
-                            static_cast<const T*>(a.wq), static_cast<const T*>(a.gqo) + tok * a.ldqo,
-                            static_cast<T*>(a.qo) + tok * a.ldgq, gq);
-    backward_heads<T, E, G>(a, lp, turn, t < n, a.Hk, first, step, static_cast<const T*>(a.k) + tok * a.ldk,
-                            static_cast<const T*>(a.wk), static_cast<const T*>(a.gko) + tok * a.ldko,
-                            static_cast<T*>(a.ko) + tok * a.ldgk, gk);
+    const bool on = t < n && lp.used;
+    const Heads<T, E> q{static_cast<const T*>(a.q) + tok * a.ldq, a.Hq, first, step, on};
+    const Heads<T, E> k{static_cast<const T*>(a.k) + tok * a.ldk, a.Hk, first, step, on};
+    const Heads<T, E> gqo{static_cast<const T*>(a.gqo) + tok * a.ldqo, a.Hq, first, step, on};
+    const Heads<T, E> gko{static_cast<const T*>(a.gko) + tok * a.ldko, a.Hk, first, step, on};
+    backward_heads<T, E, G>(a, lp, turn, q, gqo, static_cast<const T*>(a.wq), static_cast<T*>(a.qo) + tok * a.ldgq, gq);
+    backward_heads<T, E, G>(a, lp, turn, k, gko, static_cast<const T*>(a.wk), static_cast<T*>(a.ko) + tok * a.ldgk, gk);
   }
   store_parts<E, G>(lp, gq, sh, a.parts + (size_t)blockIdx.x * a.D, a.D);
   store_parts<E, G>(lp, gk, sh, a.parts + (size_t)(gridDim.x + blockIdx.x) * a.D, a.D);
@@ -404,8 +410,8 @@ QkArgs args_of(const ipttt_qk_params& p) {
   a.R = p.R;
   a.interleaved = p.interleaved;
   a.eps = p.eps;
-  // four tokens share a block's angle pass, unless that leaves SMs without a block
-  a.tile = a.tokens >= (long long)kTokens * kGradBlocks ? kTokens : 1;
+  // four tokens a block, unless that leaves SMs without one
+  a.tile = a.tokens >= (long long)kTokens * 148 ? kTokens : 1;
   return a;
 }
 
