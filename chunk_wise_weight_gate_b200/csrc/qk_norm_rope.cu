@@ -10,10 +10,11 @@
 // ran at the rate those issue (172 us for 32768 tokens of 32 + 8 heads of 128, bf16, where
 // the bytes take 103).  So a lane holds 16 elements of a vector where the widths allow
 // (8 elsewhere), in two strips chosen so that both halves of every pair lie in the same
-// lane: the rotation needs no exchange between lanes, the norm one sum over the 4 to
-// 32 lanes of a vector, and the arithmetic goes two elements an instruction.  Strips: elements
+// lane: the rotation needs no exchange between lanes, and the norm one sum over the 4 to
+// 32 lanes of a vector.  (Arithmetic two elements an instruction took more instructions, not
+// fewer: pairing registers up costs moves.)  Strips: elements
 // from E/2 l and from R/2 + E/2 l on (pairs (i, i + R/2)), or E l.. and E l + E/2.. (pairs
-// (2i, 2i+1), and elements that do not turn).  A block takes up to four tokens with
+// (2i, 2i+1), and elements that do not turn).  A block takes up to eight tokens with
 // all their heads; a group of lanes stays with one token, whose sines and cosines
 // (angle reduced to a turn in 64 bits, sincospif of the rest) are computed once for
 // all heads and then stay in registers.
@@ -29,9 +30,9 @@ namespace ipttt {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kTokens = 4;        // tokens of a tile (1 where there are few)
+constexpr int kTokens = 8;        // tokens of a tile (1 where there are few)
 constexpr int kMaxD = 256;
-constexpr int kGradBlocks = 592;  // most blocks (= partial weight gradients) of the backward: 4 per SM
+constexpr int kForwardBlocks = 444, kBackwardBlocks = 296;  // most blocks: 3 and 2 per SM, as their registers allow
 
 struct QkArgs {
   const void *q, *k, *wq, *wk, *gqo, *gko;
@@ -41,37 +42,12 @@ struct QkArgs {
   long long ldq, ldk, ldqo, ldko, ldgq, ldgk;
   float* parts;                  // backward: [2][blocks][D]
   long long tokens;
-  int Hq, Hk, D, R, interleaved, tile;
-  float eps;
+  int Hq, Hk, D, R, interleaved;
+  int shift;                     // tiles of 1 << shift tokens
+  float eps, inv_d;
 };
 
-// Two fp32 numbers in one register pair, and operations on both at once.
-__device__ __forceinline__ uint64_t two(float lo, float hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ float2 apart(uint64_t v) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-  return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-__device__ __forceinline__ float sum2(uint64_t v) {
-  const float2 f = apart(v);
-  return f.x + f.y;
-}
-
-// N elements (4 or 8) as they lie in memory, as pairs of fp32, and back.
+// N elements (4 or 8) as they lie in memory, as fp32, and back.
 template <typename T, int N> struct Strip;
 template <int N> struct Strip<float, N> {
   float4 v[N / 4];
@@ -79,19 +55,19 @@ template <int N> struct Strip<float, N> {
 #pragma unroll
     for (int i = 0; i < N / 4; ++i) v[i] = reinterpret_cast<const float4*>(p)[i];
   }
-  __device__ __forceinline__ void unpack(uint64_t* x) const {
+  __device__ __forceinline__ void unpack(float* x) const {
 #pragma unroll
     for (int i = 0; i < N / 4; ++i) {
-      x[2 * i] = two(v[i].x, v[i].y);
-      x[2 * i + 1] = two(v[i].z, v[i].w);
+      x[4 * i] = v[i].x;
+      x[4 * i + 1] = v[i].y;
+      x[4 * i + 2] = v[i].z;
+      x[4 * i + 3] = v[i].w;
     }
   }
-  static __device__ __forceinline__ void store(float* p, const uint64_t* x) {
+  static __device__ __forceinline__ void store(float* p, const float* x) {
 #pragma unroll
-    for (int i = 0; i < N / 4; ++i) {
-      const float2 a = apart(x[2 * i]), b = apart(x[2 * i + 1]);
-      reinterpret_cast<float4*>(p)[i] = make_float4(a.x, a.y, b.x, b.y);
-    }
+    for (int i = 0; i < N / 4; ++i)
+      reinterpret_cast<float4*>(p)[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
   }
 };
 template <int N> struct Strip<__nv_bfloat16, N> {
@@ -100,16 +76,18 @@ template <int N> struct Strip<__nv_bfloat16, N> {
     if constexpr (N == 8) *reinterpret_cast<uint4*>(v) = *reinterpret_cast<const uint4*>(p);
     else *reinterpret_cast<uint2*>(v) = *reinterpret_cast<const uint2*>(p);
   }
-  __device__ __forceinline__ void unpack(uint64_t* x) const {
+  __device__ __forceinline__ void unpack(float* x) const {
 #pragma unroll
-    for (int i = 0; i < N / 2; ++i) x[i] = two(__uint_as_float(v[i] << 16), __uint_as_float(v[i] & 0xffff0000u));
+    for (int i = 0; i < N / 2; ++i) {
+      x[2 * i] = __uint_as_float(v[i] << 16);
+      x[2 * i + 1] = __uint_as_float(v[i] & 0xffff0000u);
+    }
   }
-  static __device__ __forceinline__ void store(__nv_bfloat16* p, const uint64_t* x) {
+  static __device__ __forceinline__ void store(__nv_bfloat16* p, const float* x) {
     uint32_t w[N / 2];
 #pragma unroll
     for (int i = 0; i < N / 2; ++i) {
-      const float2 f = apart(x[i]);
-      const __nv_bfloat162 b = __floats2bfloat162_rn(f.x, f.y);
+      const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
       w[i] = *reinterpret_cast<const uint32_t*>(&b);
     }
     if constexpr (N == 8) *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(w);
@@ -124,45 +102,49 @@ template <typename T, int E> struct Piece {
     a.load(p + o0);
     b.load(p + o1);
   }
-  __device__ __forceinline__ void unpack(uint64_t* x) const {
+  __device__ __forceinline__ void unpack(float* x) const {
     a.unpack(x);
-    b.unpack(x + E / 4);
+    b.unpack(x + E / 2);
   }
-  static __device__ __forceinline__ void store(T* p, int o0, int o1, const uint64_t* x) {
+  static __device__ __forceinline__ void store(T* p, int o0, int o1, const float* x) {
     Strip<T, E / 2>::store(p + o0, x);
-    Strip<T, E / 2>::store(p + o1, x + E / 4);
+    Strip<T, E / 2>::store(p + o1, x + E / 2);
   }
 };
 
-// The cosines and sines of a lane's E/2 pairs (in order), read once for its token.
-template <int E> struct Turn {
-  uint64_t c[E / 4], s[E / 4];
+// The cosines and sines of a lane's E/2 pairs (in order), read once for its token; BACK turns the
+// other way.  Lanes whose elements do not turn keep c = 1, s = 0.
+template <int E, bool BACK> struct Turn {
+  float c[E / 2], s[E / 2];
+  __device__ __forceinline__ void none() {
+#pragma unroll
+    for (int i = 0; i < E / 2; ++i) {
+      c[i] = 1.0f;
+      s[i] = 0.0f;
+    }
+  }
   __device__ __forceinline__ void read(const float* cs, const float* sn) {
 #pragma unroll
     for (int i = 0; i < E / 8; ++i) {
-      const float4 x = reinterpret_cast<const float4*>(cs)[i], y = reinterpret_cast<const float4*>(sn)[i];
-      c[2 * i] = two(x.x, x.y);
-      c[2 * i + 1] = two(x.z, x.w);
-      s[2 * i] = two(y.x, y.y);
-      s[2 * i + 1] = two(y.z, y.w);
+      *reinterpret_cast<float4*>(c + 4 * i) = reinterpret_cast<const float4*>(cs)[i];
+      *reinterpret_cast<float4*>(s + 4 * i) = reinterpret_cast<const float4*>(sn)[i];
     }
   }
-  // sign 1: by the angle; -1: back
-  __device__ __forceinline__ void apply(uint64_t* x, bool interleaved, float sign) const {
-    const uint64_t plus = two(sign, sign), minus = two(-sign, -sign);
+  __device__ __forceinline__ void apply(float* x, bool interleaved) const {
+    constexpr float sign = BACK ? -1.0f : 1.0f;
     if (!interleaved) {  // strip 0 holds the first halves, strip 1 the second
 #pragma unroll
-      for (int i = 0; i < E / 4; ++i) {
-        const uint64_t a = x[i], b = x[E / 4 + i];
-        x[i] = fma2(mul2(b, minus), s[i], mul2(a, c[i]));
-        x[E / 4 + i] = fma2(mul2(a, plus), s[i], mul2(b, c[i]));
+      for (int i = 0; i < E / 2; ++i) {
+        const float a = x[i], b = x[E / 2 + i];
+        x[i] = fmaf(-sign * b, s[i], a * c[i]);
+        x[E / 2 + i] = fmaf(sign * a, s[i], b * c[i]);
       }
-    } else {  // a pair is one register pair
+    } else {
 #pragma unroll
       for (int i = 0; i < E / 2; ++i) {
-        const float2 ci = apart(c[i / 2]), si = apart(s[i / 2]), v = apart(x[i]);
-        const float cc = i % 2 ? ci.y : ci.x, ss = (i % 2 ? si.y : si.x) * sign;
-        x[i] = two(v.x * cc - v.y * ss, v.y * cc + v.x * ss);
+        const float a = x[2 * i], b = x[2 * i + 1];
+        x[2 * i] = fmaf(-sign * b, s[i], a * c[i]);
+        x[2 * i + 1] = fmaf(sign * a, s[i], b * c[i]);
       }
     }
   }
@@ -193,32 +175,40 @@ __device__ __forceinline__ LanePlace place_of(const QkArgs& a, int l) {
   return p;
 }
 
-// cos and sin of every (token, pair) of the tile that starts at token t0.
+// cos and sin of every (token, pair) of the tile that starts at token t0.  The turns are reduced in
+// 64 bits whatever the type; bf16 then takes the hardware's sine and cosine (off by 2^-21
+// at most on [-pi, pi], far below its rounding of 2^-8), which with the accurate ones
+// would be a third of all instructions.
+template <typename T>
 __device__ __forceinline__ void fill_angles(const QkArgs& a, long long t0, int n, float* cs, float* sn) {
-  const int half = a.R / 2;
-  for (int i = threadIdx.x; i < n * half; i += kThreads) {
-    const int t = i / half, f = i % half;
-    const double turns = (double)a.pos[t0 + t] * (a.inv_freq[f] * 0.15915494309189533577);  // 1 / (2 pi)
-    float s, c;
-    sincospif(2.0f * (float)(turns - rint(turns)), &s, &c);
-    cs[t * (kMaxD / 2) + f] = c;
-    sn[t * (kMaxD / 2) + f] = s;
+  for (int t = threadIdx.x >> 6; t < n; t += kThreads / 64) {
+    const double pos = (double)a.pos[t0 + t];
+    for (int f = threadIdx.x & 63; f < a.R / 2; f += 64) {
+      const double turns = pos * (a.inv_freq[f] * 0.15915494309189533577);  // 1 / (2 pi)
+      const float part = (float)(turns - rint(turns));
+      float s, c;
+      if constexpr (sizeof(T) == 2) __sincosf(6.283185307179586f * part, &s, &c);
+      else sincospif(2.0f * part, &s, &c);
+      cs[t * (kMaxD / 2) + f] = c;
+      sn[t * (kMaxD / 2) + f] = s;
+    }
   }
 }
 
-// A group of lanes takes the heads first, first + step, ... of its token of one operand.
+// A group of lanes takes the heads first, first + step, ... of its token of one operand.  Lanes that
+// hold no elements keep the zeros they start with; a group past the last head keeps what it
+// has, which goes nowhere.
 template <typename T, int E> struct Heads {
   const T* x;
   int H, first, step;
   bool on;  // the lane holds elements, and the token is there
   __device__ __forceinline__ void load(Piece<T, E>& raw, const LanePlace& lp, int D, int h0) const {
     if (on && h0 + first < H) raw.load(x + (h0 + first) * D, lp.o0, lp.o1);
-    else raw = Piece<T, E>{};
   }
 };
 
 template <typename T, int E>
-__device__ __forceinline__ void load_weight(uint64_t* wv, const T* w, const LanePlace& lp) {
+__device__ __forceinline__ void load_weight(float* wv, const T* w, const LanePlace& lp) {
   Piece<T, E> pw{};
   if (lp.used) pw.load(w, lp.o0, lp.o1);
   pw.unpack(wv);
@@ -228,28 +218,27 @@ __device__ __forceinline__ void load_weight(uint64_t* wv, const T* w, const Lane
 // first two rounds' elements; a round's place is filled again, two rounds ahead, once it
 // has been read.
 template <typename T, int E, int G>
-__device__ __forceinline__ void forward_heads(const QkArgs& a, const LanePlace& lp, const Turn<E>& turn,
+__device__ __forceinline__ void forward_heads(const QkArgs& a, const LanePlace& lp, const Turn<E, false>& turn,
                                               const Heads<T, E>& hd, Piece<T, E> (&raw)[2], const T* w, T* y) {
-  uint64_t wv[E / 2];
+  float wv[E];
   load_weight<T, E>(wv, w, lp);
-  const float inv_d = 1.0f / (float)a.D;
+#pragma unroll 1
   for (int h0 = 0; h0 < hd.H; h0 += 2 * hd.step) {
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const int h = h0 + u * hd.step + hd.first;
-      uint64_t v[E / 2], ss = 0ull;
+      float v[E], ss[2] = {};
       raw[u].unpack(v);
       hd.load(raw[u], lp, a.D, h0 + (u + 2) * hd.step);
 #pragma unroll
-      for (int i = 0; i < E / 2; ++i) {
-        ss = fma2(v[i], v[i], ss);
-        v[i] = mul2(v[i], wv[i]);
+      for (int i = 0; i < E; ++i) {
+        ss[i & 1] = fmaf(v[i], v[i], ss[i & 1]);
+        v[i] *= wv[i];
       }
-      const float r = rsqrtf(group_sum<G>(sum2(ss)) * inv_d + a.eps);
-      const uint64_t r2 = two(r, r);
-      if (lp.rotates) turn.apply(v, a.interleaved, 1.0f);
+      const float r = rsqrtf(group_sum<G>(ss[0] + ss[1]) * a.inv_d + a.eps);
+      turn.apply(v, a.interleaved);
 #pragma unroll
-      for (int i = 0; i < E / 2; ++i) v[i] = mul2(v[i], r2);
+      for (int i = 0; i < E; ++i) v[i] *= r;
       if (hd.on && h < hd.H) Piece<T, E>::store(y + h * a.D, lp.o0, lp.o1, v);
     }
   }
@@ -260,66 +249,70 @@ __global__ void __launch_bounds__(kThreads, 3) k_qk_forward(const QkArgs a) {
   constexpr int kGroups = kThreads / G;
   __shared__ __align__(16) float cs[kTokens * kMaxD / 2], sn[kTokens * kMaxD / 2];
   const LanePlace lp = place_of<E>(a, threadIdx.x % G);
-  const long long t0 = (long long)blockIdx.x * a.tile;
-  const int n = (int)min((long long)a.tile, a.tokens - t0);
-  const int grp = threadIdx.x / G, t = grp % a.tile, first = grp / a.tile, step = kGroups / a.tile;
-  const long long tok = t0 + t;
-  const bool on = t < n && lp.used;
-  const Heads<T, E> hq{static_cast<const T*>(a.q) + tok * a.ldq, a.Hq, first, step, on};
-  const Heads<T, E> hk{static_cast<const T*>(a.k) + tok * a.ldk, a.Hk, first, step, on};
-  Piece<T, E> raw[2];
-  hq.load(raw[0], lp, a.D, 0);
-  hq.load(raw[1], lp, a.D, step);
-  fill_angles(a, t0, n, cs, sn);  // while the first elements are on their way
-  __syncthreads();
-  Turn<E> turn{};
-  if (lp.rotates && t < n) turn.read(cs + t * (kMaxD / 2) + lp.pair, sn + t * (kMaxD / 2) + lp.pair);
-  forward_heads<T, E, G>(a, lp, turn, hq, raw, static_cast<const T*>(a.wq), static_cast<T*>(a.qo) + tok * a.ldqo);
-  hk.load(raw[0], lp, a.D, 0);
-  hk.load(raw[1], lp, a.D, step);
-  forward_heads<T, E, G>(a, lp, turn, hk, raw, static_cast<const T*>(a.wk), static_cast<T*>(a.ko) + tok * a.ldko);
+  const int grp = threadIdx.x / G, t = grp & ((1 << a.shift) - 1), first = grp >> a.shift, step = kGroups >> a.shift;
+  for (long long t0 = (long long)blockIdx.x << a.shift; t0 < a.tokens; t0 += (long long)gridDim.x << a.shift) {
+    const int n = (int)min(1ll << a.shift, a.tokens - t0);
+    const long long tok = t0 + t;
+    const bool on = t < n && lp.used;
+    const Heads<T, E> hq{static_cast<const T*>(a.q) + tok * a.ldq, a.Hq, first, step, on};
+    const Heads<T, E> hk{static_cast<const T*>(a.k) + tok * a.ldk, a.Hk, first, step, on};
+    Piece<T, E> raw[2] = {};
+    hq.load(raw[0], lp, a.D, 0);
+    hq.load(raw[1], lp, a.D, step);
+    __syncthreads();  // the last tile's angles have been read
+    fill_angles<T>(a, t0, n, cs, sn);  // while the first elements are on their way
+    __syncthreads();
+    Turn<E, false> turn;
+    if (lp.rotates && t < n) turn.read(cs + t * (kMaxD / 2) + lp.pair, sn + t * (kMaxD / 2) + lp.pair);
+    else turn.none();
+    forward_heads<T, E, G>(a, lp, turn, hq, raw, static_cast<const T*>(a.wq), static_cast<T*>(a.qo) + tok * a.ldqo);
+    hk.load(raw[0], lp, a.D, 0);
+    hk.load(raw[1], lp, a.D, step);
+    forward_heads<T, E, G>(a, lp, turn, hk, raw, static_cast<const T*>(a.wk), static_cast<T*>(a.ko) + tok * a.ldko);
+  }
 }
 
 // As forward_heads, a round of x and gy ahead; the lane's share of the weight gradient is added to gw.
 template <typename T, int E, int G>
-__device__ __forceinline__ void backward_heads(const QkArgs& a, const LanePlace& lp, const Turn<E>& turn,
+__device__ __forceinline__ void backward_heads(const QkArgs& a, const LanePlace& lp, const Turn<E, true>& turn,
                                                const Heads<T, E>& hx, const Heads<T, E>& hg, const T* w, T* gx,
-                                               uint64_t* gw) {
-  uint64_t wv[E / 2];
+                                               float* gw) {
+  float wv[E];
   load_weight<T, E>(wv, w, lp);
-  const float inv_d = 1.0f / (float)a.D;
-  Piece<T, E> rx, rg;
+  Piece<T, E> rx{}, rg{};
   hx.load(rx, lp, a.D, 0);
   hg.load(rg, lp, a.D, 0);
   for (int h0 = 0; h0 < hx.H; h0 += hx.step) {
     const int h = h0 + hx.first;
-    uint64_t v[E / 2], z[E / 2], ss = 0ull, ux = 0ull;
+    const bool here = hx.on && h < hx.H;
+    float v[E], z[E], ss[2] = {}, ux[2] = {};
     rx.unpack(v);
     rg.unpack(z);
     hx.load(rx, lp, a.D, h0 + hx.step);
     hg.load(rg, lp, a.D, h0 + hx.step);
-    if (lp.rotates) turn.apply(z, a.interleaved, -1.0f);
+    turn.apply(z, a.interleaved);
 #pragma unroll
-    for (int i = 0; i < E / 2; ++i) {
-      ss = fma2(v[i], v[i], ss);
-      ux = fma2(mul2(z[i], wv[i]), v[i], ux);
+    for (int i = 0; i < E; ++i) {
+      ss[i & 1] = fmaf(v[i], v[i], ss[i & 1]);
+      ux[i & 1] = fmaf(z[i] * wv[i], v[i], ux[i & 1]);
     }
-    const float r = rsqrtf(group_sum<G>(sum2(ss)) * inv_d + a.eps);
-    const float m = group_sum<G>(sum2(ux)) * r * inv_d;  // mean(gz w xh)
-    const uint64_t r2 = two(r, r), m2 = two(-m, -m);
+    const float r = rsqrtf(group_sum<G>(ss[0] + ss[1]) * a.inv_d + a.eps);
+    const float m = -group_sum<G>(ux[0] + ux[1]) * r * a.inv_d;  // -mean(gz w xh)
+    if (here) {
 #pragma unroll
-    for (int i = 0; i < E / 2; ++i) {
-      v[i] = mul2(v[i], r2);
-      gw[i] = fma2(z[i], v[i], gw[i]);
-      z[i] = mul2(fma2(v[i], m2, mul2(z[i], wv[i])), r2);
+      for (int i = 0; i < E; ++i) {
+        const float xh = v[i] * r;
+        gw[i] = fmaf(z[i], xh, gw[i]);
+        z[i] = fmaf(xh, m, z[i] * wv[i]) * r;
+      }
+      Piece<T, E>::store(gx + h * a.D, lp.o0, lp.o1, z);
     }
-    if (hx.on && h < hx.H) Piece<T, E>::store(gx + h * a.D, lp.o0, lp.o1, z);
   }
 }
 
 // The block's sum of every element's weight gradient, in the order of its groups of lanes.
 template <int E, int G>
-__device__ __forceinline__ void store_parts(const LanePlace& lp, const uint64_t* gw, float* sh, float* out, int D) {
+__device__ __forceinline__ void store_parts(const LanePlace& lp, const float* gw, float* sh, float* out, int D) {
   constexpr int kGroups = kThreads / G;
   __syncthreads();  // sh's last readers
   if (lp.used) Piece<float, E>::store(sh + (threadIdx.x / G) * (G * E), lp.o0, lp.o1, gw);
@@ -337,17 +330,17 @@ __global__ void __launch_bounds__(kThreads, 2) k_qk_backward(const QkArgs a) {
   __shared__ __align__(16) float cs[kTokens * kMaxD / 2], sn[kTokens * kMaxD / 2];
   __shared__ __align__(16) float sh[kThreads * E];  // [kGroups][G E]
   const LanePlace lp = place_of<E>(a, threadIdx.x % G);
-  const int grp = threadIdx.x / G, t = grp % a.tile, first = grp / a.tile, step = kGroups / a.tile;
-  uint64_t gq[E / 2] = {}, gk[E / 2] = {};
-  const long long tiles = (a.tokens + a.tile - 1) / a.tile;
-  for (long long i = blockIdx.x; i < tiles; i += gridDim.x) {
-    const long long t0 = i * a.tile, tok = t0 + t;
-    const int n = (int)min((long long)a.tile, a.tokens - t0);
+  const int grp = threadIdx.x / G, t = grp & ((1 << a.shift) - 1), first = grp >> a.shift, step = kGroups >> a.shift;
+  float gq[E] = {}, gk[E] = {};
+  for (long long t0 = (long long)blockIdx.x << a.shift; t0 < a.tokens; t0 += (long long)gridDim.x << a.shift) {
+    const long long tok = t0 + t;
+    const int n = (int)min(1ll << a.shift, a.tokens - t0);
     __syncthreads();  // the last tile's angles have been read
-    fill_angles(a, t0, n, cs, sn);
+    fill_angles<T>(a, t0, n, cs, sn);
     __syncthreads();
-    Turn<E> turn{};
+    Turn<E, true> turn;
     if (lp.rotates && t < n) turn.read(cs + t * (kMaxD / 2) + lp.pair, sn + t * (kMaxD / 2) + lp.pair);
+    else turn.none();
     const bool on = t < n && lp.used;
     const Heads<T, E> q{static_cast<const T*>(a.q) + tok * a.ldq, a.Hq, first, step, on};
     const Heads<T, E> k{static_cast<const T*>(a.k) + tok * a.ldk, a.Hk, first, step, on};
@@ -410,19 +403,20 @@ QkArgs args_of(const ipttt_qk_params& p) {
   a.R = p.R;
   a.interleaved = p.interleaved;
   a.eps = p.eps;
-  // four tokens a block, unless that leaves SMs without one
-  a.tile = a.tokens >= (long long)kTokens * 148 ? kTokens : 1;
+  a.inv_d = 1.0f / (float)p.D;
+  // eight tokens a tile, unless that leaves SMs without one
+  a.shift = a.tokens >= (long long)kTokens * 148 ? 3 : 0;
+  static_assert(kTokens == 8, "shift");
   return a;
 }
 
-int grad_blocks(const QkArgs& a) {
-  return (int)std::min<long long>(kGradBlocks, (a.tokens + a.tile - 1) / a.tile);
-}
+long long tiles_of(const QkArgs& a) { return (a.tokens + (1ll << a.shift) - 1) >> a.shift; }
+int grad_blocks(const QkArgs& a) { return (int)std::min<long long>(kBackwardBlocks, tiles_of(a)); }
 
 struct Forward {
   template <typename T, int E, int G>
   static void launch(const QkArgs& a, cudaStream_t st) {
-    k_qk_forward<T, E, G><<<(unsigned)((a.tokens + a.tile - 1) / a.tile), kThreads, 0, st>>>(a);
+    k_qk_forward<T, E, G><<<(unsigned)std::min<long long>(kForwardBlocks, tiles_of(a)), kThreads, 0, st>>>(a);
   }
 };
 struct Backward {
