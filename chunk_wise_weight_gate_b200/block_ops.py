@@ -84,6 +84,9 @@ def _tokens(t, name, shape, dtype, device):
     return t.data_ptr(), ld
 
 
+_packed = torch.contiguous_format
+
+
 def _starts(doc_starts, device):
     """(pointer, count, tensor to keep) of document starts b*T + t on `device`."""
     if doc_starts is None:
@@ -147,11 +150,15 @@ def qk_norm_rope(cfg: QKNormRopeConfig, q, k, wq, wk, inv_freq, positions, *, q_
     ptrs, ldq, ldk, sq, sk, dt, dev = _qk_inputs(cfg, q, k, wq, wk, inv_freq, positions)
     with _On(q, stream) as st:
         if q_out is None:
-            q_out = torch.empty(sq, dtype=dt, device=dev)
+            q_out = torch.empty_like(q, memory_format=_packed)
+            pq, ldqo = q_out.data_ptr(), 0
+        else:
+            pq, ldqo = _tokens(q_out, "q_out", sq, dt, dev)
         if k_out is None:
-            k_out = torch.empty(sk, dtype=dt, device=dev)
-        pq, ldqo = _tokens(q_out, "q_out", sq, dt, dev)
-        pk, ldko = _tokens(k_out, "k_out", sk, dt, dev)
+            k_out = torch.empty_like(k, memory_format=_packed)
+            pk, ldko = k_out.data_ptr(), 0
+        else:
+            pk, ldko = _tokens(k_out, "k_out", sk, dt, dev)
         rc = lib().ipttt_qk_norm_rope(_byref(cfg.params(ldq, ldk, ldqo, ldko)), *ptrs, pq, pk, st)
         if rc:
             _check(rc, "ipttt_qk_norm_rope")
@@ -166,8 +173,8 @@ def qk_norm_rope_backward(cfg: QKNormRopeConfig, q, k, wq, wk, inv_freq, positio
     pgq, ldqo = _tokens(gq_out, "gq_out", sq, dt, dev)
     pgk, ldko = _tokens(gk_out, "gk_out", sk, dt, dev)
     with _On(q, stream) as st:
-        gq = torch.empty(sq, dtype=dt, device=dev) if gq is None else gq
-        gk = torch.empty(sk, dtype=dt, device=dev) if gk is None else gk
+        gq = torch.empty_like(q, memory_format=_packed) if gq is None else gq
+        gk = torch.empty_like(k, memory_format=_packed) if gk is None else gk
         po, ldgq = _tokens(gq, "gq", sq, dt, dev)
         pk, ldgk = _tokens(gk, "gk", sk, dt, dev)
         gw = torch.empty(2, cfg.D, dtype=torch.float32, device=dev)
@@ -224,7 +231,7 @@ def linear_attention(cfg: LinearAttentionConfig, q, k, v, log_decay, doc_starts=
     p0 = _flat(S0, "S0", sh["S"], f32, dev)
     with _On(q, stream) as st:
         if O is None:
-            O = torch.empty(sh["O"], dtype=dt, device=dev)
+            O = q.new_empty(sh["O"])
         Sf = torch.empty(sh["S"], dtype=f32, device=dev) if S_final is True else S_final if S_final is not False else None
         po, ldo = _tokens(O, "O", sh["O"], dt, dev)
         p = cfg.params(ldq, ldk, ldv, ldo)
@@ -250,7 +257,7 @@ def linear_attention_backward(cfg: LinearAttentionConfig, q, k, v, log_decay, do
     p0 = _flat(S0, "S0", sh["S"], f32, dev)
     ps = _flat(gS_final, "gS_final", sh["S"], f32, dev)
     with _On(q, stream) as st:
-        out = {n: torch.empty(sh[n], dtype=dt, device=dev) for n in ("q", "k", "v")}
+        out = {n: torch.empty_like(t, memory_format=_packed) for n, t in (("q", q), ("k", k), ("v", v))}
         if S0 is not None:
             out["S0"] = torch.empty(sh["S"], dtype=f32, device=dev)
         p = cfg.params(ldq, ldk, ldv, ldo)
@@ -290,8 +297,10 @@ def linear_attention_step(cfg: LinearAttentionConfig, S, q, k, v, log_decay, sta
         raise ValueError("S is missing")
     with _On(q, stream) as st:
         if o is None:
-            o = torch.empty((B, H, Dv), dtype=dt, device=dev)
-        po, ldo = _rows(o, "o", (B, H, Dv), dt, dev)
+            o = q.new_empty((B, H, Dv))
+            po, ldo = o.data_ptr(), 0
+        else:
+            po, ldo = _rows(o, "o", (B, H, Dv), dt, dev)
         rc = lib().ipttt_linattn_step(_byref(cfg.params(ldq, ldk, ldv, ldo, T=1)), ps, pq, pk, pv, pd, pn, po, st)
         if rc:
             _check(rc, "ipttt_linattn_step")

@@ -44,16 +44,28 @@ __device__ __forceinline__ float4 scale4(float4 a, float s) { return make_float4
 
 // ------------------------------------------------------------------ document starts
 
-// Bit t of a row's words for every listed start (strictly increasing offsets b*T + t).
+// The start bits of 32 tokens a thread, from the sorted list of offsets b*T + t: the first start at
+// or after its tokens by search, then those before their end.  (One kernel, where
+// clearing the words and marking every start takes two.)  Every entry is checked by some thread.
 __global__ void k_mark(uint32_t* words, long long wpr, int B, int T, const int32_t* ds, int n, int* status) {
-  const int i = blockIdx.x * blockDim.x + threadIdx.x;
-  if (i >= n) return;
-  const long long g = ds[i];
-  if (g < 0 || g >= (long long)B * T || (i > 0 && (long long)ds[i - 1] >= g)) {
-    set_status(status, IPTTT_ERR_ARG);
-    return;
+  const long long i = blockIdx.x * (long long)blockDim.x + threadIdx.x;
+  for (long long k = i; k < n; k += (long long)gridDim.x * blockDim.x)
+    if (ds[k] < 0 || ds[k] >= (long long)B * T || (k > 0 && ds[k - 1] >= ds[k])) set_status(status, IPTTT_ERR_ARG);
+  if (i >= B * wpr) return;
+  const int t0 = (int)(i % wpr) * 32;
+  uint32_t bits = 0u;
+  if (t0 < T) {
+    const long long base = i / wpr * T + t0, end = base + min(32, T - t0);
+    int lo = 0, hi = n;
+    while (lo < hi) {
+      const int mid = (lo + hi) / 2;
+      if (ds[mid] < base) lo = mid + 1;
+      else hi = mid;
+    }
+    for (; lo < n && ds[lo] < end; ++lo)
+      if (ds[lo] >= base) bits |= 1u << (int)(ds[lo] - base);
   }
-  atomicOr(words + (g / T) * wpr + (g % T) / 32, 1u << ((g % T) % 32));
+  words[i] = bits;
 }
 
 // ------------------------------------------------------------------ the pass on the CUDA cores
@@ -462,9 +474,7 @@ cudaError_t mark_starts(const ipttt_linattn_params& p, const Work& w, uint8_t* w
   *out = nullptr;
   if (n == 0) return cudaSuccess;
   uint32_t* words = reinterpret_cast<uint32_t*>(ws + w.starts);
-  cudaError_t e = cudaMemsetAsync(words, 0, (size_t)p.B * w.words * 4, st);
-  if (e != cudaSuccess) return e;
-  k_mark<<<(n + 255) / 256, 256, 0, st>>>(words, w.words, p.B, p.T, ds, n, status);
+  k_mark<<<(unsigned)((p.B * w.words + 127) / 128), 128, 0, st>>>(words, w.words, p.B, p.T, ds, n, status);
   ++*launches;
   *out = words;
   return cudaGetLastError();
