@@ -199,11 +199,14 @@ __global__ void __launch_bounds__(Cfg<DA, DC, KIND == STATES>::THREADS, 1) k_pas
   float* tabs = reinterpret_cast<float*>(f_buf + Cf::FB);
   uint64_t* bars = reinterpret_cast<uint64_t*>(tabs + 2 * kTab);
   uint64_t *full = bars, *empty = bars + NS;
-  uint64_t *sc_full = bars + 2 * NS, *p_ready = sc_full + 1, *conv_done = sc_full + 2, *d_full = sc_full + 3;
-  uint64_t *f_ready = sc_full + 4, *o_full = sc_full + 5, *o_free = sc_full + 6, *tab_ready = sc_full + 7;
-  uint64_t *a_full = sc_full + 8, *a_empty = sc_full + 10, *drain = sc_full + 12;
-  uint64_t* d_odd = sc_full + 13;  // STATES: d_full of the odd chunks (its waiters are a chunk behind)
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(d_odd + 1);
+  // Pairs are taken in turn by even and odd chunks, where a waiter may be a chunk behind.
+  uint64_t* sc_full = bars + 2 * NS;     // [2]
+  uint64_t* conv_done = sc_full + 2;     // [2][2]: chunk, half of its tokens
+  uint64_t* d_full = sc_full + 6;        // [2]
+  uint64_t *a_full = sc_full + 8, *a_empty = sc_full + 10;  // [2]: the a buffers
+  uint64_t *p_ready = sc_full + 12, *f_ready = sc_full + 13, *o_full = sc_full + 14, *o_free = sc_full + 15;
+  uint64_t *tab_ready = sc_full + 16, *f_free = sc_full + 17, *drain = sc_full + 18;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   uint32_t* issued = tmem_slot + 2;  // ring tiles and a tiles whose loads were issued
 
@@ -215,22 +218,23 @@ __global__ void __launch_bounds__(Cfg<DA, DC, KIND == STATES>::THREADS, 1) k_pas
   if (threadIdx.x == 0) {
     for (int s = 0; s < NS; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1);
+      mbar_init(&empty[s], STATE ? 1 : 2);
     }
-    mbar_init(sc_full, 1);
-    mbar_init(p_ready, 8);
-    mbar_init(conv_done, 8);
-    mbar_init(d_full, 1);
-    mbar_init(d_odd, 1);
-    mbar_init(f_ready, 8);
-    mbar_init(o_full, 1);
-    mbar_init(o_free, 8);
-    mbar_init(tab_ready, STATE ? 8 : 16);
     for (int s = 0; s < 2; ++s) {
+      mbar_init(&sc_full[s], 1);
+      mbar_init(&conv_done[2 * s], 8);
+      mbar_init(&conv_done[2 * s + 1], 8);
+      mbar_init(&d_full[s], 1);
       mbar_init(&a_full[s], 1);
       mbar_init(&a_empty[s], 8);
     }
-    mbar_init(drain, 1);
+    mbar_init(p_ready, 8);
+    mbar_init(f_ready, 8);
+    mbar_init(f_free, 1);
+    mbar_init(o_full, 1);
+    mbar_init(o_free, 8);
+    mbar_init(tab_ready, STATE ? 8 : 16);
+    mbar_init(drain, STATE ? 1 : 2);
     *abort_flag = 0;
     issued[0] = issued[1] = 0;
     fence_mbar_init();
@@ -277,10 +281,31 @@ __global__ void __launch_bounds__(Cfg<DA, DC, KIND == STATES>::THREADS, 1) k_pas
         mbar_arrive_expect_tx(bar, 256 * width);
         for (int q = 0; q < width / 64; ++q) tma_load_3d(dst + q * 16384, m, bar, x + 64 * q, ch * CH, b);
       };
+      // The ring is short of what HBM's latency asks for, so tiles are brought into L2 kAhead chunks
+      // before their place in the ring comes free.
+      constexpr int kAhead = 2;
+      int ai = blockIdx.x, an = 0;  // the item and chunk that the prefetches have come to
+      auto prefetch = [&]() {
+        if (ai >= ta.items) return;
+        const Item it = item_of(p, ai);
+        const int ch = rev ? it.last - 1 - an : it.first + an;
+        auto one = [&](const CUtensorMap* m, int width, int x) {
+          for (int q = 0; q < width / 64; ++q) tma_prefetch_3d(m, x + 64 * q, ch * CH, it.b);
+        };
+        one(&ta.mb, DA, it.h / p.gb * DA);
+        if constexpr (!STATE) one(&ta.ma, DA, it.h / p.ga * DA);
+        one(&ta.mc, DC, it.h / p.gc * DC);
+        if (++an == it.last - it.first) {
+          an = 0;
+          ai += gridDim.x;
+        }
+      };
+      for (int k = 0; k < kAhead; ++k) prefetch();
       for (int i = blockIdx.x; ok && i < ta.items; i += gridDim.x) {
         const Item it = item_of(p, i);
         for (int n = 0; n < it.last - it.first; ++n, ++cc) {
           const int ch = rev ? it.last - 1 - n : it.first + n;
+          prefetch();
           LA_WAIT(&empty[tl % NS], (tl / NS) ^ 1u);
           load(ring + tl % NS * SLOT, &ta.mb, &full[tl % NS], DA, it.h / p.gb * DA, ch, it.b);
           ++tl;
@@ -295,7 +320,9 @@ __global__ void __launch_bounds__(Cfg<DA, DC, KIND == STATES>::THREADS, 1) k_pas
         }
       }
       issued[0] = tl;
-    } else if (warp == 1 && lane == 0) {
+    } else if ((warp == 1 || warp == 2) && lane == 0 && !(STATE && warp == 1)) {
+      // Two threads issue the MMAs, warp 1's (1), (2) and (3), warp 2's (4): issuing takes longer than
+      // the tensor pipe does, and (4) is on the path that bounds a chunk, from state to state.
       constexpr uint32_t id1 = idesc_bf16(128, 128, false, false), id2 = idesc_bf16(128, DC, false, true),
                          id3 = idesc_bf16(128, DC, false, true), id4 = idesc_bf16(128, DC, true, true);
       // width 64: rows 64-127 of (4) repeat rows 0-63 (the second block of 64 is the first)
@@ -305,51 +332,65 @@ __global__ void __launch_bounds__(Cfg<DA, DC, KIND == STATES>::THREADS, 1) k_pas
       // clocks a MMA, where the tensor pipe takes 64.
       auto k_major = [](const uint8_t* t) { return sdesc_sw128(smem_u32(t), 16, 1024); };
       auto mn_major = [](const uint8_t* t, uint32_t lbo) { return sdesc_sw128(smem_u32(t), lbo, 1024); };
-      const uint64_t a_k = k_major(a_buf), b_k = k_major(ring), b_mn = mn_major(ring, lbo4), c_mn = mn_major(ring, 16384),
-                     lo_mn = mn_major(lo_buf, lbo4), f_mn = mn_major(f_buf, DA * 128);
-      uint32_t tl = 0, cc = 0;
-      for (int i = blockIdx.x; ok && i < ta.items; i += gridDim.x) {
+      uint32_t total = 0;  // chunks this block walks
+      for (int i = blockIdx.x; i < ta.items; i += gridDim.x) {
         const Item it = item_of(p, i);
-        for (int n = it.first; n < it.last; ++n, ++cc, tl += 2) {
-          const uint32_t sb = tl % NS, sc = (tl + 1) % NS;
-          const uint64_t da = a_k + (cc & 1) * (ASLOT / 16), db = b_k + sb * (SLOT / 16), dbm = b_mn + sb * (SLOT / 16),
-                         dc = c_mn + sc * (SLOT / 16);
-          if constexpr (!STATE) {
-            LA_WAIT(&full[sb], tl / NS);
-            LA_WAIT(&a_full[cc & 1], cc >> 1);
-            tc_fence_after();
-#pragma unroll
-            for (int k = 0; k < DA / 16; ++k)
-              mma_bf16(tm + kSC, da + (k / 4) * 1024 + (k % 4) * 2, db + (k / 4) * 1024 + (k % 4) * 2, id1, k > 0);
-            mma_commit(sc_full);
-            LA_WAIT(f_ready, cc);
-            LA_WAIT(o_free, cc ^ 1u);
-            tc_fence_after();
-#pragma unroll
-            for (int k = 0; k < DA / 16; ++k)
-              mma_bf16(tm + kO1, da + (k / 4) * 1024 + (k % 4) * 2, f_mn + k * 128, id2, k > 0);
-          }
-          LA_WAIT(conv_done, cc);
-          LA_WAIT(&full[sc], (tl + 1) / NS);
+        total += it.last - it.first;
+      }
+      const uint64_t c_mn = mn_major(ring, 16384);
+      auto tile = [](uint32_t n) { return n % NS; };
+      if (warp == 1) {
+        const uint64_t a_k = k_major(a_buf), b_k = k_major(ring), f_mn = mn_major(f_buf, DA * 128);
+        for (uint32_t c = 0; c < total; ++c) {
+          const uint32_t sb = tile(2 * c), sc = tile(2 * c + 1);
+          const uint64_t da = a_k + (c & 1) * (ASLOT / 16), db = b_k + sb * (SLOT / 16), dc = c_mn + sc * (SLOT / 16);
+          LA_WAIT(&full[sb], 2 * c / NS);
+          LA_WAIT(&a_full[c & 1], c >> 1);
           tc_fence_after();
 #pragma unroll
-          for (int k = 0; k < CH / 16; ++k) mma_bf16(tm + d_col + two_col * (cc & 1), dbm + k * 128, dc + k * 128, id4, k > 0);
+          for (int k = 0; k < DA / 16; ++k)
+            mma_bf16(tm + kSC, da + (k / 4) * 1024 + (k % 4) * 2, db + (k / 4) * 1024 + (k % 4) * 2, id1, k > 0);
+          mma_commit(&sc_full[c & 1]);
+          mma_commit(&empty[sb]);
+          LA_WAIT(f_ready, c);
+          LA_WAIT(o_free, c ^ 1u);
+          tc_fence_after();
+#pragma unroll
+          for (int k = 0; k < DA / 16; ++k)
+            mma_bf16(tm + kO1, da + (k / 4) * 1024 + (k % 4) * 2, f_mn + k * 128, id2, k > 0);
+          mma_commit(f_free);
+          LA_WAIT(p_ready, c);
+          LA_WAIT(&full[sc], (2 * c + 1) / NS);
+          tc_fence_after();
+          // P lies in columns 0-31 and 64-95 of the scores' place
 #pragma unroll
           for (int k = 0; k < CH / 16; ++k)
-            mma_bf16(tm + d_col + two_col * (cc & 1), lo_mn + (cc & 1) * two_lo + k * 128, dc + k * 128, id4, 1);
-          mma_commit(&empty[sb]);
-          if constexpr (STATE) mma_commit(&empty[sc]);
-          mma_commit(STATE && (cc & 1) ? d_odd : d_full);
-          if constexpr (!STATE) {
-            LA_WAIT(p_ready, cc);
-            tc_fence_after();
-            // P lies in columns 0-31 and 64-95 of the scores' place
+            mma_bf16_ta(tm + col_o2(DC), tm + kSC + 8 * k + (k < 4 ? 0 : 32), dc + k * 128, id3, k > 0);
+          mma_commit(&empty[sc]);
+          mma_commit(o_full);
+        }
+      } else {
+        const uint64_t b_mn = mn_major(ring, lbo4), lo_mn = mn_major(lo_buf, lbo4);
+        for (uint32_t c = 0; c < total; ++c) {
+          const uint32_t sb = tile(2 * c), sc = tile(2 * c + 1);
+          const uint64_t db = b_mn + sb * (SLOT / 16), dc = c_mn + sc * (SLOT / 16), dl = lo_mn + (c & 1) * two_lo;
+          const uint32_t d = tm + d_col + two_col * (c & 1);
+          LA_WAIT(&full[sc], (2 * c + 1) / NS);
+          LA_WAIT(&conv_done[2 * (c & 1)], c >> 1);  // the first 64 tokens (and the last chunk's D has been read)
+          tc_fence_after();
 #pragma unroll
-            for (int k = 0; k < CH / 16; ++k)
-              mma_bf16_ta(tm + col_o2(DC), tm + kSC + 8 * k + (k < 4 ? 0 : 32), dc + k * 128, id3, k > 0);
-            mma_commit(&empty[sc]);
-            mma_commit(o_full);
-          }
+          for (int k = 0; k < 4; ++k) mma_bf16(d, db + k * 128, dc + k * 128, id4, k > 0);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) mma_bf16(d, dl + k * 128, dc + k * 128, id4, 1);
+          LA_WAIT(&conv_done[2 * (c & 1) + 1], c >> 1);
+          tc_fence_after();
+#pragma unroll
+          for (int k = 4; k < 8; ++k) mma_bf16(d, db + k * 128, dc + k * 128, id4, 1);
+#pragma unroll
+          for (int k = 4; k < 8; ++k) mma_bf16(d, dl + k * 128, dc + k * 128, id4, 1);
+          mma_commit(&d_full[c & 1]);
+          mma_commit(&empty[sb]);
+          mma_commit(&empty[sc]);
         }
       }
       mma_commit(drain);
@@ -390,7 +431,7 @@ __global__ void __launch_bounds__(Cfg<DA, DC, KIND == STATES>::THREADS, 1) k_pas
               in = row < st.first();
             }
           }
-          LA_WAIT_WARP(sc_full, cc);
+          LA_WAIT_WARP(&sc_full[cc & 1], cc >> 1);
           if (cc > 0 && lane == 0) {  // the last chunk's output has left the a tile's place
             bulk_wait_read<0>();
             mbar_arrive(&a_empty[(cc - 1) & 1]);
@@ -557,18 +598,35 @@ __global__ void __launch_bounds__(Cfg<DA, DC, KIND == STATES>::THREADS, 1) k_pas
 #pragma unroll
           for (int e = 0; e < NC; ++e) f[e] = 0.0f;
         }
-        uint32_t r[2][16];
-        tmem_ld16(addr, r[0]);
+        constexpr int STEP = NC < 32 ? NC : 32;
 #pragma unroll
-        for (int q = 0; q < NC / 16; ++q) {
+        for (int q = 0; q < NC / STEP; ++q) {
+          uint32_t r[STEP];
+          if constexpr (STEP == 16) tmem_ld16(addr + STEP * q, r);
+          else tmem_ld32(addr + STEP * q, r);
           tmem_ld_wait();
-          if (q + 1 < NC / 16) tmem_ld16(addr + 16 * (q + 1), r[(q + 1) & 1]);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) f[16 * q + e] = fmaf(keep, f[16 * q + e], __uint_as_float(r[q & 1][e]));
+          for (int e = 0; e < STEP; ++e) f[STEP * q + e] = fmaf(keep, f[STEP * q + e], __uint_as_float(r[e]));
+        }
+      };
+      // each row's weight in a chunk as wh + wl (bf16 each); a thread's 16-byte units lie in four rows
+      __nv_bfloat162 wh[4], wl[4];
+      auto weights = [&](int ch, const Starts& st) {
+        const int len = min(CH, p.T - ch * CH);
+        // rows that reach the state at the chunk's far end
+        const int from = rev ? 0 : st.last(), to = rev ? min(len, st.first()) : len;
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          const int j = (tid >> 3) + 32 * m;
+          const float w = j >= from && j < to ? pw[rev ? j : len - 1 - j] : 0.0f;
+          const __nv_bfloat16 x = __float2bfloat16_rn(w);
+          wh[m] = __bfloat162bfloat162(x);
+          wl[m] = __float2bfloat162_rn(w - __bfloat162float(x));
         }
       };
       float keep = 0.0f;
       Starts next = starts_of(p, it.b, rev ? it.last - 1 : it.first);
+      weights(rev ? it.last - 1 : it.first, next);
       for (int n = 0; n < it.last - it.first; ++n, ++cc, tl += 2) {
         const int ch = rev ? it.last - 1 - n : it.first + n;
         const int t0 = ch * CH, len = min(CH, p.T - t0);
@@ -576,12 +634,11 @@ __global__ void __launch_bounds__(Cfg<DA, DC, KIND == STATES>::THREADS, 1) k_pas
         if (n + 1 < it.last - it.first) next = starts_of(p, it.b, ch + step);
         const bool any = st.any();
         const int lag = rev && t0 + len == p.T ? 1 : 0;
-        // rows that reach the state at the chunk's far end
-        const int out_from = rev ? 0 : st.last(), out_to = rev ? min(len, st.first()) : len;
         const uint32_t sb = tl % NS;
         if constexpr (!STATE) {
-          // the operand copy of the state, [Dc / 64][Da][64] in 128-byte swizzled rows; the last
-          // chunk's (2) has read the old one: its d_full came after it
+          // the operand copy of the state, [Dc / 64][Da][64] in 128-byte swizzled rows, once the last
+          // chunk's (2) has read the old one
+          if (cc > 0) LA_WAIT_WARP(f_free, cc - 1);
           uint8_t* fb = f_buf + (c0 / 64) * (DA * 128) + row * 128;
 #pragma unroll
           for (int e = 0; e < NC / 8; ++e) {
@@ -594,63 +651,56 @@ __global__ void __launch_bounds__(Cfg<DA, DC, KIND == STATES>::THREADS, 1) k_pas
           __syncwarp();
           if (lane == 0) mbar_arrive(f_ready);
         }
-        // each row's weight as wh + wl (bf16 each); a thread's units lie in four rows
-        __nv_bfloat162 wh[4], wl[4];
-#pragma unroll
-        for (int m = 0; m < 4; ++m) {
-          const int j = (tid >> 3) + 32 * m;
-          const float w = j >= out_from && j < out_to ? pw[rev ? j : len - 1 - j] : 0.0f;
-          const __nv_bfloat16 x = __float2bfloat16_rn(w);
-          wh[m] = __bfloat162bfloat162(x);
-          wl[m] = __float2bfloat162_rn(w - __bfloat162float(x));
-        }
         LA_WAIT_WARP(&full[sb], tl / NS);
         uint8_t* bt = ring + sb * SLOT + tid * 16;
         uint8_t* lt = lo_buf + (cc & 1) * (two_lo * 16) + tid * 16;
-        uint4 v[4];
+        if constexpr (!STATE) LA_WAIT_WARP(&sc_full[cc & 1], cc >> 1);  // (1) has read B: it may be overwritten
+        // hi = bf16(b wh); b wh - hi is a bf16 number, so lo = bf16(b wl + (b wh - hi)) loses 2^-9 of lo
+        // alone.  64 tokens at a time: the first half's (4) starts while the second is scaled.
 #pragma unroll
-        for (int m = 0; m < 4; ++m) v[m] = *reinterpret_cast<const uint4*>(bt + m * 4096);
-        if constexpr (!STATE) LA_WAIT_WARP(sc_full, cc);  // (1) has read B: it may be overwritten
-        // hi = bf16(b wh); b wh - hi is a bf16 number, so lo = bf16(b wl + (b wh - hi)) loses 2^-9 of lo alone
-#pragma unroll 1
-        for (int k = 0; k < DA / 64; ++k) {
+        for (int half = 0; half < 2; ++half) {
+          uint4 v[DA / 32];
 #pragma unroll
-          for (int m = 0; m < 4; ++m) {
-            uint32_t hi4[4], lo4[4];
+          for (int m = 0; m < DA / 32; ++m)
+            v[m] = *reinterpret_cast<const uint4*>(bt + (2 * half + (m & 1) + 4 * (m >> 1)) * 4096);
+#pragma unroll
+          for (int m = 0; m < DA / 32; ++m) {
+            const __nv_bfloat162 h = wh[2 * half + (m & 1)], l = wl[2 * half + (m & 1)];
             const uint32_t u[4] = {v[m].x, v[m].y, v[m].z, v[m].w};
-            if (k + 1 < DA / 64) v[m] = *reinterpret_cast<const uint4*>(bt + (m + 4) * 4096);
+            uint32_t hi4[4], lo4[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const __nv_bfloat162 x = *reinterpret_cast<const __nv_bfloat162*>(&u[e]);
-              const __nv_bfloat162 h2 = __hmul2(x, wh[m]);
-              const __nv_bfloat162 l2 = __hfma2(x, wl[m], __hfma2(x, wh[m], __hneg2(h2)));
+              const __nv_bfloat162 h2 = __hmul2(x, h);
+              const __nv_bfloat162 l2 = __hfma2(x, l, __hfma2(x, h, __hneg2(h2)));
               hi4[e] = *reinterpret_cast<const uint32_t*>(&h2);
               lo4[e] = *reinterpret_cast<const uint32_t*>(&l2);
             }
-            *reinterpret_cast<uint4*>(bt + (m + 4 * k) * 4096) = make_uint4(hi4[0], hi4[1], hi4[2], hi4[3]);
-            *reinterpret_cast<uint4*>(lt + (m + 4 * k) * 4096) = make_uint4(lo4[0], lo4[1], lo4[2], lo4[3]);
+            const int at = (2 * half + (m & 1) + 4 * (m >> 1)) * 4096;
+            *reinterpret_cast<uint4*>(bt + at) = make_uint4(hi4[0], hi4[1], hi4[2], hi4[3]);
+            *reinterpret_cast<uint4*>(lt + at) = make_uint4(lo4[0], lo4[1], lo4[2], lo4[3]);
           }
+          fence_proxy_async_smem();
+          tc_fence_before();  // the last chunk's D has been read
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&conv_done[2 * (cc & 1) + half]);
         }
-        fence_proxy_async_smem();
-        tc_fence_before();  // the last chunk's D has been read
-        __syncwarp();
-        if (lane == 0) mbar_arrive(conv_done);
-
         const float keep_now = any ? 0.0f : pw[len - lag];
+        if (n + 1 < it.last - it.first) weights(ch + step, next);
         if constexpr (STATE) {
           if (n > 0) {
-            LA_WAIT_WARP(cc & 1 ? d_full : d_odd, (cc - 1) >> 1);
+            LA_WAIT_WARP(&d_full[(cc - 1) & 1], (cc - 1) >> 1);
             advance(keep, cc - 1);
           }
           keep = keep_now;
         } else {
-          LA_WAIT_WARP(d_full, cc);
+          LA_WAIT_WARP(&d_full[cc & 1], cc >> 1);
           advance(keep_now, cc);
         }
       }
       if (!ok) break;
       if constexpr (STATE) {
-        LA_WAIT_WARP(cc & 1 ? d_full : d_odd, (cc - 1) >> 1);
+        LA_WAIT_WARP(&d_full[(cc - 1) & 1], (cc - 1) >> 1);
         advance(keep, cc - 1);
       }
       if (!ok) break;

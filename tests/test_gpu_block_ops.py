@@ -180,6 +180,25 @@ def test_linear_attention_many_segments_and_long_rows():
     assert status() == 0
 
 
+@pytest.mark.parametrize("B,T,H,D", [(1, 32768, 20, 128), (1, 5100, 150, 64), (2, 9000, 30, 128)])
+def test_linear_attention_long_items(B, T, H, D):
+    # many chunks to a work item, cut rows and whole ones: the tensor-core pass against the fp32 pass (held
+    # to the definition above) on the same values
+    docs = sorted(set(torch.randint(0, B * T, (15,), generator=torch.Generator().manual_seed(4)).tolist()))
+    cfg, q, k, v, _, S0, ds = attn_case(B, T, H, H, D, D, "bf16", docs, True)
+    ld = torch.log1p(-torch.exp2(-4.0 - 7.0 * torch.arange(H) / H)).cuda()
+    f32 = pkg.LinearAttentionConfig(B, T, H, H, D, D, cfg.scale, "f32")
+    gO = ref.rand(20, B, T, H, D, dtype=torch.bfloat16).cuda()
+    O, S = pkg.linear_attention(cfg, q, k, v, ld, ds, S0=S0, S_final=True)
+    want, want_S = pkg.linear_attention(f32, q.float(), k.float(), v.float(), ld, ds, S0=S0, S_final=True)
+    assert ref.relative(O, want.cpu()) <= 6e-3 and ref.relative(S, want_S.cpu()) <= 1e-5
+    g = pkg.linear_attention_backward(cfg, q, k, v, ld, ds, gO, S0=S0, gS_final=S0)
+    w = pkg.linear_attention_backward(f32, q.float(), k.float(), v.float(), ld, ds, gO.float(), S0=S0, gS_final=S0)
+    for n in g:
+        assert ref.relative(g[n], w[n].cpu()) <= (1e-5 if n == "S0" else 6e-3), n
+    assert status() == 0
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("shape", [(1, 1, 1, 64, 64), (3, 4, 2, 128, 128), (2, 3, 3, 40, 56), (20, 16, 4, 128, 128),
                                    (2, 2, 1, 256, 136)])
