@@ -150,29 +150,6 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// Two fp32 operations in one instruction.
-__device__ __forceinline__ uint64_t two(float lo, float hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-__device__ __forceinline__ uint32_t pack2(uint64_t v) {
-  float lo, hi;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-  return pack2(lo, hi);
-}
-__device__ __forceinline__ uint64_t two(const uint32_t* r) { return two(__uint_as_float(r[0]), __uint_as_float(r[1])); }
-
 // mbar_wait_or_abort in few instructions: there are some twenty waits in the kernel.
 __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile int* abort) {
   bool done = mbar_try_wait(bar, parity);
@@ -405,7 +382,6 @@ __global__ void __launch_bounds__(Cfg<DA, DC, KIND == STATES>::THREADS, 1) k_pas
       const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
       const uint32_t sc_addr = tm + kSC + lanes + 64 * half, o1_addr = tm + kO1 + lanes + HC * half,
                      o2_addr = tm + col_o2(DC) + lanes + HC * half;
-      const uint64_t s0_2 = two(p.scale, p.scale);
       uint32_t cc = 0, ic = 0;
       for (int i = blockIdx.x; ok && i < ta.items; i += gridDim.x, ++ic) {
         const Item it = item_of(p, i);
@@ -455,17 +431,17 @@ __global__ void __launch_bounds__(Cfg<DA, DC, KIND == STATES>::THREADS, 1) k_pas
                 tmem_ld_wait();
 #pragma unroll
                 for (int e = 0; e < 16; ++e)
-                  w[e] = pack2(mul2(two(v + 2 * e), rev ? two(wt[2 * e], wt[2 * e + 1]) : two(wt[-2 * e], wt[-2 * e - 1])));
+                  w[e] = pack2(__uint_as_float(v[2 * e]) * wt[rev ? 2 * e : -2 * e],
+                               __uint_as_float(v[2 * e + 1]) * wt[rev ? 2 * e + 1 : -2 * e - 1]);
               } else {  // a factor of the column times one of the row, neither above 1
                 const float rf = rev ? pw[32 * block - row] : pw[row - 32 * block - 31];
-                const uint64_t rf2 = two(rf, rf);
-                const ulonglong2* col = reinterpret_cast<const ulonglong2*>(rev ? pw : pw - 128 + kPw);
+                const float4* col = reinterpret_cast<const float4*>(rev ? pw : pw - 128 + kPw);
                 tmem_ld_wait();
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                  const ulonglong2 c2 = col[e];
-                  w[2 * e] = pack2(mul2(mul2(two(v + 4 * e), c2.x), rf2));
-                  w[2 * e + 1] = pack2(mul2(mul2(two(v + 4 * e + 2), c2.y), rf2));
+                  const float4 c = col[e];
+                  w[2 * e] = pack2(__uint_as_float(v[4 * e]) * c.x * rf, __uint_as_float(v[4 * e + 1]) * c.y * rf);
+                  w[2 * e + 1] = pack2(__uint_as_float(v[4 * e + 2]) * c.z * rf, __uint_as_float(v[4 * e + 3]) * c.w * rf);
                 }
               }
               if (any) {
@@ -489,7 +465,6 @@ __global__ void __launch_bounds__(Cfg<DA, DC, KIND == STATES>::THREADS, 1) k_pas
           const bool write = row < len;
           const float win = in && write ? pw[rev ? len - row - lag : row + 1] : 0.0f;
           const float s1 = win * p.scale;
-          const uint64_t s1_2 = two(s1, s1);
           // the output goes out through the a tile's place: (1) and (2) are done with it
           uint8_t* stage = a_buf + (cc & 1) * ASLOT + half * (256 * HC);
           LA_WAIT_WARP(o_full, cc);
@@ -500,30 +475,31 @@ __global__ void __launch_bounds__(Cfg<DA, DC, KIND == STATES>::THREADS, 1) k_pas
             tmem_ld16(o2_addr + 16 * q, x);
             tmem_ld16(o1_addr + 16 * q, y);
             tmem_ld_wait();
-            uint64_t o[8];
+            float o[16];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              // rows of another document take nothing of the state, whatever is in it
-              const uint64_t s = win != 0.0f ? two(y + 2 * e) : 0ull;
-              o[e] = fma2(s1_2, s, mul2(s0_2, two(x + 2 * e)));
+            for (int e = 0; e < 16; ++e) o[e] = p.scale * __uint_as_float(x[e]);
+            if (!any || win != 0.0f) {  // rows of another document take nothing of the state, whatever is in it
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] = fmaf(s1, __uint_as_float(y[e]), o[e]);
             }
             if (p.out_f32) {
               if (write) {
-                ulonglong2* g = reinterpret_cast<ulonglong2*>(
-                    static_cast<float*>(p.out) + ((long long)it.b * p.T + t0 + row) * p.ldo + (long long)it.h * DC +
-                    HC * half + 16 * q);
+                float4* g = reinterpret_cast<float4*>(static_cast<float*>(p.out) +
+                                                      ((long long)it.b * p.T + t0 + row) * p.ldo + (long long)it.h * DC +
+                                                      HC * half + 16 * q);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) g[e] = make_ulonglong2(o[2 * e], o[2 * e + 1]);
+                for (int e = 0; e < 4; ++e) g[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
               }
-              __syncwarp();
             } else {  // rows of HC columns, swizzled as the store's map is
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
                 const int unit = (2 * q + e) ^ (HC == 64 ? row & 7 : (row >> 1) & 3);
                 *reinterpret_cast<uint4*>(stage + row * (2 * HC) + unit * 16) =
-                    make_uint4(pack2(o[4 * e]), pack2(o[4 * e + 1]), pack2(o[4 * e + 2]), pack2(o[4 * e + 3]));
+                    make_uint4(pack2(o[8 * e], o[8 * e + 1]), pack2(o[8 * e + 2], o[8 * e + 3]),
+                               pack2(o[8 * e + 4], o[8 * e + 5]), pack2(o[8 * e + 6], o[8 * e + 7]));
               }
             }
+            __syncwarp();
           }
           tc_fence_before();  // the accumulators are free
           __syncwarp();
