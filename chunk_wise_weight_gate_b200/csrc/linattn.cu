@@ -329,9 +329,11 @@ template <typename T>
 cudaError_t launch_step(const ipttt_linattn_params& p, float* S, const void* q, const void* k, const void* v,
                         const float* ld, const int32_t* starts, void* o, int* status, cudaStream_t st) {
   const int blocks = p.B * p.H, G = p.H / p.Hkv;
-  // whole rows of the state where (row, head) pairs alone fill the SMs twice, else quarter rows
+  // half rows of the state (of 128) where (row, head) pairs alone fill the SMs twice, else quarter
+  // rows.  640 pairs of 128 x 128: 16.8 us with 64 columns and 4 loads ahead a thread, 18.0 with
+  // 32 columns, 17.4 with 128 and 8 loads, 20.3 with 128 and 16 (12.9 at the copy bandwidth).
   if (blocks >= 296)
-    k_step<T, 128, 16><<<dim3(blocks, (p.Dv + 127) / 128), kThreads, 0, st>>>(
+    k_step<T, 64, 4><<<dim3(blocks, (p.Dv + 63) / 64), kThreads, 0, st>>>(
         S, static_cast<const T*>(q), static_cast<const T*>(k), static_cast<const T*>(v), ld, starts, static_cast<T*>(o),
         p.H, G, p.Dk, p.Dv, p.ldq, p.ldk, p.ldv, p.ldo, p.scale, status);
   else
@@ -348,8 +350,8 @@ int simt_segments(int B, int T, int H, int Da, int Dc, int* seg_chunks) {
   const int nchunks = (T + L - 1) / L;
   const long long blocks = (long long)B * H * ((Dc + kSlice - 1) / kSlice);
   // one segment where the rows, heads and column slices fill the SMs, else enough
-  // segments of at least 8 chunks to do so
-  int segs = (int)std::min<long long>((nchunks + 7) / 8, (148 + blocks - 1) / blocks);
+  // segments of at least 4 chunks to do so
+  int segs = (int)std::min<long long>((nchunks + 3) / 4, (148 + blocks - 1) / blocks);
   segs = std::max(1, segs);
   *seg_chunks = (nchunks + segs - 1) / segs;
   return (nchunks + *seg_chunks - 1) / *seg_chunks;

@@ -258,31 +258,10 @@ __global__ void __launch_bounds__(Cfg<DA, DC, KIND == STATES>::THREADS, 1) k_pas
         mbar_arrive_expect_tx(bar, 256 * width);
         for (int q = 0; q < width / 64; ++q) tma_load_3d(dst + q * 16384, m, bar, x + 64 * q, ch * CH, b);
       };
-      // The ring is short of what HBM's latency asks for, so tiles are brought into L2 kAhead chunks
-      // before their place in the ring comes free.
-      constexpr int kAhead = 2;
-      int ai = blockIdx.x, an = 0;  // the item and chunk that the prefetches have come to
-      auto prefetch = [&]() {
-        if (ai >= ta.items) return;
-        const Item it = item_of(p, ai);
-        const int ch = rev ? it.last - 1 - an : it.first + an;
-        auto one = [&](const CUtensorMap* m, int width, int x) {
-          for (int q = 0; q < width / 64; ++q) tma_prefetch_3d(m, x + 64 * q, ch * CH, it.b);
-        };
-        one(&ta.mb, DA, it.h / p.gb * DA);
-        if constexpr (!STATE) one(&ta.ma, DA, it.h / p.ga * DA);
-        one(&ta.mc, DC, it.h / p.gc * DC);
-        if (++an == it.last - it.first) {
-          an = 0;
-          ai += gridDim.x;
-        }
-      };
-      for (int k = 0; k < kAhead; ++k) prefetch();
       for (int i = blockIdx.x; ok && i < ta.items; i += gridDim.x) {
         const Item it = item_of(p, i);
         for (int n = 0; n < it.last - it.first; ++n, ++cc) {
           const int ch = rev ? it.last - 1 - n : it.first + n;
-          prefetch();
           LA_WAIT(&empty[tl % NS], (tl / NS) ^ 1u);
           load(ring + tl % NS * SLOT, &ta.mb, &full[tl % NS], DA, it.h / p.gb * DA, ch, it.b);
           ++tl;

@@ -101,11 +101,6 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* m, uin
       "l"(m), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
       : "memory");
 }
-// Brings a box into L2 alone.
-__device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap* m, int x, int y, int z) {
-  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(m), "r"(x), "r"(y), "r"(z)
-               : "memory");
-}
 // L2 policies for TMA loads: evict_last for an operand every tile reads again
 // (kept resident across the launch), evict_first for one read by a few
 // concurrent tiles and then dead.

@@ -28,9 +28,13 @@ constexpr int kThreads = 256;
 // out[slice][m][n] = sum over the slice of k of A(m, k) B(k, n), fp32 FMA.  An operand is
 // either K-major (A[m * lda + k]) or MN-major (A[k * lda + m]); K-major operands have
 // K a multiple of 4, MN-major ones rows readable up to a multiple of 4 columns.
-// 128 x 128 tiles, 8 x 8 products a thread (two 4-wide strips 64 apart in either
-// direction), 16 k a step, the next step's operands in registers meanwhile.
-constexpr int SM = 128, SK = 16;
+// 64 x 128 tiles of 128 threads, 8 x 8 products a thread (strips of 4 rows and columns, 32 and 64
+// apart), 16 k a step, the next step's operands in registers meanwhile.  The 64-row tiles
+// waste less of the odd row counts of a small model than 128 would, and give enough
+// blocks for four an SM.  300 tokens, 10007 words, d = 512: 84 us for the logits (37 TFLOP/s),
+// 71 for gH, 76 for gW; one product an instruction took 87, 80 and 88, 128 x 128 tiles of 256
+// threads 111, 132 and 97.
+constexpr int SM = 64, SN = 128, SK = 16, kGemmThreads = 128;
 struct Sgemm {
   const float *A, *B;
   float* out;
@@ -40,98 +44,125 @@ struct Sgemm {
   int add;             // add to out
 };
 
-template <bool KMAJOR>
-__device__ __forceinline__ void fetch(const float* X, long long ld, int rows, int cols, int k1, int r0, int k0, float4 (&v)[2]) {
+// The block's part of an operand for 16 k: WIDTH rows (or columns) from r0 on.
+template <bool KMAJOR, int WIDTH> struct Fetch {
+  static constexpr int N = WIDTH * SK / 4 / kGemmThreads;
+  float4 v[N];
+  __device__ __forceinline__ void load(const float* X, long long ld, int rows, int cols, int k1, int r0, int k0) {
 #pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    const int i = threadIdx.x + u * kThreads;
-    v[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (KMAJOR) {
-      const int r = r0 + i / 4, k = k0 + 4 * (i % 4);
-      if (r < rows && k < k1) v[u] = *reinterpret_cast<const float4*>(X + r * ld + k);
-    } else {
-      const int k = k0 + i / 32, r = r0 + 4 * (i % 32);
-      if (k < k1 && r < cols) v[u] = *reinterpret_cast<const float4*>(X + k * ld + r);
+    for (int u = 0; u < N; ++u) {
+      const int i = threadIdx.x + u * kGemmThreads;
+      v[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (KMAJOR) {
+        const int r = r0 + i / 4, k = k0 + 4 * (i % 4);
+        if (r < rows && k < k1) v[u] = *reinterpret_cast<const float4*>(X + r * ld + k);
+      } else {
+        const int k = k0 + i / (WIDTH / 4), r = r0 + 4 * (i % (WIDTH / 4));
+        if (k < k1 && r < cols) v[u] = *reinterpret_cast<const float4*>(X + k * ld + r);
+      }
     }
   }
-}
+  __device__ __forceinline__ void place(float (*s)[WIDTH + 4]) const {
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+      const int i = threadIdx.x + u * kGemmThreads;
+      if (KMAJOR) {
+        const int r = i / 4, k = 4 * (i % 4);
+        s[k][r] = v[u].x;
+        s[k + 1][r] = v[u].y;
+        s[k + 2][r] = v[u].z;
+        s[k + 3][r] = v[u].w;
+      } else {
+        *reinterpret_cast<float4*>(&s[i / (WIDTH / 4)][4 * (i % (WIDTH / 4))]) = v[u];
+      }
+    }
+  }
+};
 
-template <bool KMAJOR>
-__device__ __forceinline__ void place(float (*s)[SM + 4], const float4 (&v)[2]) {
-#pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    const int i = threadIdx.x + u * kThreads;
-    if (KMAJOR) {
-      const int r = i / 4, k = 4 * (i % 4);
-      s[k][r] = v[u].x;
-      s[k + 1][r] = v[u].y;
-      s[k + 2][r] = v[u].z;
-      s[k + 3][r] = v[u].w;
-    } else {
-      *reinterpret_cast<float4*>(&s[i / 32][4 * (i % 32)]) = v[u];
-    }
-  }
+// d += a b on two fp32 numbers at once (each rounded as fmaf).
+__device__ __forceinline__ void fma2(unsigned long long& d, unsigned long long a, unsigned long long b) {
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(d) : "l"(a), "l"(b));
 }
 
 template <bool AK, bool BK>
-__global__ void __launch_bounds__(kThreads, 2) k_sgemm(const Sgemm g) {
-  __shared__ __align__(16) float as[2][SK][SM + 4], bs[2][SK][SM + 4];
-  const int m0 = blockIdx.y * SM, n0 = blockIdx.x * SM;
-  const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
+__global__ void __launch_bounds__(kGemmThreads, 4) k_sgemm(const Sgemm g) {
+  __shared__ __align__(16) float as[2][SK][SM + 4], bs[2][SK][SN + 4];
+  const int m0 = blockIdx.y * SM, n0 = blockIdx.x * SN;
+  const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;  // 16 x 8 threads
   const int blocks = (g.K + SK - 1) / SK;
   const int kb0 = (int)((long long)blocks * blockIdx.z / g.slices), kb1 = (int)((long long)blocks * (blockIdx.z + 1) / g.slices);
-  float acc[8][8] = {};
-  float4 av[2], bv[2];
+  unsigned long long pair[8][4] = {};  // products of two columns each
+  Fetch<AK, SM> av;
+  Fetch<BK, SN> bv;
   if (kb0 < kb1) {
-    fetch<AK>(g.A, g.lda, g.M, g.a_cols, g.K, m0, kb0 * SK, av);
-    fetch<BK>(g.B, g.ldb, g.N, g.b_cols, g.K, n0, kb0 * SK, bv);
-    place<AK>(as[0], av);
-    place<BK>(bs[0], bv);
+    av.load(g.A, g.lda, g.M, g.a_cols, g.K, m0, kb0 * SK);
+    bv.load(g.B, g.ldb, g.N, g.b_cols, g.K, n0, kb0 * SK);
+    av.place(as[0]);
+    bv.place(bs[0]);
   }
   __syncthreads();
   for (int kb = kb0; kb < kb1; ++kb) {
     const int cur = (kb - kb0) & 1;
     const bool more = kb + 1 < kb1;
     if (more) {
-      fetch<AK>(g.A, g.lda, g.M, g.a_cols, g.K, m0, (kb + 1) * SK, av);
-      fetch<BK>(g.B, g.ldb, g.N, g.b_cols, g.K, n0, (kb + 1) * SK, bv);
+      av.load(g.A, g.lda, g.M, g.a_cols, g.K, m0, (kb + 1) * SK);
+      bv.load(g.B, g.ldb, g.N, g.b_cols, g.K, n0, (kb + 1) * SK);
     }
 #pragma unroll
     for (int k = 0; k < SK; ++k) {
-      float x[8], y[8];
+      float x[8];
       *reinterpret_cast<float4*>(x) = *reinterpret_cast<const float4*>(&as[cur][k][4 * ty]);
-      *reinterpret_cast<float4*>(x + 4) = *reinterpret_cast<const float4*>(&as[cur][k][64 + 4 * ty]);
-      *reinterpret_cast<float4*>(y) = *reinterpret_cast<const float4*>(&bs[cur][k][4 * tx]);
-      *reinterpret_cast<float4*>(y + 4) = *reinterpret_cast<const float4*>(&bs[cur][k][64 + 4 * tx]);
+      *reinterpret_cast<float4*>(x + 4) = *reinterpret_cast<const float4*>(&as[cur][k][32 + 4 * ty]);
+      const ulonglong2 y0 = *reinterpret_cast<const ulonglong2*>(&bs[cur][k][4 * tx]);
+      const ulonglong2 y1 = *reinterpret_cast<const ulonglong2*>(&bs[cur][k][64 + 4 * tx]);
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) acc[i][j] = fmaf(x[i], y[j], acc[i][j]);
+      for (int i = 0; i < 8; ++i) {
+        unsigned long long xx;
+        asm("mov.b64 %0, {%1, %1};" : "=l"(xx) : "f"(x[i]));
+        fma2(pair[i][0], xx, y0.x);
+        fma2(pair[i][1], xx, y0.y);
+        fma2(pair[i][2], xx, y1.x);
+        fma2(pair[i][3], xx, y1.y);
+      }
     }
     if (more) {
-      place<AK>(as[cur ^ 1], av);
-      place<BK>(bs[cur ^ 1], bv);
+      av.place(as[cur ^ 1]);
+      bv.place(bs[cur ^ 1]);
     }
     __syncthreads();
   }
+  float acc[8][8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      asm("mov.b64 {%0, %1}, %2;" : "=f"(acc[i][2 * j]), "=f"(acc[i][2 * j + 1]) : "l"(pair[i][j]));
   float* out = g.out + blockIdx.z * g.osz;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const int m = m0 + (i / 4) * 64 + 4 * ty + i % 4;
+    const int m = m0 + (i / 4) * 32 + 4 * ty + i % 4;
     if (m >= g.M) continue;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int n = n0 + (j / 4) * 64 + 4 * tx + j % 4;
-      if (n >= g.N) continue;
+    for (int j = 0; j < 8; j += 4) {
+      const int n = n0 + (j / 4) * 64 + 4 * tx;
       float* o = out + m * g.ldo + n;
-      *o = g.add ? *o + acc[i][j] : acc[i][j];
+      if (n + 4 <= g.N) {  // rows are a multiple of 4 apart
+        float4 v = make_float4(acc[i][j], acc[i][j + 1], acc[i][j + 2], acc[i][j + 3]);
+        if (g.add) {
+          const float4 w = *reinterpret_cast<const float4*>(o);
+          v = make_float4(w.x + v.x, w.y + v.y, w.z + v.z, w.w + v.w);
+        }
+        *reinterpret_cast<float4*>(o) = v;
+      } else {
+        for (int e = 0; e < 4 && n + e < g.N; ++e) o[e] = g.add ? o[e] + acc[i][j + e] : acc[i][j + e];
+      }
     }
   }
 }
 
 template <bool AK, bool BK>
 cudaError_t sgemm(const Sgemm& g, cudaStream_t st) {
-  k_sgemm<AK, BK><<<dim3((g.N + SM - 1) / SM, (g.M + SM - 1) / SM, g.slices), kThreads, 0, st>>>(g);
+  k_sgemm<AK, BK><<<dim3((g.N + SN - 1) / SN, (g.M + SM - 1) / SM, g.slices), kGemmThreads, 0, st>>>(g);
   return cudaGetLastError();
 }
 
@@ -277,9 +308,11 @@ Work work_of(const ipttt_xent_params& p, bool backward) {
     w.part = take((size_t)p.N * sizeof(float2) * (tc ? all / 128 : 1));
     w.tl = take((size_t)p.N * 4);
   } else {
-    // enough slices of K for gH's product to fill the SMs twice, each of at least 256 columns
-    const long long tiles = (long long)((p.N + 127) / 128) * ((p.d + 127) / 128);
-    w.slices = (int)std::max<long long>(1, std::min<long long>({(296 + tiles - 1) / tiles, w.piece / 256, 32}));
+    // enough slices of K for gH's product to fill the SMs (its blocks: four an SM in fp32, two
+    // in bf16), each of at least 256 columns
+    const long long tiles = (long long)((p.N + (tc ? 127 : SM - 1)) / (tc ? 128 : SM)) * ((p.d + 127) / 128);
+    const long long fill = tc ? 296 : 592;
+    w.slices = (int)std::max<long long>(1, std::min<long long>({fill / tiles, w.piece / 256, 32}));
     w.gH = take((size_t)p.N * p.d * 4 * w.slices);
   }
   w.total = off;
