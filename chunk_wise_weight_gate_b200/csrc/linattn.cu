@@ -6,6 +6,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "linattn.h"
 
@@ -360,16 +361,20 @@ int simt_segments(int B, int T, int H, int Da, int Dc, int* seg_chunks) {
 cudaError_t run_simt(const Pass& p, int dtype, cudaStream_t st) {
   const size_t smem = simt_smem(p.Da);
   const dim3 grid((p.Dc + kSlice - 1) / kSlice, p.B * p.H, p.segs);
-  cudaError_t e;
-  if (dtype == IPTTT_BF16) {
-    e = cudaFuncSetAttribute(k_pass<__nv_bfloat16>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  static std::atomic<bool> ready[64];  // room for the widest heads, once a device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!ready[dev].load()) {
+    const int most = (int)simt_smem(kMaxWidth);
+    e = cudaFuncSetAttribute(k_pass<__nv_bfloat16>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(k_pass<float>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
     if (e != cudaSuccess) return e;
-    k_pass<__nv_bfloat16><<<grid, kThreads, smem, st>>>(p);
-  } else {
-    e = cudaFuncSetAttribute(k_pass<float>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-    k_pass<float><<<grid, kThreads, smem, st>>>(p);
+    ready[dev].store(true);
   }
+  if (dtype == IPTTT_BF16) k_pass<__nv_bfloat16><<<grid, kThreads, smem, st>>>(p);
+  else k_pass<float><<<grid, kThreads, smem, st>>>(p);
   return cudaGetLastError();
 }
 
@@ -464,6 +469,7 @@ cudaError_t run_pass(const ipttt_linattn_params& p, Pass q, float* seg, bool hav
     const cudaError_t e = run_one(p, s, st);
     if (e != cudaSuccess) return e;
     ++*launches;
+    q.after_states = 1;
   }
   q.seg_in = seg;
   ++*launches;

@@ -40,6 +40,7 @@ struct Pass {
   const float* seg_in;           // [B][H][segs][Da][Dc]: the segments' own states (segs > 1)
   float* seg_state;              // the same array, written when out is null
   int segs, seg_chunks;          // segments of a row, chunks of each (the last may have fewer)
+  int after_states;              // the launch before is the pass for this one's segment states
   int whole;                     // (row, head) pairs b * H + h below this are not cut into segments
   int B, T, H, Da, Dc;
   int rev;

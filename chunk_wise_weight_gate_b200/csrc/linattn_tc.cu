@@ -21,6 +21,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "linattn.h"
 #include "tc.cuh"
@@ -232,6 +233,9 @@ __global__ void __launch_bounds__(Cfg<DA, DC, KIND == STATES>::THREADS, 1) k_pas
   __syncthreads();
   tc_fence_after();
   const uint32_t tm = *tmem_slot;
+  // The pass may start while the one for its segments' states still runs (it reads them at
+  // its cut segments' starts, and ends after it in any case).
+  if (STATE) launch_dependents();
   const bool rev = STATE ? p.rev != 0 : KIND == REVERSE;
   const int step = rev ? -1 : 1;
   // STATES has room for two chunks' lo halves and D, so that a chunk's scaling runs beside the last one's (4)
@@ -540,6 +544,7 @@ __global__ void __launch_bounds__(Cfg<DA, DC, KIND == STATES>::THREADS, 1) k_pas
         };
         if (p.init) add(p.init + bh * DA * DC, p.init_t, p.init_mul * reach(p, g, -1, lo, hi, start, CH));
         const int s0 = rev ? it.seg + 1 : 0, s1 = rev ? it.segs : it.seg;
+        if (s0 < s1) wait_for_launch_before();
         for (int s = s0; s < s1; ++s)
           add(p.seg_in + (bh * p.segs + s) * DA * DC, p.seg_t, reach(p, g, s, lo, hi, start, CH));
       }
@@ -683,6 +688,7 @@ __global__ void __launch_bounds__(Cfg<DA, DC, KIND == STATES>::THREADS, 1) k_pas
   }
 
   __syncthreads();
+  if (!STATE && threadIdx.x == 0) wait_for_launch_before();
   if (*abort_flag && threadIdx.x == 0) {
     // copies that were issued land before the block's shared memory is given back
     const uint32_t n = issued[0], na = issued[1];
@@ -701,17 +707,33 @@ template <int DA, int DC, int KIND>
 cudaError_t launch(const TcArgs& a, cudaStream_t st) {
   using Cf = Cfg<DA, DC, KIND == STATES>;
   static_assert(Cf::SMEM <= 232448 && Cf::NS >= 3, "ring");
-  cudaError_t e = cudaFuncSetAttribute(k_pass_tc<DA, DC, KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cf::SMEM);
+  // once a device: the shared memory, and a check of the registers.  The register split takes what
+  // the launch gives: with less, the state's warps would wait for good.
+  static std::atomic<bool> ready[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (KIND != STATES) {
-    // the register split takes what the launch gives: with less, the state's warps would wait for good
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!ready[dev].load()) {
+    e = cudaFuncSetAttribute(k_pass_tc<DA, DC, KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cf::SMEM);
+    if (e != cudaSuccess) return e;
     cudaFuncAttributes at;
     e = cudaFuncGetAttributes(&at, k_pass_tc<DA, DC, KIND>);
     if (e != cudaSuccess) return e;
-    if (at.numRegs < kRegsLaunch) return cudaErrorInvalidConfiguration;
+    if (KIND != STATES && at.numRegs < kRegsLaunch) return cudaErrorInvalidConfiguration;
+    ready[dev].store(true);
   }
-  k_pass_tc<DA, DC, KIND><<<std::min(a.items, device_sms()), Cf::THREADS, Cf::SMEM, st>>>(a);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3((unsigned)std::min(a.items, device_sms()));
+  cfg.blockDim = dim3(Cf::THREADS);
+  cfg.dynamicSmemBytes = Cf::SMEM;
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = a.p.after_states ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, k_pass_tc<DA, DC, KIND>, a);
 }
 
 template <int DA, int DC>
