@@ -234,7 +234,7 @@ __device__ __forceinline__ void row_epilogue(const Args& a, uint32_t tacc, int m
     if (on && n < s.cols) s.part[(long long)((s.v0 + n) / 128) * a.M + m] = make_float2(mx, sum);
     if (hit >= 0) s.target_logit[m] = tl;
   } else {
-    const float lse = part ? s.lse[m] : 0.0f, g = part ? s.gloss[m] : 0.0f;
+    const float lse = part ? s.lse[m] : 0.0f, g = part ? s.gloss[m] / s.unit[0] : 0.0f;
     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + (long long)m * a.ldo + n;
 #pragma unroll 1
     for (int q = 0; q < 4; ++q) {
@@ -562,7 +562,7 @@ cudaError_t run(const Args& a, int num_sms, cudaStream_t st) {
   }
   if (a.out_kind >= GO_ROW_STATS &&
       (a.mode != GM_PLAIN || a.ksplit > 1 || !a.softmax.targets || a.softmax.v0 % 256 != 0 || a.softmax.cols > a.N ||
-       (stats ? !a.softmax.part || !a.softmax.target_logit : !a.softmax.lse || !a.softmax.gloss)))
+       (stats ? !a.softmax.part || !a.softmax.target_logit : !a.softmax.lse || !a.softmax.gloss || !a.softmax.unit)))
     return cudaErrorInvalidValue;
   // Pairs where a 256-row tile is not mostly padding: M of at least 256; in the
   // per-chunk-rows form chunks of a multiple of 256 tokens; in the per-chunk-K

@@ -36,7 +36,7 @@ enum Out { GO_F32 = 0, GO_F32_ADD = 1, GO_BF16 = 2, GO_ROW_STATS = 3, GO_ROW_GRA
 // vocabulary's entries [v0, v0 + cols).
 //   GO_ROW_STATS: part[2 (v0 + n) / 256 + half][m] = (max l, sum exp(l - max)) over each 128 columns, and
 //                 target_logit[m] = l at the token's target, where it lies here
-//   GO_ROW_GRAD : out (bf16) = (exp(l - lse[m]) - [the target]) gloss[m]; 0 in rows left out
+//   GO_ROW_GRAD : out (bf16) = (exp(l - lse[m]) - [the target]) gloss[m] / unit[0]; 0 in rows left out
 // A token takes part when its target is not `ignore` and lies in [0, V).
 struct Softmax {
   const int64_t* targets;
@@ -46,6 +46,7 @@ struct Softmax {
   float* target_logit;
   const float* lse;
   const float* gloss;
+  const float* unit;
 };
 
 // A bf16 operand: a row-major {outer, rows, inner} array (inner contiguous), its rows `ld`

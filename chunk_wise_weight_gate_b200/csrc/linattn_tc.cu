@@ -11,13 +11,27 @@
 // decay to the chunk's end, is split in two bf16 halves (hi + lo, 2^-17 relative), so
 // the fp32 state is good to fp32-like accuracy; P and the operand copy of F are
 // rounded to bf16 once, like the inputs and outputs are.
-// Roles: warp 0 issues the TMA loads into a ring of tiles, one thread of warp 1 the
-// MMAs; warps 2-5 turn SC into P and write the output; warps 6-13 scale and split B
-// in place, hold the state (a row and a strip of columns a thread) and write its bf16
-// copy, the B operand of the next chunk's (2).
-// Per chunk of width 128: 131 KB of HBM traffic (20 us a GB/s per SM: 3.0 us at the
-// measured copy bandwidth over 148 SMs) against some 2600 clocks (1.4 us) of tensor
-// pipe, so HBM bounds it as long as the loads run ahead: the ring holds 5 tiles of 32 KB.
+//
+// Roles: warp 0 issues the TMA loads, a thread of warp 1 the MMAs (1) to (3), a thread of
+// warp 2 those of (4); 8 warps turn SC into P (two a quarter of the rows, 64 columns
+// each) and write the output (through the a tile's place and TMA stores); 8 warps scale
+// and split B in place, hold the state (a row and a strip of columns a thread) and write
+// its bf16 copy, the B operand of (2).  Every wait is bounded and reports IPTTT_ERR_TIMEOUT; where
+// a waiter may be a whole chunk behind, a pair of barriers is taken in turn (a parity
+// tells a phase only from its neighbours).
+//
+// What bounds it, at width 128: a chunk moves 131 KB (3.0 us an SM at the measured copy bandwidth
+// over 148 SMs) and takes 2600 clocks of tensor pipe (N = 128: 64 clocks a MMA).  Shared
+// memory is full (two a tiles, three b and c tiles, the lo half, the state's copy: 224 KB),
+// so a tile's load starts less than a chunk ahead, and a chunk takes 3.3 to 3.7 us: 148 heads of 2048
+// tokens 64 us, 310 MB at 4.8 TB/s (73% of the copy bandwidth).  Measured on the way there: descriptors
+// rebuilt for each MMA cost its issuing thread 100 clocks a MMA; loops unrolled as far as they go
+// overran the instruction caches (a third of all stalls); one issuing thread instead of
+// two: 68 us; tiles brought into L2 ahead of their loads: 72 us.
+//
+// Rows are cut into segments when rows and heads alone leave SMs idle: a first pass (STATES) forms
+// each segment's own state from b and c alone (1.5 to 1.7 us a chunk: 64 KB, HBM), and the full
+// pass starts each segment from their sum under the decay.
 #include <cuda_bf16.h>
 
 #include <algorithm>

@@ -34,7 +34,10 @@ constexpr int kThreads = 256;
 // blocks for four an SM.  300 tokens, 10007 words, d = 512: 84 us for the logits (37 TFLOP/s),
 // 71 for gH, 76 for gW; one product an instruction took 87, 80 and 88, 128 x 128 tiles of 256
 // threads 111, 132 and 97.
+// Few rows (a batch of a few tokens against the whole vocabulary, bound by reading W) take
+// 16-row tiles, 2 x 8 products a thread.
 constexpr int SM = 64, SN = 128, SK = 16, kGemmThreads = 128;
+constexpr int kFewRows = 32;  // at most so many rows take 16-row tiles
 struct Sgemm {
   const float *A, *B;
   float* out;
@@ -46,13 +49,15 @@ struct Sgemm {
 
 // The block's part of an operand for 16 k: WIDTH rows (or columns) from r0 on.
 template <bool KMAJOR, int WIDTH> struct Fetch {
-  static constexpr int N = WIDTH * SK / 4 / kGemmThreads;
+  static constexpr int N = (WIDTH * SK / 4 + kGemmThreads - 1) / kGemmThreads;
+  static constexpr bool WHOLE = N * kGemmThreads * 4 == WIDTH * SK;  // else threads past the end idle
   float4 v[N];
   __device__ __forceinline__ void load(const float* X, long long ld, int rows, int cols, int k1, int r0, int k0) {
 #pragma unroll
     for (int u = 0; u < N; ++u) {
       const int i = threadIdx.x + u * kGemmThreads;
       v[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (!WHOLE && i >= WIDTH * SK / 4) continue;
       if (KMAJOR) {
         const int r = r0 + i / 4, k = k0 + 4 * (i % 4);
         if (r < rows && k < k1) v[u] = *reinterpret_cast<const float4*>(X + r * ld + k);
@@ -66,6 +71,7 @@ template <bool KMAJOR, int WIDTH> struct Fetch {
 #pragma unroll
     for (int u = 0; u < N; ++u) {
       const int i = threadIdx.x + u * kGemmThreads;
+      if (!WHOLE && i >= WIDTH * SK / 4) continue;
       if (KMAJOR) {
         const int r = i / 4, k = 4 * (i % 4);
         s[k][r] = v[u].x;
@@ -84,15 +90,17 @@ __device__ __forceinline__ void fma2(unsigned long long& d, unsigned long long a
   asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(d) : "l"(a), "l"(b));
 }
 
-template <bool AK, bool BK>
+template <bool AK, bool BK, int TM>
 __global__ void __launch_bounds__(kGemmThreads, 4) k_sgemm(const Sgemm g) {
-  __shared__ __align__(16) float as[2][SK][SM + 4], bs[2][SK][SN + 4];
-  const int m0 = blockIdx.y * SM, n0 = blockIdx.x * SN;
+  constexpr int R = TM / 8;  // rows a thread
+  __shared__ __align__(16) float as[2][SK][TM + 4], bs[2][SK][SN + 4];
+  const int nt = (g.N + SN - 1) / SN;
+  const int m0 = blockIdx.x / nt * TM, n0 = blockIdx.x % nt * SN;
   const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;  // 16 x 8 threads
   const int blocks = (g.K + SK - 1) / SK;
   const int kb0 = (int)((long long)blocks * blockIdx.z / g.slices), kb1 = (int)((long long)blocks * (blockIdx.z + 1) / g.slices);
-  unsigned long long pair[8][4] = {};  // products of two columns each
-  Fetch<AK, SM> av;
+  unsigned long long pair[R][4] = {};  // products of two columns each
+  Fetch<AK, TM> av;
   Fetch<BK, SN> bv;
   if (kb0 < kb1) {
     av.load(g.A, g.lda, g.M, g.a_cols, g.K, m0, kb0 * SK);
@@ -110,13 +118,17 @@ __global__ void __launch_bounds__(kGemmThreads, 4) k_sgemm(const Sgemm g) {
     }
 #pragma unroll
     for (int k = 0; k < SK; ++k) {
-      float x[8];
-      *reinterpret_cast<float4*>(x) = *reinterpret_cast<const float4*>(&as[cur][k][4 * ty]);
-      *reinterpret_cast<float4*>(x + 4) = *reinterpret_cast<const float4*>(&as[cur][k][32 + 4 * ty]);
+      float x[R];
+      if constexpr (R == 8) {
+        *reinterpret_cast<float4*>(x) = *reinterpret_cast<const float4*>(&as[cur][k][4 * ty]);
+        *reinterpret_cast<float4*>(x + 4) = *reinterpret_cast<const float4*>(&as[cur][k][32 + 4 * ty]);
+      } else {
+        *reinterpret_cast<float2*>(x) = *reinterpret_cast<const float2*>(&as[cur][k][2 * ty]);
+      }
       const ulonglong2 y0 = *reinterpret_cast<const ulonglong2*>(&bs[cur][k][4 * tx]);
       const ulonglong2 y1 = *reinterpret_cast<const ulonglong2*>(&bs[cur][k][64 + 4 * tx]);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < R; ++i) {
         unsigned long long xx;
         asm("mov.b64 %0, {%1, %1};" : "=l"(xx) : "f"(x[i]));
         fma2(pair[i][0], xx, y0.x);
@@ -131,16 +143,16 @@ __global__ void __launch_bounds__(kGemmThreads, 4) k_sgemm(const Sgemm g) {
     }
     __syncthreads();
   }
-  float acc[8][8];
+  float acc[R][8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
+  for (int i = 0; i < R; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j)
       asm("mov.b64 {%0, %1}, %2;" : "=f"(acc[i][2 * j]), "=f"(acc[i][2 * j + 1]) : "l"(pair[i][j]));
   float* out = g.out + blockIdx.z * g.osz;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int m = m0 + (i / 4) * 32 + 4 * ty + i % 4;
+  for (int i = 0; i < R; ++i) {
+    const int m = m0 + (R == 8 ? (i / 4) * 32 + 4 * ty + i % 4 : 2 * ty + i);
     if (m >= g.M) continue;
 #pragma unroll
     for (int j = 0; j < 8; j += 4) {
@@ -162,7 +174,12 @@ __global__ void __launch_bounds__(kGemmThreads, 4) k_sgemm(const Sgemm g) {
 
 template <bool AK, bool BK>
 cudaError_t sgemm(const Sgemm& g, cudaStream_t st) {
-  k_sgemm<AK, BK><<<dim3((g.N + SN - 1) / SN, (g.M + SM - 1) / SM, g.slices), kGemmThreads, 0, st>>>(g);
+  const int tm = g.M <= kFewRows ? 16 : SM;
+  const long long tiles = (long long)((g.N + SN - 1) / SN) * ((g.M + tm - 1) / tm);
+  if (tiles > 0x7fffffffLL) return cudaErrorInvalidValue;
+  const dim3 grid((unsigned)tiles, 1, g.slices);
+  if (tm == 16) k_sgemm<AK, BK, 16><<<grid, kGemmThreads, 0, st>>>(g);
+  else k_sgemm<AK, BK, SM><<<grid, kGemmThreads, 0, st>>>(g);
   return cudaGetLastError();
 }
 
@@ -236,10 +253,32 @@ __global__ void __launch_bounds__(kThreads) k_row_join(const float2* part, int p
   if (threadIdx.x % 32 == 0 && at < N) finish_row(at, v, tl[at], V, targets, ignore, loss, lse, status);
 }
 
-// Reports targets that are neither in the vocabulary nor the one to leave out.
-__global__ void k_check_targets(const int64_t* targets, int N, int V, int64_t ignore, int* status) {
-  const int n = blockIdx.x * blockDim.x + threadIdx.x;
-  if (n < N && (targets[n] < 0 || targets[n] >= V) && targets[n] != ignore) set_status(status, IPTTT_ERR_ARG);
+// bf16: p is formed with gloss divided by its largest magnitude, unit[0], which goes onto the
+// products' fp32 results instead.  For a mean every row's gloss is the same, and the target's p
+// - 1, nearly -1, is then as good as exact, where -gloss would be off by the same rounding in
+// every row.  Also reports targets that are neither in the vocabulary nor the one to leave out.
+// One block.
+__global__ void __launch_bounds__(1024) k_unit(const int64_t* targets, const float* gloss, int N, int V, int64_t ignore,
+                                               float* unit, int* status) {
+  __shared__ float sh[32];
+  float top = 0.0f;
+  for (int n = threadIdx.x; n < N; n += 1024) {
+    const int64_t t = targets[n];
+    if (t == ignore) continue;
+    if (t < 0 || t >= V) set_status(status, IPTTT_ERR_ARG);
+    else top = fmaxf(top, fabsf(gloss[n]));
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  if (threadIdx.x % 32 == 0) sh[threadIdx.x / 32] = top;
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    top = sh[threadIdx.x];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    // no gradient at all, or one that is not finite, is left as it is
+    if (threadIdx.x == 0) unit[0] = top > 0.0f && top < INFINITY ? top : 1.0f;
+  }
 }
 
 // fp32: p = (exp(l - lse) - onehot) gloss for the piece's columns; 0 in the padding.
@@ -259,13 +298,15 @@ __global__ void __launch_bounds__(kThreads) k_row_grad(float* l, long long ld, i
   }
 }
 
-// gH (in T) = the sum of the fp32 slices, in slice order.
+// gH (in T) = the sum of the fp32 slices, in slice order, times *unit (null: 1).
 template <typename T>
-__global__ void __launch_bounds__(kThreads) k_sum_slices(const float* part, T* out, long long n, int slices) {
+__global__ void __launch_bounds__(kThreads) k_sum_slices(const float* part, T* out, long long n, int slices,
+                                                       const float* unit) {
+  const float f = unit ? *unit : 1.0f;
   for (long long i = blockIdx.x * (long long)kThreads + threadIdx.x; i < n; i += (long long)gridDim.x * kThreads) {
     float s = part[i];
     for (int q = 1; q < slices; ++q) s += part[q * n + i];
-    out[i] = from_f<T>(s);
+    out[i] = from_f<T>(s * f);
   }
 }
 
@@ -287,7 +328,7 @@ ipttt_status check(const ipttt_xent_params* p) {
 struct Work {
   int piece;  // vocabulary rows at a time, a multiple of 256
   int slices; // partial sums of gH: slices of a piece's columns
-  size_t p, part, tl, gH, total;  // p: fp32 logits and p, or bf16 p
+  size_t p, part, tl, gH, unit, total;  // p: fp32 logits and p, or bf16 p
 };
 
 Work work_of(const ipttt_xent_params& p, bool backward) {
@@ -310,10 +351,12 @@ Work work_of(const ipttt_xent_params& p, bool backward) {
   } else {
     // enough slices of K for gH's product to fill the SMs (its blocks: four an SM in fp32, two
     // in bf16), each of at least 256 columns
-    const long long tiles = (long long)((p.N + (tc ? 127 : SM - 1)) / (tc ? 128 : SM)) * ((p.d + 127) / 128);
+    const int rows = tc ? 128 : p.N <= kFewRows ? 16 : SM;
+    const long long tiles = (long long)((p.N + rows - 1) / rows) * ((p.d + 127) / 128);
     const long long fill = tc ? 296 : 592;
     w.slices = (int)std::max<long long>(1, std::min<long long>({fill / tiles, w.piece / 256, 32}));
     w.gH = take((size_t)p.N * p.d * 4 * w.slices);
+    w.unit = take(4);
   }
   w.total = off;
   return w;
@@ -385,9 +428,9 @@ cudaError_t backward(const ipttt_xent_params& p, const Work& w, const void* H, c
   float* acc = reinterpret_cast<float*>(ws + w.gH);
   const long long nd = (long long)p.N * p.d;
   const bool tc = p.dtype == IPTTT_BF16;
+  float* unit = reinterpret_cast<float*>(ws + w.unit);
   if (tc) {
-    k_check_targets<<<(p.N + kThreads - 1) / kThreads, kThreads, 0, st>>>(targets, p.N, p.V, p.ignore_index,
-                                                                           device_status());
+    k_unit<<<1, 1024, 0, st>>>(targets, gloss, p.N, p.V, p.ignore_index, unit, device_status());
     ++*launches;
   }
   int all_slices = 0;
@@ -421,6 +464,7 @@ cudaError_t backward(const ipttt_xent_params& p, const Work& w, const void* H, c
     l.ldo = w.piece;
     l.softmax.lse = lse;
     l.softmax.gloss = gloss;
+    l.softmax.unit = unit;
     e = gemm::run(l, device_sms(), st);
     if (e != cudaSuccess) return e;
     gemm::Args a{};
@@ -449,6 +493,7 @@ cudaError_t backward(const ipttt_xent_params& p, const Work& w, const void* H, c
     b.N = p.d;
     b.K = p.N;
     b.out_kind = gemm::GO_BF16;
+    b.scale = unit;
     b.out = static_cast<__nv_bfloat16*>(gW) + (long long)v0 * p.d;
     b.ldo = p.d;
     b.status = device_status();
@@ -457,8 +502,8 @@ cudaError_t backward(const ipttt_xent_params& p, const Work& w, const void* H, c
     *launches += 3;
   }
   const unsigned grid = (unsigned)std::min<long long>((nd + kThreads - 1) / kThreads, 148 * 16);
-  if (p.dtype == IPTTT_F32) k_sum_slices<<<grid, kThreads, 0, st>>>(acc, static_cast<float*>(gH), nd, all_slices);
-  else k_sum_slices<<<grid, kThreads, 0, st>>>(acc, static_cast<__nv_bfloat16*>(gH), nd, all_slices);
+  if (p.dtype == IPTTT_F32) k_sum_slices<<<grid, kThreads, 0, st>>>(acc, static_cast<float*>(gH), nd, all_slices, nullptr);
+  else k_sum_slices<<<grid, kThreads, 0, st>>>(acc, static_cast<__nv_bfloat16*>(gH), nd, all_slices, unit);
   ++*launches;
   return cudaGetLastError();
 }
