@@ -30,7 +30,8 @@ namespace ipttt {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kTokens = 8;        // tokens of a tile (1 where there are few)
+constexpr int kTokens = 8;        // tokens of a forward tile (1 where there are few)
+constexpr int kMaxTokens = 32;    // of a backward tile
 constexpr int kMaxD = 256;
 constexpr int kForwardBlocks = 444, kBackwardBlocks = 296;  // most blocks: 3 and 2 per SM, as their registers allow
 
@@ -40,7 +41,9 @@ struct QkArgs {
   const long long* pos;
   void *qo, *ko;                 // forward: the outputs; backward: gq, gk
   long long ldq, ldk, ldqo, ldko, ldgq, ldgk;
-  float* parts;                  // backward: [2][blocks][D]
+  float* parts;                  // backward: [blocks][D]
+  int qblocks, blocks;           // backward: blocks that take q, all blocks
+  int qshift, kshift;            // backward: their tiles' tokens
   long long tokens;
   int Hq, Hk, D, R, interleaved;
   int shift;                     // tiles of 1 << shift tokens
@@ -272,49 +275,10 @@ __global__ void __launch_bounds__(kThreads, 3) k_qk_forward(const QkArgs a) {
   }
 }
 
-// As forward_heads, a round of x and gy ahead; the lane's share of the weight gradient is added to gw.
-template <typename T, int E, int G>
-__device__ __forceinline__ void backward_heads(const QkArgs& a, const LanePlace& lp, const Turn<E, true>& turn,
-                                               const Heads<T, E>& hx, const Heads<T, E>& hg, const T* w, T* gx,
-                                               float* gw) {
-  float wv[E];
-  load_weight<T, E>(wv, w, lp);
-  Piece<T, E> rx{}, rg{};
-  hx.load(rx, lp, a.D, 0);
-  hg.load(rg, lp, a.D, 0);
-  for (int h0 = 0; h0 < hx.H; h0 += hx.step) {
-    const int h = h0 + hx.first;
-    const bool here = hx.on && h < hx.H;
-    float v[E], z[E], ss[2] = {}, ux[2] = {};
-    rx.unpack(v);
-    rg.unpack(z);
-    hx.load(rx, lp, a.D, h0 + hx.step);
-    hg.load(rg, lp, a.D, h0 + hx.step);
-    turn.apply(z, a.interleaved);
-#pragma unroll
-    for (int i = 0; i < E; ++i) {
-      ss[i & 1] = fmaf(v[i], v[i], ss[i & 1]);
-      ux[i & 1] = fmaf(z[i] * wv[i], v[i], ux[i & 1]);
-    }
-    const float r = rsqrtf(group_sum<G>(ss[0] + ss[1]) * a.inv_d + a.eps);
-    const float m = -group_sum<G>(ux[0] + ux[1]) * r * a.inv_d;  // -mean(gz w xh)
-    if (here) {
-#pragma unroll
-      for (int i = 0; i < E; ++i) {
-        const float xh = v[i] * r;
-        gw[i] = fmaf(z[i], xh, gw[i]);
-        z[i] = fmaf(xh, m, z[i] * wv[i]) * r;
-      }
-      Piece<T, E>::store(gx + h * a.D, lp.o0, lp.o1, z);
-    }
-  }
-}
-
 // The block's sum of every element's weight gradient, in the order of its groups of lanes.
 template <int E, int G>
 __device__ __forceinline__ void store_parts(const LanePlace& lp, const float* gw, float* sh, float* out, int D) {
   constexpr int kGroups = kThreads / G;
-  __syncthreads();  // sh's last readers
   if (lp.used) Piece<float, E>::store(sh + (threadIdx.x / G) * (G * E), lp.o0, lp.o1, gw);
   __syncthreads();
   for (int e = threadIdx.x; e < D; e += kThreads) {
@@ -324,43 +288,82 @@ __device__ __forceinline__ void store_parts(const LanePlace& lp, const float* gw
   }
 }
 
+// The first a.qblocks blocks take q, the rest k (in proportion to their heads), so that a thread holds one
+// operand's weight and weight gradient alone: with both, registers spill.  A round of x and
+// gy is on its way while the last one is worked on.
 template <typename T, int E, int G>
 __global__ void __launch_bounds__(kThreads, 2) k_qk_backward(const QkArgs a) {
   constexpr int kGroups = kThreads / G;
-  __shared__ __align__(16) float cs[kTokens * kMaxD / 2], sn[kTokens * kMaxD / 2];
+  __shared__ __align__(16) float cs[kMaxTokens * kMaxD / 2], sn[kMaxTokens * kMaxD / 2];
   __shared__ __align__(16) float sh[kThreads * E];  // [kGroups][G E]
+  const bool is_q = (int)blockIdx.x < a.qblocks;
+  const int block = is_q ? blockIdx.x : blockIdx.x - a.qblocks, blocks = is_q ? a.qblocks : gridDim.x - a.qblocks;
+  const T* x = static_cast<const T*>(is_q ? a.q : a.k);
+  const T* gy = static_cast<const T*>(is_q ? a.gqo : a.gko);
+  T* gx = static_cast<T*>(is_q ? a.qo : a.ko);
+  const long long ldx = is_q ? a.ldq : a.ldk, ldgy = is_q ? a.ldqo : a.ldko, ldgx = is_q ? a.ldgq : a.ldgk;
+  const int H = is_q ? a.Hq : a.Hk, shift = is_q ? a.qshift : a.kshift;
   const LanePlace lp = place_of<E>(a, threadIdx.x % G);
-  const int grp = threadIdx.x / G, t = grp & ((1 << a.shift) - 1), first = grp >> a.shift, step = kGroups >> a.shift;
-  float gq[E] = {}, gk[E] = {};
-  for (long long t0 = (long long)blockIdx.x << a.shift; t0 < a.tokens; t0 += (long long)gridDim.x << a.shift) {
+  const int grp = threadIdx.x / G, t = grp & ((1 << shift) - 1), first = grp >> shift, step = kGroups >> shift;
+  float wv[E], gw[E] = {};
+  load_weight<T, E>(wv, static_cast<const T*>(is_q ? a.wq : a.wk), lp);
+  for (long long t0 = (long long)block << shift; t0 < a.tokens; t0 += (long long)blocks << shift) {
     const long long tok = t0 + t;
-    const int n = (int)min(1ll << a.shift, a.tokens - t0);
+    const int n = (int)min(1ll << shift, a.tokens - t0);
+    const bool on = t < n && lp.used;
+    const Heads<T, E> hx{x + tok * ldx, H, first, step, on}, hg{gy + tok * ldgy, H, first, step, on};
+    T* out = gx + tok * ldgx;
+    Piece<T, E> rx{}, rg{};
+    hx.load(rx, lp, a.D, 0);
+    hg.load(rg, lp, a.D, 0);
     __syncthreads();  // the last tile's angles have been read
     fill_angles<T>(a, t0, n, cs, sn);
     __syncthreads();
     Turn<E, true> turn;
     if (lp.rotates && t < n) turn.read(cs + t * (kMaxD / 2) + lp.pair, sn + t * (kMaxD / 2) + lp.pair);
     else turn.none();
-    const bool on = t < n && lp.used;
-    const Heads<T, E> q{static_cast<const T*>(a.q) + tok * a.ldq, a.Hq, first, step, on};
-    const Heads<T, E> k{static_cast<const T*>(a.k) + tok * a.ldk, a.Hk, first, step, on};
-    const Heads<T, E> gqo{static_cast<const T*>(a.gqo) + tok * a.ldqo, a.Hq, first, step, on};
-    const Heads<T, E> gko{static_cast<const T*>(a.gko) + tok * a.ldko, a.Hk, first, step, on};
-    backward_heads<T, E, G>(a, lp, turn, q, gqo, static_cast<const T*>(a.wq), static_cast<T*>(a.qo) + tok * a.ldgq, gq);
-    backward_heads<T, E, G>(a, lp, turn, k, gko, static_cast<const T*>(a.wk), static_cast<T*>(a.ko) + tok * a.ldgk, gk);
+#pragma unroll 1
+    for (int h0 = 0; h0 < H; h0 += step) {
+      const int h = h0 + first;
+      float v[E], z[E], ss[2] = {}, ux[2] = {};
+      rx.unpack(v);
+      rg.unpack(z);
+      hx.load(rx, lp, a.D, h0 + step);
+      hg.load(rg, lp, a.D, h0 + step);
+      turn.apply(z, a.interleaved);
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        ss[i & 1] = fmaf(v[i], v[i], ss[i & 1]);
+        ux[i & 1] = fmaf(z[i] * wv[i], v[i], ux[i & 1]);
+      }
+      const float r = rsqrtf(group_sum<G>(ss[0] + ss[1]) * a.inv_d + a.eps);
+      const float m = -group_sum<G>(ux[0] + ux[1]) * r * a.inv_d;  // -mean(gz w xh)
+      if (on && h < H) {
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+          const float xh = v[i] * r;
+          gw[i] = fmaf(z[i], xh, gw[i]);
+          z[i] = fmaf(xh, m, z[i] * wv[i]) * r;
+        }
+        Piece<T, E>::store(out + h * a.D, lp.o0, lp.o1, z);
+      }
+    }
   }
-  store_parts<E, G>(lp, gq, sh, a.parts + (size_t)blockIdx.x * a.D, a.D);
-  store_parts<E, G>(lp, gk, sh, a.parts + (size_t)(gridDim.x + blockIdx.x) * a.D, a.D);
+  store_parts<E, G>(lp, gw, sh, a.parts + (size_t)blockIdx.x * a.D, a.D);
 }
 
 // gw[e] = the blocks' partial sums, in 64 bits and a fixed order; one block of 32 x 32
 // threads takes 32 elements of gwq (y = 0) or gwk (y = 1).
-__global__ void __launch_bounds__(1024) k_qk_weight_grad(const float* parts, float* gwq, float* gwk, int blocks, int D) {
+__global__ void __launch_bounds__(1024) k_qk_weight_grad(const float* parts, float* gwq, float* gwk, int qblocks,
+                                                         int blocks, int D) {
   __shared__ double sh[32][33];
   const int e = blockIdx.x * 32 + threadIdx.x;
+  const int lo = blockIdx.y == 0 ? 0 : qblocks, hi = blockIdx.y == 0 ? qblocks : blocks;
   double s = 0.0;
-  if (e < D)
-    for (int i = threadIdx.y; i < blocks; i += 32) s += parts[((size_t)blockIdx.y * blocks + i) * D + e];
+  if (e < D) {
+#pragma unroll 4
+    for (int i = lo + threadIdx.y; i < hi; i += 32) s += parts[(size_t)i * D + e];
+  }
   sh[threadIdx.x][threadIdx.y] = s;
   __syncthreads();
   // warp y sums element y
@@ -411,7 +414,43 @@ QkArgs args_of(const ipttt_qk_params& p) {
 }
 
 long long tiles_of(const QkArgs& a) { return (a.tokens + (1ll << a.shift) - 1) >> a.shift; }
-int grad_blocks(const QkArgs& a) { return (int)std::min<long long>(kBackwardBlocks, tiles_of(a)); }
+
+// Lanes and elements a lane of a vector: 16 elements where D and R are multiples of 16, else 8; the
+// fewest lanes that hold D.
+struct Form {
+  int elements, lanes;
+};
+Form form_of(int D, int R) {
+  const int e = D % 16 == 0 && R % 16 == 0 ? 16 : 8;
+  const int base = 64 / e;
+  return {e, D <= 64 ? base : D <= 128 ? 2 * base : 4 * base};
+}
+
+// The backward's tiles and blocks.  A tile holds so many tokens (up to 32) that a group of lanes has
+// at least four heads of its token, and that every block still has one; the blocks, as many as
+// run at once, are shared between q and k by what their tiles cost: the rounds of
+// heads, and about two rounds for the angles and the first loads.
+void share_blocks(QkArgs& a) {
+  const int groups = kThreads / form_of(a.D, a.R).lanes, most = kBackwardBlocks;
+  auto shift_of = [&](int H) {
+    int s = 0;
+    while ((2 << s) <= std::min(groups, kMaxTokens) && (groups >> s) > std::max(1, H / 4) &&
+           (a.tokens >> (s + 1)) >= most / 2)
+      ++s;
+    return s;
+  };
+  auto tiles = [&](int shift) { return (a.tokens + (1ll << shift) - 1) >> shift; };
+  auto cost = [&](int H, int shift) {
+    const int step = groups >> shift;
+    return tiles(shift) * ((H + step - 1) / step + 2);
+  };
+  a.qshift = shift_of(a.Hq);
+  a.kshift = shift_of(a.Hk);
+  const long long cq = cost(a.Hq, a.qshift), ck = cost(a.Hk, a.kshift);
+  const int k = (int)std::min<long long>(most - 1, std::max<long long>(1, (most * ck + (cq + ck) / 2) / (cq + ck)));
+  a.qblocks = (int)std::min<long long>(most - k, tiles(a.qshift));
+  a.blocks = a.qblocks + (int)std::min<long long>(k, tiles(a.kshift));
+}
 
 struct Forward {
   template <typename T, int E, int G>
@@ -422,20 +461,20 @@ struct Forward {
 struct Backward {
   template <typename T, int E, int G>
   static void launch(const QkArgs& a, cudaStream_t st) {
-    k_qk_backward<T, E, G><<<(unsigned)grad_blocks(a), kThreads, 0, st>>>(a);
+    k_qk_backward<T, E, G><<<(unsigned)a.blocks, kThreads, 0, st>>>(a);
   }
 };
 
-// 16 elements a lane where D and R are multiples of 16, else 8; the fewest lanes that hold D.
 template <typename K, typename T>
 cudaError_t launch(const QkArgs& a, cudaStream_t st) {
-  if (a.D % 16 == 0 && a.R % 16 == 0) {
-    if (a.D <= 64) K::template launch<T, 16, 4>(a, st);
-    else if (a.D <= 128) K::template launch<T, 16, 8>(a, st);
+  const Form f = form_of(a.D, a.R);
+  if (f.elements == 16) {
+    if (f.lanes == 4) K::template launch<T, 16, 4>(a, st);
+    else if (f.lanes == 8) K::template launch<T, 16, 8>(a, st);
     else K::template launch<T, 16, 16>(a, st);
   } else {
-    if (a.D <= 64) K::template launch<T, 8, 8>(a, st);
-    else if (a.D <= 128) K::template launch<T, 8, 16>(a, st);
+    if (f.lanes == 8) K::template launch<T, 8, 8>(a, st);
+    else if (f.lanes == 16) K::template launch<T, 8, 16>(a, st);
     else K::template launch<T, 8, 32>(a, st);
   }
   return cudaGetLastError();
@@ -483,8 +522,9 @@ ipttt_status ipttt_qk_norm_rope(const ipttt_qk_params* p, const void* q, const v
 
 size_t ipttt_qk_norm_rope_backward_workspace_size(const ipttt_qk_params* p) {
   if (check(p) != IPTTT_OK) return 0;
-  const QkArgs a = args_of(*p);
-  return ((size_t)2 * grad_blocks(a) * a.D * sizeof(float) + 255) & ~size_t(255);
+  QkArgs a = args_of(*p);
+  share_blocks(a);
+  return ((size_t)a.blocks * a.D * sizeof(float) + 255) & ~size_t(255);
 }
 
 ipttt_status ipttt_qk_norm_rope_backward(const ipttt_qk_params* p, const void* q, const void* k, const void* wq,
@@ -514,10 +554,11 @@ ipttt_status ipttt_qk_norm_rope_backward(const ipttt_qk_params* p, const void* q
   a.qo = gq;
   a.ko = gk;
   a.parts = static_cast<float*>(workspace);
+  share_blocks(a);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e = p->dtype == IPTTT_BF16 ? launch<Backward, __nv_bfloat16>(a, st) : launch<Backward, float>(a, st);
   if (e == cudaSuccess) {
-    k_qk_weight_grad<<<dim3((a.D + 31) / 32, 2), dim3(32, 32), 0, st>>>(a.parts, gwq, gwk, grad_blocks(a), a.D);
+    k_qk_weight_grad<<<dim3((a.D + 31) / 32, 2), dim3(32, 32), 0, st>>>(a.parts, gwq, gwk, a.qblocks, a.blocks, a.D);
     e = cudaGetLastError();
   }
   if (e != cudaSuccess) return cuda_fail("qk_norm_rope_backward", e);
