@@ -319,3 +319,22 @@ def test_cross_entropy_far_logits_and_empty_batches(dtype):
     pad = pkg.CrossEntropyConfig(N=70, V=900, d=64, dtype=dtype, ignore_index=7)
     t[t < 0] = 7
     assert not pkg.cross_entropy(pad, H, W, t)[0][t == 7].any() and status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N,V,d,piece", [(3, 300, 64, 256), (300, 1000, 128, 512)])
+def test_cross_entropy_rows_left_out_reach_nothing(N, V, d, piece, dtype):
+    cfg, H, W, t = xent_case(N, V, d, dtype, piece=piece)
+    gl = ref.rand(5, N).cuda()
+    loss, lse = pkg.cross_entropy(cfg, H, W, t)
+    want = pkg.cross_entropy_backward(cfg, H, W, t, lse, gl)
+    out = t == -100
+    assert bool(out.any())
+    for bad in (math.nan, math.inf):
+        h, g = H.clone(), gl.clone()
+        h[out], g[out] = bad, bad
+        loss2, lse2 = pkg.cross_entropy(cfg, h, W, t)
+        assert torch.equal(loss2, loss) and torch.equal(lse2[~out], lse[~out])
+        got = pkg.cross_entropy_backward(cfg, h, W, t, lse2, g)
+        assert torch.equal(got["H"], want["H"]) and torch.equal(got["W"], want["W"])
+    assert status() == 0
