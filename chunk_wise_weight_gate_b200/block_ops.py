@@ -168,7 +168,7 @@ def qk_norm_rope(cfg: QKNormRopeConfig, q, k, wq, wk, inv_freq, positions, *, q_
 def qk_norm_rope_backward(cfg: QKNormRopeConfig, q, k, wq, wk, inv_freq, positions, gq_out, gk_out, *, gq=None,
                           gk=None, workspace=None, stream=None):
     """Gradients of <gq_out, q_out> + <gk_out, k_out>: a dict with q and k (the call's dtype,
-    packed unless gq, gk are given; they may be gq_out, gk_out) and wq, wk (fp32)."""
+    packed unless gq, gk are given; they may be gq_out, gk_out, or q, k) and wq, wk (fp32)."""
     ptrs, ldq, ldk, sq, sk, dt, dev = _qk_inputs(cfg, q, k, wq, wk, inv_freq, positions)
     pgq, ldqo = _tokens(gq_out, "gq_out", sq, dt, dev)
     pgk, ldko = _tokens(gk_out, "gk_out", sk, dt, dev)

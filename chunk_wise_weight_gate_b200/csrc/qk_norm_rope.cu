@@ -504,7 +504,8 @@ ipttt_status ipttt_qk_norm_rope(const ipttt_qk_params* p, const void* q, const v
     return IPTTT_ERR_ALIGN;
   QkArgs a = args_of(*p);
   // in place means the same elements: another stride would write vectors not yet read
-  if ((q == q_out && a.ldq != a.ldqo) || (k == k_out && a.ldk != a.ldko)) return IPTTT_ERR_ARG;
+  if ((q == q_out && a.ldq != a.ldqo) || (k == k_out && a.ldk != a.ldko) || q == k_out || k == q_out)
+    return IPTTT_ERR_ARG;
   a.q = q;
   a.k = k;
   a.wq = wq;
@@ -542,7 +543,9 @@ ipttt_status ipttt_qk_norm_rope_backward(const ipttt_qk_params* p, const void* q
   if (!workspace || workspace_bytes < ipttt_qk_norm_rope_backward_workspace_size(p)) return IPTTT_ERR_WORKSPACE;
   if (reinterpret_cast<uintptr_t>(workspace) % 256) return IPTTT_ERR_ALIGN;
   QkArgs a = args_of(*p);
-  if ((gq == gqo && a.ldgq != a.ldqo) || (gk == gko && a.ldgk != a.ldko)) return IPTTT_ERR_ARG;
+  if ((gq == gqo && a.ldgq != a.ldqo) || (gk == gko && a.ldgk != a.ldko) || (gq == q && a.ldgq != a.ldq) ||
+      (gk == k && a.ldgk != a.ldk) || gq == k || gq == gko || gk == q || gk == gqo)
+    return IPTTT_ERR_ARG;
   a.q = q;
   a.k = k;
   a.wq = wq;

@@ -565,6 +565,7 @@ ipttt_status ipttt_xent_backward(const ipttt_xent_params* p, const void* H, cons
   const ipttt_status rc = check(p);
   if (rc != IPTTT_OK) return rc;
   if (!H || !W || !targets || !lse || !gloss || !gH || !gW) return IPTTT_ERR_ARG;
+  if (gW == W || gW == H || gH == W || gH == H) return IPTTT_ERR_ARG;
   if (!aligned({H, W, gH, gW}, 16) || !aligned({targets}, 8) || !aligned({lse, gloss}, 4)) return IPTTT_ERR_ALIGN;
   const Work w = work_of(*p, true);
   if (!workspace || workspace_bytes < w.total) return IPTTT_ERR_WORKSPACE;

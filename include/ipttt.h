@@ -376,10 +376,12 @@ IPTTT_API ipttt_status ipttt_backward(const ipttt_params* p, const void* H, cons
  * Operators around the layer: what a block puts before the MLP (norms of queries
  * and keys with the position rotation, linear attention with a decay for each
  * head) and the loss that the model trains with.  The conventions at the top of
- * this file hold: device pointers owned by the caller and 16-byte aligned (the
- * state arrays and workspaces 256-byte), nothing allocated, asynchronous on
- * `stream` of the current device, argument errors returned before any launch,
- * results deterministic run to run.  A workspace holds nothing between calls.
+ * this file hold: device pointers owned by the caller and 16-byte aligned
+ * (workspaces 256-byte), nothing allocated, asynchronous on `stream` of the
+ * current device, argument errors returned before any launch, results
+ * deterministic run to run.  A workspace holds nothing between calls.  No output
+ * overlaps an input or another output, except where a call says that it may be one;
+ * an output that is an input's pointer all the same is refused (IPTTT_ERR_ARG).
  * Token tensors [B, T, heads, width] are read through a token stride: the elements
  * between a token and the next (b, t) -> (b*T + t) * ld, heads packed within a
  * token; 0 means packed tokens (heads * width).  Strides are multiples of 8
@@ -413,7 +415,7 @@ IPTTT_API ipttt_status ipttt_qk_norm_rope(const ipttt_qk_params* p, const void* 
                                           const void* wk, const double* inv_freq, const int64_t* positions,
                                           void* q_out, void* k_out, void* stream);
 /* Gradients of <gqo, q_out> + <gko, k_out>: gq, gk in the call's dtype, gwq and gwk [D]
- * in fp32.  gq may be gqo itself (same pointer and stride), gk gko. */
+ * in fp32.  gq may be gqo or q itself (same pointer and stride), gk gko or k. */
 IPTTT_API size_t ipttt_qk_norm_rope_backward_workspace_size(const ipttt_qk_params* p);
 IPTTT_API ipttt_status ipttt_qk_norm_rope_backward(const ipttt_qk_params* p, const void* q, const void* k,
                                                    const void* wq, const void* wk, const double* inv_freq,

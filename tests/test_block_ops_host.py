@@ -175,3 +175,20 @@ def test_binding_refuses_what_it_cannot_take():
         pkg.cross_entropy(pkg.CrossEntropyConfig(3, 9, 64, dtype="f32"), H, W, t.int())
     with pytest.raises(ValueError, match="CUDA"):
         pkg.cross_entropy(pkg.CrossEntropyConfig(3, 9, 64, dtype="f32"), H, W, t)
+
+
+def test_outputs_that_are_inputs_are_refused():
+    for i in range(3):  # q, k, v
+        assert la_forward(la(), O=FAKE[i]) == 1
+        assert la_step(la(T=1), o=FAKE[i]) == 1
+        assert la_backward(la(), gq=FAKE[i]) == 1
+    assert la_backward(la(), gq=FAKE[5]) == 1  # gO
+    L = ip.lib()
+    assert qk_call(qk(), FAKE[:6] + [FAKE[1], FAKE[7]]) == 1  # q_out is k
+    assert qk_call(qk(), FAKE[:6] + [FAKE[6], FAKE[0]]) == 1  # k_out is q
+    for gq, gk in ((FAKE[1], FAKE[9]), (FAKE[7], FAKE[9]), (FAKE[8], FAKE[0]), (FAKE[8], FAKE[6])):
+        assert L.ipttt_qk_norm_rope_backward(ctypes.byref(qk()), *FAKE[:8], gq, gk, *FAKE[10:13], 1 << 30, None) == 1
+    # gq in q's place with another stride
+    assert L.ipttt_qk_norm_rope_backward(ctypes.byref(qk(ldq=1024)), *FAKE[:8], FAKE[0], *FAKE[9:13], 1 << 30, None) == 1
+    for gH, gW in ((FAKE[0], FAKE[6]), (FAKE[1], FAKE[6]), (FAKE[5], FAKE[0]), (FAKE[5], FAKE[1])):
+        assert L.ipttt_xent_backward(ctypes.byref(xe()), *FAKE[:5], gH, gW, FAKE[7], 1 << 40, None) == 1

@@ -90,6 +90,9 @@ def test_qk_in_place_strided_and_zero_rows():
     a, b = want[0].clone(), want[1].clone()
     g2 = pkg.qk_norm_rope_backward(cfg, q, k, wq, wk, inv, pos, a, b, gq=a, gk=b)
     assert all(torch.equal(gq[n], g2[n]) for n in gq) and g2["q"] is a
+    # in the inputs' own places, one projection's views
+    g3 = pkg.qk_norm_rope_backward(cfg, q, k, wq, wk, inv, pos, want[0], want[1], gq=q, gk=k)
+    assert all(torch.equal(gq[n], g3[n]) for n in gq) and g3["q"] is q
     assert status() == 0
 
 
