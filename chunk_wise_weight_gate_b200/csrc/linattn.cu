@@ -17,8 +17,10 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxWidth = 256;
+constexpr long long kSmemSm = 233472;  // shared memory of an SM
 constexpr int L = kSimtChunk;
 constexpr int kSlice = 64;  // columns of the state a block holds
+constexpr int kSp = L + 4;  // row stride of a chunk's products
 
 __device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
 __device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
@@ -72,14 +74,17 @@ __global__ void k_mark(uint32_t* words, long long wpr, int B, int T, const int32
 // ------------------------------------------------------------------ the pass on the CUDA cores
 
 size_t simt_smem(int Da) {
-  return sizeof(float) * ((size_t)Da * kSlice + 2 * (size_t)L * (Da + 4) + (size_t)L * kSlice + L * (L + 1) + 3 * L + 4);
+  return sizeof(float) * ((size_t)Da * kSlice + 2 * (size_t)L * (Da + 4) + (size_t)L * kSlice + L * kSp + 3 * L + 4);
 }
 
 // One block walks a segment's chunks of 32 tokens for one (row, head) and 64 columns
 // of c, with its columns of the state in shared memory: the chunk's a, b and c are
 // staged as fp32, the 32 x 32 products a . b under the decay formed, the chunk's
-// output written and the state advanced.  Bound by the fp32 pipe and shared memory;
-// a 2 x 4 tile of outputs a thread halves the shared-memory reads a product takes.
+// output written and the state advanced.  Bound by the reads of shared memory and the
+// latency of a chunk's steps: 4 heads of 128 x 8192 tokens, fp32, 268 us (24 TFLOP/s of some
+// 70).  So a thread holds 2 x 4 outputs and reads their operands four at a time, and 4 x 4
+// of the state, a row of c read once for four of its rows (with a row of c for each, and
+// a scalar an operand, 2 rows of 6 heads of 64 x 96 took 324 us backwards instead of 183).
 template <typename T>
 __global__ void __launch_bounds__(kThreads) k_pass(const Pass p) {
   extern __shared__ __align__(16) float smem[];
@@ -88,8 +93,8 @@ __global__ void __launch_bounds__(kThreads) k_pass(const Pass p) {
   float* sa = F + (size_t)Da * kSlice;  // [L][lda]
   float* sb = sa + (size_t)L * lda;     // [L][lda]
   float* sc = sb + (size_t)L * lda;     // [L][kSlice]
-  float* sp = sc + L * kSlice;          // [L][L + 1]
-  float* pw = sp + L * (L + 1);         // [L + 1] powers of gamma
+  float* sp = sc + L * kSlice;          // [L][kSp]
+  float* pw = sp + L * kSp;         // [L + 1] powers of gamma
   float* win = pw + L + 1;              // [L] the state's weight in each row
   float* wout = win + L;                // [L] each row's weight in the new state
   int* sh = reinterpret_cast<int*>(wout + L);
@@ -188,22 +193,32 @@ __global__ void __launch_bounds__(kThreads) k_pass(const Pass p) {
 #pragma unroll
         for (int v = 0; v < 2; ++v) {
           const int j = tx + 16 * v;
-          sp[i * (L + 1) + j] = j >= from && j < to ? s[u][v] * pw[abs(i - j)] : 0.0f;
+          sp[i * kSp + j] = j >= from && j < to ? s[u][v] * pw[abs(i - j)] : 0.0f;
         }
       }
       __syncthreads();
       float4 o[2], e[2];
       o[0] = o[1] = e[0] = e[1] = zero;
-      for (int j = 0; j < L; ++j) {
-        const float4 v = *reinterpret_cast<const float4*>(sc + j * kSlice + 4 * tx);
-        fma4(o[0], sp[ty * (L + 1) + j], v);
-        fma4(o[1], sp[(ty + 16) * (L + 1) + j], v);
-      }
-      for (int d = 0; d < Da; ++d) {
-        const float4 f = *reinterpret_cast<const float4*>(F + d * kSlice + 4 * tx);
-        fma4(e[0], sa[ty * lda + d], f);
-        fma4(e[1], sa[(ty + 16) * lda + d], f);
-      }
+      // acc[u] += row ty + 16 u of x [.][ld] times y [n][kSlice]
+      auto rows_times = [&](float4* acc, const float* x, int ld, const float* y, int n) {
+#pragma unroll 2
+        for (int d = 0; d < n; d += 4) {
+          const float4 x0 = load4(x + ty * ld + d), x1 = load4(x + (ty + 16) * ld + d);
+          float4 v[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) v[k] = load4(y + (d + k) * kSlice + 4 * tx);
+          fma4(acc[0], x0.x, v[0]);
+          fma4(acc[1], x1.x, v[0]);
+          fma4(acc[0], x0.y, v[1]);
+          fma4(acc[1], x1.y, v[1]);
+          fma4(acc[0], x0.z, v[2]);
+          fma4(acc[1], x1.z, v[2]);
+          fma4(acc[0], x0.w, v[3]);
+          fma4(acc[1], x1.w, v[3]);
+        }
+      };
+      rows_times(o, sp, kSp, sc, L);
+      rows_times(e, sa, lda, F, Da);
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const int i = ty + 16 * u;
@@ -217,14 +232,26 @@ __global__ void __launch_bounds__(kThreads) k_pass(const Pass p) {
       __syncthreads();
     }
     const float keep = w ? 0.0f : pw[len - lag];
-    for (int r = ty; r < Da; r += 16) {
-      float4* fp = reinterpret_cast<float4*>(F + r * kSlice + 4 * tx);
-      float4 f = keep != 0.0f ? scale4(*fp, keep) : zero;
+    // four rows of the state at a time, so that a row of c is read once for them
+    for (int r0 = ty; r0 < Da; r0 += 64) {
+      float4 f[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int r = r0 + 16 * u;
+        f[u] = keep != 0.0f && r < Da ? scale4(load4(F + r * kSlice + 4 * tx), keep) : zero;
+      }
+#pragma unroll 4
       for (int j = 0; j < len; ++j) {
         const float x = wout[j];
-        if (x != 0.0f) fma4(f, sb[j * lda + r] * x, *reinterpret_cast<const float4*>(sc + j * kSlice + 4 * tx));
+        if (x == 0.0f) continue;
+        const float4 v = scale4(load4(sc + j * kSlice + 4 * tx), x);
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          if (r0 + 16 * u < Da) fma4(f[u], sb[j * lda + r0 + 16 * u], v);
       }
-      *fp = f;
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (r0 + 16 * u < Da) store4(F + (r0 + 16 * u) * kSlice + 4 * tx, f[u]);
     }
   }
 
@@ -346,16 +373,34 @@ cudaError_t launch_step(const ipttt_linattn_params& p, float* S, const void* q, 
 
 }  // namespace
 
-int simt_segments(int B, int T, int H, int Da, int Dc, int* seg_chunks) {
-  (void)Da;
-  const int nchunks = (T + L - 1) / L;
-  const long long blocks = (long long)B * H * ((Dc + kSlice - 1) / kSlice);
-  // one segment where the rows, heads and column slices fill the SMs, else enough
-  // segments of at least 4 chunks to do so
-  int segs = (int)std::min<long long>((nchunks + 3) / 4, (148 + blocks - 1) / blocks);
-  segs = std::max(1, segs);
-  *seg_chunks = (nchunks + segs - 1) / segs;
-  return (nchunks + *seg_chunks - 1) / *seg_chunks;
+// One cut for all passes of a call (`width`: the wider of Dk and Dv), so that the pass for gk can
+// take the states of the one for gv.
+int simt_segments(int B, int T, int H, int width, int* seg_chunks) {
+  const int n = (T + L - 1) / L;
+  const long long blocks = (long long)B * H * ((width + kSlice - 1) / kSlice), sms = 148;
+  // The number of segments that comes out fastest, in two-hundredths of a chunk's time: an SM
+  // holds up to three blocks (two at width 128), each more of them slowing all by 0.3; a block starts
+  // in half a chunk's time, the pass for the segments' states takes 0.3 of the time a chunk and
+  // its launch a quarter of one.  fp32, backwards: 4 heads of 128 x 8192 tokens 744 us in 37
+  // segments (947 in 25, 967 in 50), 12 heads of 64 x 96, 777 tokens, 188 in 13 (320 in 4, 243 in
+  // 25), 160 heads of 128 x 512 tokens 1625 in 3 (1979 in one).
+  const long long room = std::min<long long>(3, kSmemSm / (long long)(simt_smem(width) + 1024));
+  auto time = [&](long long count, long long twentieths) {
+    const long long full = count / (sms * room), rest = (count % (sms * room) + sms - 1) / sms;
+    return twentieths * (full * (10 + 3 * (room - 1)) + (rest ? 10 + 3 * (rest - 1) : 0));
+  };
+  long long best = 0;
+  for (int s = 1; s <= std::min(n, 148); ++s) {
+    const int each = (n + s - 1) / s, segs = (n + each - 1) / each;
+    if (segs != s) continue;
+    long long t = time(blocks * segs, 20 * each + 10);
+    if (segs > 1) t += time(blocks * (segs - 1), 6 * each + 10) + 50;
+    if (best == 0 || t < best) {
+      best = t;
+      *seg_chunks = each;
+    }
+  }
+  return (n + *seg_chunks - 1) / *seg_chunks;
 }
 
 cudaError_t run_simt(const Pass& p, int dtype, cudaStream_t st) {
@@ -430,8 +475,7 @@ bool on_tensor_cores(const ipttt_linattn_params& p) { return p.dtype == IPTTT_BF
 struct Work {
   size_t starts, seg, S0, parts, total;
   long long words;
-  int segs_o, chunks_o;  // passes whose output is Dv wide (O, gv)
-  int segs_q, chunks_q;  // passes whose output is Dk wide (gq, gk)
+  int segs, seg_chunks;  // segments of a row, chunks of each
   int whole;             // (row, head) pairs that are not cut
 };
 
@@ -445,16 +489,10 @@ Work work_of(const ipttt_linattn_params& p, bool backward) {
   };
   w.words = (p.T + kTcChunk - 1) / kTcChunk * (kTcChunk / 32);
   w.starts = take((size_t)p.B * w.words * 4);
-  if (on_tensor_cores(p)) {
-    w.segs_o = w.segs_q = tc_segments(p.B, p.T, p.H, &w.chunks_o, &w.whole);
-    w.chunks_q = w.chunks_o;
-  } else {
-    w.segs_o = simt_segments(p.B, p.T, p.H, p.Dk, p.Dv, &w.chunks_o);
-    w.segs_q = simt_segments(p.B, p.T, p.H, p.Dv, p.Dk, &w.chunks_q);
-  }
-  const int segs = backward ? std::max(w.segs_o, w.segs_q) : w.segs_o;
-  w.seg = take(segs > 1 ? (size_t)p.B * p.H * segs * p.Dk * p.Dv * 4 : 0);
-  w.S0 = take(!backward && segs > 1 ? (size_t)p.B * p.H * p.Dk * p.Dv * 4 : 0);
+  w.segs = on_tensor_cores(p) ? tc_segments(p.B, p.T, p.H, &w.seg_chunks, &w.whole)
+                              : simt_segments(p.B, p.T, p.H, std::max(p.Dk, p.Dv), &w.seg_chunks);
+  w.seg = take(w.segs > 1 ? (size_t)p.B * p.H * w.segs * p.Dk * p.Dv * 4 : 0);
+  w.S0 = take(!backward && w.segs > 1 ? (size_t)p.B * p.H * p.Dk * p.Dv * 4 : 0);
   w.parts = take(backward && p.H != p.Hkv ? (size_t)p.B * p.T * p.H * std::max(p.Dk, p.Dv) * 4 : 0);
   w.total = std::max<size_t>(off, 256);
   return w;
@@ -552,8 +590,8 @@ ipttt_status ipttt_linattn_forward(const ipttt_linattn_params* pp, const void* q
   a.ldo = p.ldo;
   a.init = S0_opt;
   a.fin = S_final_opt;
-  a.segs = w.segs_o;
-  a.seg_chunks = w.chunks_o;
+  a.segs = w.segs;
+  a.seg_chunks = w.seg_chunks;
   a.whole = w.whole;
   cudaError_t e = mark_starts(p, w, ws, doc_starts, n_doc_starts, status, &a.starts, &launches, st);
   if (e == cudaSuccess && S0_opt && S0_opt == S_final_opt && a.segs > 1) {
@@ -597,6 +635,8 @@ ipttt_status ipttt_linattn_backward(const ipttt_linattn_params* pp, const void* 
   base.log_decay = log_decay;
   base.words = w.words;
   base.scale = p.scale;
+  base.segs = w.segs;
+  base.seg_chunks = w.seg_chunks;
   base.whole = w.whole;
   base.status = status;
   cudaError_t e = mark_starts(p, w, ws, doc_starts, n_doc_starts, status, &base.starts, &launches, st);
@@ -620,8 +660,6 @@ ipttt_status ipttt_linattn_backward(const ipttt_linattn_params* pp, const void* 
     s.gc = c.g;
     s.Da = Da;
     s.Dc = Dc;
-    s.segs = Dc == p.Dv && Da == p.Dk ? w.segs_o : w.segs_q;
-    s.seg_chunks = Dc == p.Dv && Da == p.Dk ? w.chunks_o : w.chunks_q;
     return s;
   };
   // a gradient of k or v: straight to the output, or per head in fp32 and then summed over the group
@@ -667,10 +705,8 @@ ipttt_status ipttt_linattn_backward(const ipttt_linattn_params* pp, const void* 
   if (e == cudaSuccess) {
     Pass s = pass_of(xv, xg, xq, p.Dv, p.Dk);  // gk, R transposed
     s.init_t = 1;
-    // where both passes cut the rows alike, the segments' R of the pass for gv serve here too
-    const bool have = s.segs > 1 && w.segs_o == w.segs_q && w.chunks_o == w.chunks_q;
-    s.seg_t = have;
-    e = shared(s, gk, p.ldgk, p.Dk, have);
+    s.seg_t = 1;      // the segments' R of the pass for gv serve here too
+    e = shared(s, gk, p.ldgk, p.Dk, true);
   }
   if (e != cudaSuccess) return cuda_fail("linattn_backward", e);
   count_launches(launches);

@@ -100,7 +100,7 @@ __device__ __forceinline__ size_t state_index(const Pass& p, int transposed, int
 // The CUDA-core pass (any widths up to 256, fp32 or bf16 operands), chunks of 32 tokens.
 constexpr int kSimtChunk = 32;
 cudaError_t run_simt(const Pass& p, int dtype, cudaStream_t st);
-int simt_segments(int B, int T, int H, int Da, int Dc, int* seg_chunks);
+int simt_segments(int B, int T, int H, int width, int* seg_chunks);
 
 // The tensor-core pass (bf16 operands, widths of 64 and 128), chunks of 128 tokens.
 constexpr int kTcChunk = 128;
