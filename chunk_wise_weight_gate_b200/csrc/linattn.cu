@@ -17,6 +17,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxWidth = 256;
+constexpr int kMaxSegs = 148;      // segments of a row
 constexpr long long kSmemSm = 233472;  // shared memory of an SM
 constexpr int L = kSimtChunk;
 constexpr int kSlice = 64;  // columns of the state a block holds
@@ -81,10 +82,12 @@ size_t simt_smem(int Da) {
 // of c, with its columns of the state in shared memory: the chunk's a, b and c are
 // staged as fp32, the 32 x 32 products a . b under the decay formed, the chunk's
 // output written and the state advanced.  Bound by the reads of shared memory and the
-// latency of a chunk's steps: 4 heads of 128 x 8192 tokens, fp32, 268 us (24 TFLOP/s of some
+// latency of a chunk's steps: 4 heads of 128 x 8192 tokens, fp32, 203 us (20 TFLOP/s of some
 // 70).  So a thread holds 2 x 4 outputs and reads their operands four at a time, and 4 x 4
-// of the state, a row of c read once for four of its rows (with a row of c for each, and
-// a scalar an operand, 2 rows of 6 heads of 64 x 96 took 324 us backwards instead of 183).
+// of the state, a row of c read once for four of its rows;
+// and a batch of loads is under way before its first store.  2 rows of 6 heads of 64 x 96, 777
+// tokens, backwards: 140 us (324 with a row of c read for each row of the state, a scalar an
+// operand and a load at a time, 183 with the loads alone like that).
 template <typename T>
 __global__ void __launch_bounds__(kThreads) k_pass(const Pass p) {
   extern __shared__ __align__(16) float smem[];
@@ -97,7 +100,6 @@ __global__ void __launch_bounds__(kThreads) k_pass(const Pass p) {
   float* pw = sp + L * kSp;         // [L + 1] powers of gamma
   float* win = pw + L + 1;              // [L] the state's weight in each row
   float* wout = win + L;                // [L] each row's weight in the new state
-  int* sh = reinterpret_cast<int*>(wout + L);
 
   const int b = blockIdx.y / p.H, h = blockIdx.y % p.H;
   const int seg = blockIdx.z;
@@ -115,29 +117,21 @@ __global__ void __launch_bounds__(kThreads) k_pass(const Pass p) {
 
   const int nchunks = (p.T + L - 1) / L;
   const int first = seg * p.seg_chunks, last = min(nchunks, first + p.seg_chunks);
-  const int lo = first * L, hi = min(p.T, last * L);
   const size_t bh = (size_t)b * p.H + h, nstate = (size_t)Da * p.Dc;
-  // the state the segment starts from
+  // the state the segment starts from: the initial one, or what k_prefix has left for it
   const int c = c0 + 4 * tx;
   {
-    const int start = only_state ? 0 : nearest_start(p, b, p.rev ? hi : lo, sh);
-    __syncthreads();
+    const float* from = p.segs > 1 ? p.seg_in + (bh * p.segs + seg) * nstate : p.init ? p.init + bh * nstate : nullptr;
+    const int turned = p.segs > 1 ? p.seg_t : p.init_t;
+    const float mul = p.segs > 1 ? 1.0f : p.init_mul;
     for (int r = ty; r < Da; r += 16) {
       float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      if (!only_state && c < p.Dc) {
-        float* e = reinterpret_cast<float*>(&f);
-        const float w0 = p.init ? p.init_mul * reach(p, g, -1, lo, hi, start, L) : 0.0f;
-        if (w0 != 0.0f)
-          for (int k = 0; k < 4; ++k) e[k] = w0 * p.init[bh * nstate + state_index(p, p.init_t, r, c + k)];
-        const int s0 = p.rev ? seg + 1 : 0, s1 = p.rev ? p.segs : seg;
-        for (int s = s0; s < s1; ++s) {
-          const float w = reach(p, g, s, lo, hi, start, L);
-          if (w == 0.0f) continue;
-          const float* in = p.seg_in + (bh * p.segs + s) * nstate;
-          for (int k = 0; k < 4; ++k) e[k] = fmaf(w, in[state_index(p, p.seg_t, r, c + k)], e[k]);
-        }
+      if (!only_state && from && c < p.Dc) {
+        if (!turned) f = load4(from + (size_t)r * p.Dc + c);
+        else f = make_float4(from[(size_t)c * Da + r], from[(size_t)(c + 1) * Da + r], from[(size_t)(c + 2) * Da + r],
+                             from[(size_t)(c + 3) * Da + r]);
       }
-      *reinterpret_cast<float4*>(F + r * kSlice + 4 * tx) = f;
+      store4(F + r * kSlice + 4 * tx, scale4(f, mul));
     }
   }
 
@@ -149,17 +143,32 @@ __global__ void __launch_bounds__(kThreads) k_pass(const Pass p) {
     const int lag = p.rev && t0 + len == p.T ? 1 : 0;
     __syncthreads();  // the last chunk's readers
     const float4 zero = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int i = threadIdx.x; i < L * (Da / 4); i += kThreads) {
-      const int r = i / (Da / 4), q = 4 * (i % (Da / 4));
-      const bool on = r < len;
-      *reinterpret_cast<float4*>(sb + r * lda + q) = on ? load4(Bm + (t0 + r) * p.ldb + q) : zero;
-      if (!only_state) *reinterpret_cast<float4*>(sa + r * lda + q) = on ? load4(A + (t0 + r) * p.lda + q) : zero;
+    // all loads of a batch before its first store: one at a time, each would wait for HBM by itself
+    float4 vc[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int r = ty + 16 * u;
+      vc[u] = r < len && c < p.Dc ? load4(C + (t0 + r) * p.ldc + c) : zero;
     }
-    for (int i = threadIdx.x; i < L * (kSlice / 4); i += kThreads) {
-      const int r = i / (kSlice / 4), q = 4 * (i % (kSlice / 4));
-      *reinterpret_cast<float4*>(sc + r * kSlice + q) =
-          r < len && c0 + q < p.Dc ? load4(C + (t0 + r) * p.ldc + c0 + q) : zero;
+    for (int q0 = 4 * tx; q0 < Da; q0 += 128) {
+      float4 va[4], vb[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int r = ty + 16 * (u & 1), q = q0 + 64 * (u >> 1);
+        const bool on = r < len && q < Da;
+        vb[u] = on ? load4(Bm + (t0 + r) * p.ldb + q) : zero;
+        va[u] = on && !only_state ? load4(A + (t0 + r) * p.lda + q) : zero;
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int r = ty + 16 * (u & 1), q = q0 + 64 * (u >> 1);
+        if (q >= Da) continue;
+        store4(sb + r * lda + q, vb[u]);
+        if (!only_state) store4(sa + r * lda + q, va[u]);
+      }
     }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) store4(sc + (ty + 16 * u) * kSlice + 4 * tx, vc[u]);
     if (threadIdx.x < L) {
       const int i = threadIdx.x;
       const bool in = p.rev ? i >= last_start : i < first_start;
@@ -266,6 +275,63 @@ __global__ void __launch_bounds__(kThreads) k_pass(const Pass p) {
   if (dst && c < p.Dc) {
     for (int r = ty; r < Da; r += 16)  // a thread's own elements: no barrier since they were written
       store4(dst + (size_t)r * p.Dc + c, scale4(*reinterpret_cast<const float4*>(F + r * kSlice + 4 * tx), mul));
+  }
+}
+
+// The segments' own states of a (row, head), seg_state, in place into the state that each segment
+// starts from: forwards in order (backwards in the opposite one), the state brought along times
+// gamma for every token of a segment, 0 where a document starts in it, plus the segment's own.  One
+// thread takes four elements.  4.7 us for 12 heads of 13 states of 64 x 96.  (Every segment's block summing the
+// states before it reads them segments^2 / 2 times, most of the time of a long row in many.)
+__global__ void __launch_bounds__(kThreads) k_prefix(const Pass p) {
+  __shared__ float keep[kMaxSegs];
+  const size_t bh = blockIdx.y, nstate = (size_t)p.Da * p.Dc;
+  const int b = blockIdx.y / p.H, h = blockIdx.y % p.H;
+  const float g = p.log_decay[h];
+  const uint32_t* words = p.starts ? p.starts + b * p.words : nullptr;
+  for (int s = threadIdx.x; s < p.segs; s += kThreads) {
+    const int w0 = s * p.seg_chunks, w1 = min((p.T + L - 1) / L, w0 + p.seg_chunks);  // one word of starts a chunk
+    uint32_t any = 0;
+    for (int w = w0; words && w < w1; ++w) any |= words[w];
+    const int hi = min(p.T, w1 * L);
+    keep[s] = any ? 0.0f : decay_pow(g, hi - w0 * L - (p.rev && hi == p.T ? 1 : 0));
+  }
+  __syncthreads();
+  const size_t e = 4 * ((size_t)blockIdx.x * kThreads + threadIdx.x);
+  if (e >= nstate) return;
+  float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if (p.init) {
+    const int r = (int)(e / p.Dc), c = (int)(e % p.Dc);
+    const float* in = p.init + bh * nstate;
+    f = p.init_t ? make_float4(in[(size_t)c * p.Da + r], in[(size_t)(c + 1) * p.Da + r], in[(size_t)(c + 2) * p.Da + r],
+                               in[(size_t)(c + 3) * p.Da + r])
+                 : load4(in + e);
+    f = scale4(f, p.init_mul);
+  }
+  float* x = p.seg_state + bh * p.segs * nstate + e;
+  constexpr int AHEAD = 8;
+  for (int n0 = 0; n0 < p.segs; n0 += AHEAD) {
+    float4 own[AHEAD];
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u) {  // the last one's own state is nobody's
+      const int s = p.rev ? p.segs - 1 - n0 - u : n0 + u;
+      if (n0 + u < p.segs - 1) own[u] = load4(x + (size_t)s * nstate);
+    }
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u) {
+      if (n0 + u >= p.segs) continue;
+      const int s = p.rev ? p.segs - 1 - n0 - u : n0 + u;
+      store4(x + (size_t)s * nstate, f);
+      if (n0 + u == p.segs - 1) continue;
+      const float k = keep[s];
+      if (k == 0.0f) {  // whatever f holds
+        f = own[u];
+      } else {
+        float4 y = own[u];
+        fma4(y, k, f);
+        f = y;
+      }
+    }
   }
 }
 
@@ -381,16 +447,16 @@ int simt_segments(int B, int T, int H, int width, int* seg_chunks) {
   // The number of segments that comes out fastest, in two-hundredths of a chunk's time: an SM
   // holds up to three blocks (two at width 128), each more of them slowing all by 0.3; a block starts
   // in half a chunk's time, the pass for the segments' states takes 0.3 of the time a chunk and
-  // its launch a quarter of one.  fp32, backwards: 4 heads of 128 x 8192 tokens 744 us in 37
-  // segments (947 in 25, 967 in 50), 12 heads of 64 x 96, 777 tokens, 188 in 13 (320 in 4, 243 in
-  // 25), 160 heads of 128 x 512 tokens 1625 in 3 (1979 in one).
+  // its launch a quarter of one.  fp32, backwards: 4 heads of 128 x 8192 tokens 529 us in 37
+  // segments (795 in 25, 720 in 50), 12 heads of 64 x 96, 777 tokens, 141 in 13 (276 in 4, 142 in
+  // 25), 160 heads of 128 x 512 tokens 1284 in 3 (1402 in one).
   const long long room = std::min<long long>(3, kSmemSm / (long long)(simt_smem(width) + 1024));
-  auto time = [&](long long count, long long twentieths) {
+  auto time = [&](long long count, long long work) {  // work in twentieths of a chunk
     const long long full = count / (sms * room), rest = (count % (sms * room) + sms - 1) / sms;
-    return twentieths * (full * (10 + 3 * (room - 1)) + (rest ? 10 + 3 * (rest - 1) : 0));
+    return work * (full * (10 + 3 * (room - 1)) + (rest ? 10 + 3 * (rest - 1) : 0));
   };
   long long best = 0;
-  for (int s = 1; s <= std::min(n, 148); ++s) {
+  for (int s = 1; s <= std::min(n, kMaxSegs); ++s) {
     const int each = (n + s - 1) / s, segs = (n + each - 1) / each;
     if (segs != s) continue;
     long long t = time(blocks * segs, 20 * each + 10);
@@ -492,10 +558,15 @@ Work work_of(const ipttt_linattn_params& p, bool backward) {
   w.segs = on_tensor_cores(p) ? tc_segments(p.B, p.T, p.H, &w.seg_chunks, &w.whole)
                               : simt_segments(p.B, p.T, p.H, std::max(p.Dk, p.Dv), &w.seg_chunks);
   w.seg = take(w.segs > 1 ? (size_t)p.B * p.H * w.segs * p.Dk * p.Dv * 4 : 0);
-  w.S0 = take(!backward && w.segs > 1 ? (size_t)p.B * p.H * p.Dk * p.Dv * 4 : 0);
+  w.S0 = take(!backward && w.segs > 1 && on_tensor_cores(p) ? (size_t)p.B * p.H * p.Dk * p.Dv * 4 : 0);
   w.parts = take(backward && p.H != p.Hkv ? (size_t)p.B * p.T * p.H * std::max(p.Dk, p.Dv) * 4 : 0);
   w.total = std::max<size_t>(off, 256);
   return w;
+}
+
+cudaError_t run_prefix(const Pass& p, cudaStream_t st) {
+  k_prefix<<<dim3((unsigned)((p.Da * p.Dc / 4 + kThreads - 1) / kThreads), p.B * p.H), kThreads, 0, st>>>(p);
+  return cudaGetLastError();
 }
 
 cudaError_t run_one(const ipttt_linattn_params& p, const Pass& q, cudaStream_t st) {
@@ -509,10 +580,15 @@ cudaError_t run_pass(const ipttt_linattn_params& p, Pass q, float* seg, bool hav
     Pass s = q;
     s.out = nullptr;
     s.seg_state = seg;
-    const cudaError_t e = run_one(p, s, st);
+    cudaError_t e = run_one(p, s, st);
     if (e != cudaSuccess) return e;
     ++*launches;
     q.after_states = 1;
+    if (!on_tensor_cores(p)) {
+      e = run_prefix(s, st);
+      if (e != cudaSuccess) return e;
+      ++*launches;
+    }
   }
   q.seg_in = seg;
   ++*launches;
@@ -594,7 +670,7 @@ ipttt_status ipttt_linattn_forward(const ipttt_linattn_params* pp, const void* q
   a.seg_chunks = w.seg_chunks;
   a.whole = w.whole;
   cudaError_t e = mark_starts(p, w, ws, doc_starts, n_doc_starts, status, &a.starts, &launches, st);
-  if (e == cudaSuccess && S0_opt && S0_opt == S_final_opt && a.segs > 1) {
+  if (e == cudaSuccess && S0_opt && S0_opt == S_final_opt && a.segs > 1 && on_tensor_cores(p)) {
     // the last segment may write the final state before the others have read the first
     a.init = reinterpret_cast<const float*>(ws + w.S0);
     e = cudaMemcpyAsync(ws + w.S0, S0_opt, (size_t)p.B * p.H * p.Dk * p.Dv * 4, cudaMemcpyDeviceToDevice, st);

@@ -37,7 +37,9 @@ struct Pass {
   const float* log_decay;        // [H]
   const uint32_t* starts;        // bit t % 32 of word [b][t / 32]: token t starts a document; null: none
   long long words;               // words of a row
-  const float* seg_in;           // [B][H][segs][Da][Dc]: the segments' own states (segs > 1)
+  // [B][H][segs][Da][Dc] (segs > 1): the segments' own states, or on the CUDA cores the states that
+  // they start from
+  const float* seg_in;
   float* seg_state;              // the same array, written when out is null
   int segs, seg_chunks;          // segments of a row, chunks of each (the last may have fewer)
   int after_states;              // the launch before is the pass for this one's segment states
@@ -49,53 +51,6 @@ struct Pass {
 };
 
 __device__ __forceinline__ float decay_pow(float g, int n) { return n <= 0 ? 1.0f : expf(g * (float)n); }
-
-// The nearest start on the far side of a segment: forwards the last start before token
-// `at` (-1: none), backwards the first start from token `at` on (T: none).  All threads
-// of the block take part; `sh` is one int of shared memory.
-__device__ __forceinline__ int nearest_start(const Pass& p, int b, int at, int* sh) {
-  const int none = p.rev ? p.T : -1;
-  if (!p.starts) return none;
-  if (threadIdx.x == 0) *sh = none;
-  __syncthreads();
-  const uint32_t* w = p.starts + b * p.words;
-  int best = none;
-  if (p.rev) {
-    for (int i = at / 32 + threadIdx.x; i < p.words; i += blockDim.x)
-      if (w[i]) {
-        const uint32_t m = i == at / 32 ? w[i] & (0xffffffffu << (at % 32)) : w[i];
-        if (m) best = min(best, 32 * i + __ffs(m) - 1);
-      }
-    if (best != none) atomicMin(sh, best);
-  } else {
-    for (int i = threadIdx.x; 32 * i < at; i += blockDim.x)
-      if (w[i]) {
-        const uint32_t m = i == at / 32 ? w[i] & ((1u << (at % 32)) - 1u) : w[i];
-        if (m) best = max(best, 32 * i + 31 - __clz(m));
-      }
-    if (best != none) atomicMax(sh, best);
-  }
-  __syncthreads();
-  return *sh;
-}
-
-// Factor with which segment s's own state, and the initial state (s = -1), reach the
-// segment of tokens [lo, hi): 0 where a document starts between.
-__device__ __forceinline__ float reach(const Pass& p, float g, int s, int lo, int hi, int start, int chunk) {
-  if (p.rev) {
-    if (s < 0) return start < p.T ? 0.0f : decay_pow(g, p.T - 1 - hi);
-    const int s0 = s * p.seg_chunks * chunk;
-    return s0 <= start ? decay_pow(g, s0 - hi) : 0.0f;
-  }
-  if (s < 0) return start >= 0 ? 0.0f : decay_pow(g, lo);
-  const int end = (s + 1) * p.seg_chunks * chunk;
-  return end > start ? decay_pow(g, lo - end) : 0.0f;
-}
-
-// Where element (r, c) of a state lies.
-__device__ __forceinline__ size_t state_index(const Pass& p, int transposed, int r, int c) {
-  return transposed ? (size_t)c * p.Da + r : (size_t)r * p.Dc + c;
-}
 
 // The CUDA-core pass (any widths up to 256, fp32 or bf16 operands), chunks of 32 tokens.
 constexpr int kSimtChunk = 32;

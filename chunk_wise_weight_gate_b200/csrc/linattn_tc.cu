@@ -141,7 +141,8 @@ __device__ __forceinline__ Starts starts_of(const Pass& p, int b, int ch) {
   return {*reinterpret_cast<const uint4*>(p.starts + b * p.words + 4 * ch)};
 }
 
-// nearest_start for one warp (every lane gets it).
+// The nearest start on the far side of a segment, for one warp (every lane gets it): forwards the
+// last start before token `at` (-1: none), backwards the first start from token `at` on (T: none).
 __device__ __forceinline__ int nearest_start_warp(const Pass& p, int b, int at, int lane) {
   int best = p.rev ? p.T : -1;
   if (!p.starts) return best;
@@ -158,6 +159,19 @@ __device__ __forceinline__ int nearest_start_warp(const Pass& p, int b, int at, 
     if (m) best = max(best, 32 * i + 31 - __clz(m));
   }
   return __reduce_max_sync(0xffffffffu, best);
+}
+
+// Factor with which segment s's own state, and the initial state (s = -1), reach the
+// segment of tokens [lo, hi): 0 where a document starts between.
+__device__ __forceinline__ float reach(const Pass& p, float g, int s, int lo, int hi, int start) {
+  if (p.rev) {
+    if (s < 0) return start < p.T ? 0.0f : decay_pow(g, p.T - 1 - hi);
+    const int s0 = s * p.seg_chunks * CH;
+    return s0 <= start ? decay_pow(g, s0 - hi) : 0.0f;
+  }
+  if (s < 0) return start >= 0 ? 0.0f : decay_pow(g, lo);
+  const int end = (s + 1) * p.seg_chunks * CH;
+  return end > start ? decay_pow(g, lo - end) : 0.0f;
 }
 
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
@@ -556,11 +570,11 @@ __global__ void __launch_bounds__(Cfg<DA, DC, KIND == STATES>::THREADS, 1) k_pas
             }
           }
         };
-        if (p.init) add(p.init + bh * DA * DC, p.init_t, p.init_mul * reach(p, g, -1, lo, hi, start, CH));
+        if (p.init) add(p.init + bh * DA * DC, p.init_t, p.init_mul * reach(p, g, -1, lo, hi, start));
         const int s0 = rev ? it.seg + 1 : 0, s1 = rev ? it.segs : it.seg;
         if (s0 < s1) wait_for_launch_before();
         for (int s = s0; s < s1; ++s)
-          add(p.seg_in + (bh * p.segs + s) * DA * DC, p.seg_t, reach(p, g, s, lo, hi, start, CH));
+          add(p.seg_in + (bh * p.segs + s) * DA * DC, p.seg_t, reach(p, g, s, lo, hi, start));
       }
       LA_WAIT_WARP(tab_ready, ic);
 
