@@ -9,6 +9,7 @@
 #include <atomic>
 
 #include "linattn.h"
+#include "tc.cuh"
 
 namespace ipttt {
 namespace la {
@@ -18,6 +19,11 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kMaxWidth = 256;
 constexpr int kMaxSegs = 148;      // segments of a row
+// The tensor-core pass sums up to so many segments' states itself, which saves a launch: 2 rows of 20
+// heads of 128 x 8192 tokens 118 us (136 by k_prefix), 20 heads of 32768 tokens, 7 segments,
+// 198 (206).  Above it k_prefix does: 10 heads of 32768 tokens 124 us (134 summed by
+// every segment), 2 heads 55 (102), 2 heads of 131072 tokens 109 (169).
+constexpr int kDirectStates = 8;
 constexpr long long kSmemSm = 233472;  // shared memory of an SM
 constexpr int L = kSimtChunk;
 constexpr int kSlice = 64;  // columns of the state a block holds
@@ -285,16 +291,16 @@ __global__ void __launch_bounds__(kThreads) k_pass(const Pass p) {
 // states before it reads them segments^2 / 2 times, most of the time of a long row in many.)
 __global__ void __launch_bounds__(kThreads) k_prefix(const Pass p) {
   __shared__ float keep[kMaxSegs];
-  const size_t bh = blockIdx.y, nstate = (size_t)p.Da * p.Dc;
-  const int b = blockIdx.y / p.H, h = blockIdx.y % p.H;
+  const size_t bh = p.whole + blockIdx.y, nstate = (size_t)p.Da * p.Dc;
+  const int b = (int)(bh / p.H), h = (int)(bh % p.H);
+  tc::launch_dependents();  // the pass may set itself up meanwhile
   const float g = p.log_decay[h];
   const uint32_t* words = p.starts ? p.starts + b * p.words : nullptr;
   for (int s = threadIdx.x; s < p.segs; s += kThreads) {
-    const int w0 = s * p.seg_chunks, w1 = min((p.T + L - 1) / L, w0 + p.seg_chunks);  // one word of starts a chunk
+    const int lo = s * p.seg_chunks * p.chunk, hi = min(p.T, lo + p.seg_chunks * p.chunk);
     uint32_t any = 0;
-    for (int w = w0; words && w < w1; ++w) any |= words[w];
-    const int hi = min(p.T, w1 * L);
-    keep[s] = any ? 0.0f : decay_pow(g, hi - w0 * L - (p.rev && hi == p.T ? 1 : 0));
+    for (int w = lo / 32; words && 32 * w < hi; ++w) any |= words[w];
+    keep[s] = any ? 0.0f : decay_pow(g, hi - lo - (p.rev && hi == p.T ? 1 : 0));
   }
   __syncthreads();
   const size_t e = 4 * ((size_t)blockIdx.x * kThreads + threadIdx.x);
@@ -543,6 +549,7 @@ struct Work {
   long long words;
   int segs, seg_chunks;  // segments of a row, chunks of each
   int whole;             // (row, head) pairs that are not cut
+  int prefixed;          // the segments' states are summed into those that they start from
 };
 
 Work work_of(const ipttt_linattn_params& p, bool backward) {
@@ -557,15 +564,16 @@ Work work_of(const ipttt_linattn_params& p, bool backward) {
   w.starts = take((size_t)p.B * w.words * 4);
   w.segs = on_tensor_cores(p) ? tc_segments(p.B, p.T, p.H, &w.seg_chunks, &w.whole)
                               : simt_segments(p.B, p.T, p.H, std::max(p.Dk, p.Dv), &w.seg_chunks);
+  w.prefixed = !on_tensor_cores(p) || w.segs > kDirectStates;
   w.seg = take(w.segs > 1 ? (size_t)p.B * p.H * w.segs * p.Dk * p.Dv * 4 : 0);
-  w.S0 = take(!backward && w.segs > 1 && on_tensor_cores(p) ? (size_t)p.B * p.H * p.Dk * p.Dv * 4 : 0);
+  w.S0 = take(!backward && w.segs > 1 && !w.prefixed ? (size_t)p.B * p.H * p.Dk * p.Dv * 4 : 0);
   w.parts = take(backward && p.H != p.Hkv ? (size_t)p.B * p.T * p.H * std::max(p.Dk, p.Dv) * 4 : 0);
   w.total = std::max<size_t>(off, 256);
   return w;
 }
 
 cudaError_t run_prefix(const Pass& p, cudaStream_t st) {
-  k_prefix<<<dim3((unsigned)((p.Da * p.Dc / 4 + kThreads - 1) / kThreads), p.B * p.H), kThreads, 0, st>>>(p);
+  k_prefix<<<dim3((unsigned)((p.Da * p.Dc / 4 + kThreads - 1) / kThreads), p.B * p.H - p.whole), kThreads, 0, st>>>(p);
   return cudaGetLastError();
 }
 
@@ -584,7 +592,7 @@ cudaError_t run_pass(const ipttt_linattn_params& p, Pass q, float* seg, bool hav
     if (e != cudaSuccess) return e;
     ++*launches;
     q.after_states = 1;
-    if (!on_tensor_cores(p)) {
+    if (q.prefixed) {
       e = run_prefix(s, st);
       if (e != cudaSuccess) return e;
       ++*launches;
@@ -669,8 +677,10 @@ ipttt_status ipttt_linattn_forward(const ipttt_linattn_params* pp, const void* q
   a.segs = w.segs;
   a.seg_chunks = w.seg_chunks;
   a.whole = w.whole;
+  a.prefixed = w.prefixed;
+  a.chunk = on_tensor_cores(p) ? kTcChunk : kSimtChunk;
   cudaError_t e = mark_starts(p, w, ws, doc_starts, n_doc_starts, status, &a.starts, &launches, st);
-  if (e == cudaSuccess && S0_opt && S0_opt == S_final_opt && a.segs > 1 && on_tensor_cores(p)) {
+  if (e == cudaSuccess && S0_opt && S0_opt == S_final_opt && a.segs > 1 && !w.prefixed) {
     // the last segment may write the final state before the others have read the first
     a.init = reinterpret_cast<const float*>(ws + w.S0);
     e = cudaMemcpyAsync(ws + w.S0, S0_opt, (size_t)p.B * p.H * p.Dk * p.Dv * 4, cudaMemcpyDeviceToDevice, st);
@@ -714,6 +724,8 @@ ipttt_status ipttt_linattn_backward(const ipttt_linattn_params* pp, const void* 
   base.segs = w.segs;
   base.seg_chunks = w.seg_chunks;
   base.whole = w.whole;
+  base.prefixed = w.prefixed;
+  base.chunk = on_tensor_cores(p) ? kTcChunk : kSimtChunk;
   base.status = status;
   cudaError_t e = mark_starts(p, w, ws, doc_starts, n_doc_starts, status, &base.starts, &launches, st);
 

@@ -37,11 +37,11 @@ struct Pass {
   const float* log_decay;        // [H]
   const uint32_t* starts;        // bit t % 32 of word [b][t / 32]: token t starts a document; null: none
   long long words;               // words of a row
-  // [B][H][segs][Da][Dc] (segs > 1): the segments' own states, or on the CUDA cores the states that
-  // they start from
+  // [B][H][segs][Da][Dc] (segs > 1): the segments' own states, or (prefixed) the states they start from
   const float* seg_in;
   float* seg_state;              // the same array, written when out is null
-  int segs, seg_chunks;          // segments of a row, chunks of each (the last may have fewer)
+  int prefixed;
+  int segs, seg_chunks, chunk;   // segments of a row, chunks of each (the last may have fewer), tokens of a chunk
   int after_states;              // the launch before is the pass for this one's segment states
   int whole;                     // (row, head) pairs b * H + h below this are not cut into segments
   int B, T, H, Da, Dc;

@@ -31,7 +31,7 @@
 //
 // Rows are cut into segments when rows and heads alone leave SMs idle: a first pass (STATES) forms
 // each segment's own state from b and c alone (1.5 to 1.7 us a chunk: 64 KB, HBM), and the full
-// pass starts each segment from their sum under the decay.
+// pass starts each segment from their sum under the decay (many segments: from what k_prefix left).
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -553,7 +553,8 @@ __global__ void __launch_bounds__(Cfg<DA, DC, KIND == STATES>::THREADS, 1) k_pas
 #pragma unroll
       for (int e = 0; e < NC; ++e) f[e] = 0.0f;
       if constexpr (!STATE) {
-        const int start = p.init || it.segs > 1 ? nearest_start_warp(p, it.b, rev ? hi : lo, lane) : 0;
+        const bool prefixed = p.prefixed && it.segs > 1;
+        const int start = !prefixed && (p.init || it.segs > 1) ? nearest_start_warp(p, it.b, rev ? hi : lo, lane) : 0;
         auto add = [&](const float* src, int transposed, float w) {
           if (w == 0.0f) return;
           if (transposed) {
@@ -570,10 +571,11 @@ __global__ void __launch_bounds__(Cfg<DA, DC, KIND == STATES>::THREADS, 1) k_pas
             }
           }
         };
-        if (p.init) add(p.init + bh * DA * DC, p.init_t, p.init_mul * reach(p, g, -1, lo, hi, start));
+        if (p.init && !prefixed) add(p.init + bh * DA * DC, p.init_t, p.init_mul * reach(p, g, -1, lo, hi, start));
         const int s0 = rev ? it.seg + 1 : 0, s1 = rev ? it.segs : it.seg;
-        if (s0 < s1) wait_for_launch_before();
-        for (int s = s0; s < s1; ++s)
+        if (s0 < s1 || prefixed) wait_for_launch_before();
+        if (prefixed) add(p.seg_in + (bh * p.segs + it.seg) * DA * DC, p.seg_t, 1.0f);
+        for (int s = s0; s < s1 && !prefixed; ++s)
           add(p.seg_in + (bh * p.segs + s) * DA * DC, p.seg_t, reach(p, g, s, lo, hi, start));
       }
       LA_WAIT_WARP(tab_ready, ic);

@@ -249,6 +249,19 @@ def test_linear_attention_views_streams_and_state_in_place():
     assert status() == 0
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,T,H,D", [(1, 3000, 2, 64), (1, 700, 4, 128), (2, 40, 1, 64), (1, 1100, 150, 64)])
+def test_linear_attention_state_in_place(B, T, H, D, dtype):
+    # one segment, few and many, whole rows beside cut ones: S_final in S0's place is S_final elsewhere
+    cfg, q, k, v, ld, S0, ds = attn_case(B, T, H, H, D, D, dtype, (T // 2,), True)
+    for docs in (None, ds):
+        want, want_S = pkg.linear_attention(cfg, q, k, v, ld, docs, S0=S0, S_final=True)
+        S = S0.clone()
+        O, _ = pkg.linear_attention(cfg, q, k, v, ld, docs, S0=S, S_final=S)
+        assert torch.equal(O, want) and torch.equal(S, want_S)
+    assert status() == 0
+
+
 def test_linear_attention_bad_starts_and_decays_are_reported():
     cfg, q, k, v, ld, _, _ = attn_case(1, 40, 1, 1, 64, 64, "bf16")
     for bad in ([40], [-1], [5, 5], [9, 3]):
