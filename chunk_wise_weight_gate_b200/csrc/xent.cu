@@ -361,12 +361,24 @@ Work work_of(const ipttt_xent_params& p, bool backward) {
     w.part = take((size_t)p.N * sizeof(float2) * (tc ? all / 128 : 1));
     w.tl = take((size_t)p.N * 4);
   } else {
-    // enough slices of K for gH's product to fill the SMs (its blocks: four an SM in fp32, two
-    // in bf16), each of at least 256 columns
+    // slices of K for gH's product, each of at least 256 columns: in bf16 enough to fill the SMs
+    // twice, in fp32 the number that comes out fastest by the busiest SM's blocks (fewer than four
+    // leave its pipe idle for part of the time) and the sum of the slices (one takes 50 /
+    // piece of the product's time).  1000 tokens of 2560, 8000 words: 801 us in 6 slices, 1215 in
+    // one; 300 of 512, 10007: 74 in 29 (580 blocks), 105 in 7 (140).
     const int rows = tc ? 128 : p.N <= kFewRows ? 16 : SM;
     const long long tiles = (long long)((p.N + rows - 1) / rows) * ((p.d + 127) / 128);
-    const long long fill = tc ? 296 : 592;
-    w.slices = (int)std::max<long long>(1, std::min<long long>({fill / tiles, w.piece / 256, 32}));
+    const int most = std::max(1, std::min(w.piece / 256, 32));
+    w.slices = tc ? (int)std::max<long long>(1, std::min<long long>(296 / tiles, most)) : 1;
+    double best = 0.0;
+    for (int s = 1; !tc && s <= most; ++s) {
+      const long long busiest = (tiles * s + 147) / 148;
+      const double pace = busiest >= 4 ? 1.0 : 0.2 + 0.2 * (double)busiest;
+      const double time = (double)busiest * 148 / (pace * (double)(tiles * s)) + 50.0 * s / w.piece;
+      if (s > 1 && time >= best) continue;
+      best = time;
+      w.slices = s;
+    }
     w.gH = take((size_t)p.N * p.d * 4 * w.slices);
     w.unit = take(4);
     w.live = take((size_t)p.N * p.d * (tc ? 2 : 4));
