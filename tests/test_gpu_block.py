@@ -165,3 +165,66 @@ def test_captured_and_replayed_calls_share_a_workspace():
     torch.cuda.synchronize()
     assert pkg.get_status() == 0
     del graphs
+
+
+@pytest.mark.parametrize("dtype,B,T,heads,D", [("bf16", 1, 4000, 2, 128), ("bf16", 1, 1100, 150, 64), ("f32", 1, 1500, 3, 96)])
+def test_captured_rows_in_many_segments(dtype, B, T, heads, D):
+    # states of segments, their prefix and the pass (which may start early) in one graph; rows cut and whole
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    cfg = pkg.LinearAttentionConfig(B, T, heads, heads, D, D, D ** -0.5, dtype)
+    q, k, v, gO = (ref.rand(i, B, T, heads, D, dtype=dt).cuda() for i in range(4))
+    ld = torch.full((heads,), -0.003, device="cuda")
+    docs = torch.tensor([T // 3, T - 7], dtype=torch.int32, device="cuda")
+    S0 = ref.rand(9, B, heads, D, D).cuda()
+
+    def run(S):
+        O, S = pkg.linear_attention(cfg, q, k, v, ld, docs, S0=S, S_final=S)
+        g = pkg.linear_attention_backward(cfg, q, k, v, ld, docs, gO, S0=S0, gS_final=S)
+        return [O, S, *g.values()]
+
+    S = S0.clone()
+    run(S)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = run(S)
+    for seed in (20, 40):
+        for i, x in enumerate((q, k, v, gO)):
+            x.copy_(ref.rand(seed + i, *x.shape, dtype=dt))
+        for _ in range(3):  # the state in place: each replay starts anew
+            S.copy_(S0)
+            graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, run(S0.clone())))
+    assert pkg.get_status() == 0
+    del graph
+
+
+def test_two_calls_at_once():
+    B, T, heads, D, N, V = 1, 6000, 8, 128, 1200, 9000
+    acfg = pkg.LinearAttentionConfig(B, T, heads, heads, D, D, D ** -0.5)
+    xcfg = pkg.CrossEntropyConfig(N, V, 256)
+    q, k, v, gO = (ref.rand(i, B, T, heads, D, dtype=torch.bfloat16).cuda() for i in range(4))
+    ld = torch.full((heads,), -0.01, device="cuda")
+    H, W = (ref.rand(i, n, 256, std=0.3, dtype=torch.bfloat16).cuda() for i, n in ((5, N), (6, V)))
+    t = torch.randint(0, V, (N,), generator=torch.Generator().manual_seed(1)).cuda()
+    g1 = torch.full((N,), 1.0 / N, device="cuda")
+
+    def attention(stream=None):
+        O, S = pkg.linear_attention(acfg, q, k, v, ld, S_final=True, stream=stream)
+        return [O, S, *pkg.linear_attention_backward(acfg, q, k, v, ld, None, gO, stream=stream).values()]
+
+    def loss(stream=None):
+        l, lse = pkg.cross_entropy(xcfg, H, W, t, stream=stream)
+        return [l, lse, *pkg.cross_entropy_backward(xcfg, H, W, t, lse, g1, stream=stream).values()]
+
+    want_a, want_l = attention(), loss()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    got = []
+    for _ in range(5):
+        got += [(want_a, attention(streams[0])), (want_l, loss(streams[1])), (want_a, attention(streams[2]))]
+    torch.cuda.synchronize()
+    for want, out in got:
+        assert all(torch.equal(a, b) for a, b in zip(want, out))
+    assert pkg.get_status() == 0
