@@ -354,3 +354,57 @@ def test_cross_entropy_rows_left_out_reach_nothing(N, V, d, piece, dtype):
         got = pkg.cross_entropy_backward(cfg, h, W, t, lse2, g)
         assert torch.equal(got["H"], want["H"]) and torch.equal(got["W"], want["W"])
     assert status() == 0
+
+
+def test_offsets_beyond_32_bits():
+    # tokens so far apart that the last ones lie more than 2^31 elements on: the packed call's values
+    T, wide = 110000, 20480
+    for H, D, dtype in ((2, 64, "bf16"), (2, 40, "bf16")):
+        cfg, q, k, v, ld, S0, ds = attn_case(1, T, H, H, D, D, dtype, (70001,), True)
+        far = torch.empty(1, T, wide, dtype=torch.bfloat16, device="cuda")
+        views = []
+        for i, x in enumerate((q, k, v, torch.empty_like(q))):
+            y = far[..., wide - (i + 1) * H * D: wide - i * H * D].unflatten(-1, (H, D))
+            y.copy_(x)
+            views.append(y)
+        O, S = pkg.linear_attention(cfg, q, k, v, ld, ds, S0=S0, S_final=True)
+        O2, S2 = pkg.linear_attention(cfg, *views[:3], ld, ds, S0=S0, O=views[3], S_final=True)
+        assert torch.equal(O, O2) and torch.equal(S, S2)
+        g = pkg.linear_attention_backward(cfg, q, k, v, ld, ds, O, S0=S0)
+        h = pkg.linear_attention_backward(cfg, *views[:3], ld, ds, views[3], S0=S0)
+        assert all(torch.equal(g[n], h[n]) for n in g)
+        qc = pkg.QKNormRopeConfig(1, T, H, H, D, D)
+        w = torch.ones(D, dtype=torch.bfloat16, device="cuda")
+        inv = torch.logspace(0, -4, D // 2, dtype=torch.float64).cuda()
+        pos = torch.arange(T, device="cuda")[None]
+        a = pkg.qk_norm_rope(qc, q, k, w, w, inv, pos)
+        ga = pkg.qk_norm_rope_backward(qc, q, k, w, w, inv, pos, k, v)
+        gb = pkg.qk_norm_rope_backward(qc, *views[:2], w, w, inv, pos, *views[1:3])
+        assert all(torch.equal(ga[n], gb[n]) for n in ga)
+        b = pkg.qk_norm_rope(qc, *views[:2], w, w, inv, pos, q_out=views[0], k_out=views[1])
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+    assert status() == 0
+
+
+def test_cross_entropy_head_beyond_32_bits():
+    N, V, d = 16, 850000, 2560  # 2.2e9 weights
+    gen = torch.Generator("cuda").manual_seed(3)
+    W = torch.empty(V, d, dtype=torch.bfloat16, device="cuda").normal_(0, d ** -0.5, generator=gen)
+    H = torch.empty(N, d, dtype=torch.bfloat16, device="cuda").normal_(generator=gen)
+    t = torch.randint(V - 2000, V, (N,), generator=torch.Generator().manual_seed(1)).cuda()
+    cfg = pkg.CrossEntropyConfig(N, V, d)
+    loss, lse = pkg.cross_entropy(cfg, H, W, t)
+    logits = torch.cat([H.double() @ W[i:i + 50000].double().T for i in range(0, V, 50000)], 1)
+    want_lse = logits.logsumexp(1)
+    want = want_lse - logits.gather(1, t[:, None])[:, 0]
+    assert float((lse - want_lse).abs().max()) <= 1e-5 * float(want_lse.abs().max())
+    assert float((loss - want).abs().max()) <= 1e-5 * float(want.abs().max())
+    g = pkg.cross_entropy_backward(cfg, H, W, t, lse, torch.full((N,), 1 / N, device="cuda"))
+    p = (logits - want_lse[:, None]).exp()
+    p[torch.arange(N), t] -= 1
+    p /= N
+    gH = sum(p[:, i:i + 50000] @ W[i:i + 50000].double() for i in range(0, V, 50000))
+    assert ref.relative(g["H"], gH.cpu()) <= 5.6e-3
+    for lo in (0, V // 2, V - 2000):
+        assert ref.relative(g["W"][lo:lo + 2000], (p[:, lo:lo + 2000].T @ H.double()).cpu()) <= 5.6e-3
+    assert status() == 0
