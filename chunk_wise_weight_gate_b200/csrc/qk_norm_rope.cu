@@ -14,10 +14,13 @@
 // 32 lanes of a vector.  (Arithmetic two elements an instruction took more instructions, not
 // fewer: pairing registers up costs moves.)  Strips: elements
 // from E/2 l and from R/2 + E/2 l on (pairs (i, i + R/2)), or E l.. and E l + E/2.. (pairs
-// (2i, 2i+1), and elements that do not turn).  A block takes up to eight tokens with
+// (2i, 2i+1), and elements that do not turn).  A block takes a tile of tokens at a time with
 // all their heads; a group of lanes stays with one token, whose sines and cosines
-// (angle reduced to a turn in 64 bits, sincospif of the rest) are computed once for
-// all heads and then stay in registers.
+// (angle reduced to a turn in 64 bits) are computed once for all heads and then stay in
+// registers.  Now 116 us for those 32768 tokens (671 MB, 5.8 TB/s; 89% of the copy
+// bandwidth), 5.4 for 300, 3.5 for 16.  Backwards, 3 x 4099 tokens of 20 + 4 heads of 128, half of
+// each turned: 68 us with the weights' sum (227 MB, 3.3 TB/s); it is at the rate its
+// instructions issue, 330 for 512 elements of x and gy.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -407,8 +410,10 @@ QkArgs args_of(const ipttt_qk_params& p) {
   a.interleaved = p.interleaved;
   a.eps = p.eps;
   a.inv_d = 1.0f / (float)p.D;
-  // eight tokens a tile, unless that leaves SMs without one
-  a.shift = a.tokens >= (long long)kTokens * 148 ? 3 : 0;
+  // a token a tile while every block has one at most, else eight, whose angles and loads share a
+  // block's latency: 32 + 8 heads of 128, 300 tokens 5.4 us (6.2 by eights), 1184 tokens 6.7 by
+  // eights (12.9 one by one), 32768 tokens 116 (298)
+  a.shift = a.tokens > kForwardBlocks ? 3 : 0;
   static_assert(kTokens == 8, "shift");
   return a;
 }

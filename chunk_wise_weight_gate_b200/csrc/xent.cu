@@ -34,10 +34,11 @@ constexpr int kThreads = 256;
 // blocks for four an SM.  300 tokens, 10007 words, d = 512: 84 us for the logits (37 TFLOP/s),
 // 71 for gH, 76 for gW; one product an instruction took 87, 80 and 88, 128 x 128 tiles of 256
 // threads 111, 132 and 97.
-// Few rows (a batch of a few tokens against the whole vocabulary, bound by reading W) take
-// 16-row tiles, 2 x 8 products a thread.
+// Up to 16 rows (a batch of a few tokens against the whole vocabulary) take 16-row tiles, 2 x 8
+// products a thread: loss and gradients of 16 tokens, 50000 words, d = 1024, 394 us (595 in
+// 64-row tiles); 32 tokens 628 us in 64-row tiles (712 in 16-row ones).
 constexpr int SM = 64, SN = 128, SK = 16, kGemmThreads = 128;
-constexpr int kFewRows = 32;  // at most so many rows take 16-row tiles
+constexpr int kFewRows = 16;  // at most so many rows take 16-row tiles
 struct Sgemm {
   const float *A, *B;
   float* out;
