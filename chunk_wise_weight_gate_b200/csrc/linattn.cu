@@ -429,10 +429,12 @@ template <typename T>
 cudaError_t launch_step(const ipttt_linattn_params& p, float* S, const void* q, const void* k, const void* v,
                         const float* ld, const int32_t* starts, void* o, int* status, cudaStream_t st) {
   const int blocks = p.B * p.H, G = p.H / p.Hkv;
-  // half rows of the state (of 128) where (row, head) pairs alone fill the SMs twice, else quarter
-  // rows.  640 pairs of 128 x 128: 16.8 us with 64 columns and 4 loads ahead a thread, 18.0 with
-  // 32 columns, 17.4 with 128 and 8 loads, 20.3 with 128 and 16 (12.9 at the copy bandwidth).
-  if (blocks >= 296)
+  // half rows of the state (of 128) where (row, head) pairs alone nearly fill the SMs, else quarter
+  // rows: 80 pairs of 128 x 128, with the state in L2, 3.3 us in quarters, 3.5 in halves; 140
+  // pairs 4.1 and 3.8, 240 pairs 5.8 and 5.3.  From HBM, 640 pairs: 16.8 us with 64 columns and
+  // 4 loads ahead a thread, 18.0 with 32 columns, 17.4 with 128 and 8 loads, 20.3 with 128
+  // and 16 (12.9 at the copy bandwidth).
+  if (blocks >= 128)
     k_step<T, 64, 4><<<dim3(blocks, (p.Dv + 63) / 64), kThreads, 0, st>>>(
         S, static_cast<const T*>(q), static_cast<const T*>(k), static_cast<const T*>(v), ld, starts, static_cast<T*>(o),
         p.H, G, p.Dk, p.Dv, p.ldq, p.ldk, p.ldv, p.ldo, p.scale, status);
@@ -542,6 +544,8 @@ bool any_of(const void* out, std::initializer_list<const void*> in) {
   return std::find(in.begin(), in.end(), out) != in.end();
 }
 
+// bf16 of their widths always, short rows too: 20 heads of 128, 8192 tokens 73 us (958 on the CUDA
+// cores), 64 tokens 12.6 (24.7), 16 tokens 12.5 (12.0).
 bool on_tensor_cores(const ipttt_linattn_params& p) { return p.dtype == IPTTT_BF16 && tc_takes(p.Dk, p.Dv); }
 
 struct Work {
