@@ -38,6 +38,7 @@
 #include <atomic>
 
 #include "linattn.h"
+#include "linattn_smem.h"
 #include "tc.cuh"
 #include "tc_kernels.h"
 
@@ -50,22 +51,15 @@ namespace {
 
 constexpr int CH = kTcChunk;
 constexpr int kOutWarp = 4;  // first of the 8 warps that turn scores into P and write the output
-// Per head: pw[128 + n] = gamma^n for 0 <= n <= 128 and 0 for n < 0, then gamma^{31 - n}, n < 32.
-constexpr int kPw = 260, kTab = kPw + 32;
 
 enum Kind { FORWARD = 0, REVERSE = 1, STATES = 2 };  // STATES: a segment's own state alone, either way
 
 template <int DA, int DC, bool STATE>
 struct Cfg {
-  static constexpr int ASLOT = 256 * (DA > DC ? DA : DC);  // an a tile, then the output tile in its place
-  static constexpr int SLOT = 256 * (DA > DC ? DA : DC);   // a b or a c tile
-  static constexpr int NA = STATE ? 0 : 2;
-  static constexpr int LO = 256 * DA * (STATE ? 2 : 1);  // lo half of the scaled B (STATES: of two chunks in turn)
-  static constexpr int FB = STATE ? 0 : DA * DC * 2;  // bf16 state
-  static constexpr int MISC = 2 * kTab * 4 + 256;
-  static constexpr int FIT = (232448 - NA * ASLOT - LO - FB - MISC) / SLOT;
-  static constexpr int NS = FIT < 6 ? FIT : 6;
-  static constexpr int SMEM = NA * ASLOT + NS * SLOT + LO + FB + MISC;
+  using Mem = Smem<DA, DC, STATE>;
+  static constexpr int SLOT = Mem::SLOT;
+  static constexpr int NS = Mem::NS;
+  static constexpr int SMEM = Mem::BYTES;
   static constexpr int NC = DA * DC / 256;   // state columns a thread holds
   static constexpr int SW = STATE ? 4 : 12;  // first of the 8 state warps
   static constexpr int THREADS = 32 * (SW + 8);
@@ -195,15 +189,16 @@ template <int DA, int DC, int KIND>
 __global__ void __launch_bounds__(Cfg<DA, DC, KIND == STATES>::THREADS, 1) k_pass_tc(const __grid_constant__ TcArgs ta) {
   constexpr bool STATE = KIND == STATES;
   using Cf = Cfg<DA, DC, STATE>;
-  constexpr int NS = Cf::NS, SLOT = Cf::SLOT, ASLOT = Cf::ASLOT, NC = Cf::NC;
+  using Mem = typename Cf::Mem;
+  constexpr int NS = Cf::NS, SLOT = Cf::SLOT, NC = Cf::NC;
   const Pass& p = ta.p;
   extern __shared__ __align__(1024) uint8_t smem[];
-  uint8_t* a_buf = smem;                  // [2][ASLOT], chunks in turn
-  uint8_t* ring = smem + Cf::NA * ASLOT;  // [NS][SLOT]: b, c, b, c, ...
-  uint8_t* lo_buf = ring + NS * SLOT;
-  uint8_t* f_buf = lo_buf + Cf::LO;
-  float* tabs = reinterpret_cast<float*>(f_buf + Cf::FB);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(tabs + 2 * kTab);
+  uint8_t* a_buf = smem;                  // [2][SLOT], chunks in turn
+  uint8_t* ring = smem + Mem::at_ring;    // [NS][SLOT]: b, c, b, c, ...
+  uint8_t* lo_buf = smem + Mem::at_lo;
+  uint8_t* f_buf = smem + Mem::at_f;
+  float* tabs = reinterpret_cast<float*>(smem + Mem::at_tabs);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Mem::at_bars);
   uint64_t *full = bars, *empty = bars + NS;
   // Pairs are taken in turn by even and odd chunks, where a waiter may be a chunk behind.
   uint64_t* sc_full = bars + 2 * NS;     // [2]
@@ -212,7 +207,8 @@ __global__ void __launch_bounds__(Cfg<DA, DC, KIND == STATES>::THREADS, 1) k_pas
   uint64_t *a_full = sc_full + 8, *a_empty = sc_full + 10;  // [2]: the a buffers
   uint64_t *p_ready = sc_full + 12, *f_ready = sc_full + 13, *o_full = sc_full + 14, *o_free = sc_full + 15;
   uint64_t *tab_ready = sc_full + 16, *f_free = sc_full + 17, *drain = sc_full + 18;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  static_assert(Mem::bars(NS) == 2 * NS + 19, "the barriers above");
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Mem::at_words);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   uint32_t* issued = tmem_slot + 2;  // ring tiles and a tiles whose loads were issued
 
@@ -299,7 +295,7 @@ __global__ void __launch_bounds__(Cfg<DA, DC, KIND == STATES>::THREADS, 1) k_pas
           ++tl;
           if constexpr (!STATE) {
             LA_WAIT(&a_empty[cc & 1], (cc >> 1) ^ 1u);
-            load(a_buf + (cc & 1) * ASLOT, &ta.ma, &a_full[cc & 1], DA, it.h / p.ga * DA, ch, it.b);
+            load(a_buf + (cc & 1) * SLOT, &ta.ma, &a_full[cc & 1], DA, it.h / p.ga * DA, ch, it.b);
             issued[1] = cc + 1;
           }
           LA_WAIT(&empty[tl % NS], (tl / NS) ^ 1u);
@@ -331,7 +327,7 @@ __global__ void __launch_bounds__(Cfg<DA, DC, KIND == STATES>::THREADS, 1) k_pas
         const uint64_t a_k = k_major(a_buf), b_k = k_major(ring), f_mn = mn_major(f_buf, DA * 128);
         for (uint32_t c = 0; c < total; ++c) {
           const uint32_t sb = tile(2 * c), sc = tile(2 * c + 1);
-          const uint64_t da = a_k + (c & 1) * (ASLOT / 16), db = b_k + sb * (SLOT / 16), dc = c_mn + sc * (SLOT / 16);
+          const uint64_t da = a_k + (c & 1) * (SLOT / 16), db = b_k + sb * (SLOT / 16), dc = c_mn + sc * (SLOT / 16);
           LA_WAIT(&full[sb], 2 * c / NS);
           LA_WAIT(&a_full[c & 1], c >> 1);
           tc_fence_after();
@@ -477,7 +473,7 @@ __global__ void __launch_bounds__(Cfg<DA, DC, KIND == STATES>::THREADS, 1) k_pas
           const float win = in && write ? pw[rev ? len - row - lag : row + 1] : 0.0f;
           const float s1 = win * p.scale;
           // the output goes out through the a tile's place: (1) and (2) are done with it
-          uint8_t* stage = a_buf + (cc & 1) * ASLOT + half * (256 * HC);
+          uint8_t* stage = a_buf + (cc & 1) * SLOT + half * (256 * HC);
           LA_WAIT_WARP(o_full, cc);
           tc_fence_after();
 #pragma unroll 1
@@ -736,7 +732,6 @@ __global__ void __launch_bounds__(Cfg<DA, DC, KIND == STATES>::THREADS, 1) k_pas
 template <int DA, int DC, int KIND>
 cudaError_t launch(const TcArgs& a, cudaStream_t st) {
   using Cf = Cfg<DA, DC, KIND == STATES>;
-  static_assert(Cf::SMEM <= 232448 && Cf::NS >= 3, "ring");
   // once a device: the shared memory, and a check of the registers.  The register split takes what
   // the launch gives: with less, the state's warps would wait for good.
   static std::atomic<bool> ready[64];
