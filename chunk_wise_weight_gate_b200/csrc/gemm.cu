@@ -186,6 +186,9 @@ __device__ __forceinline__ bool keep_row(const Args& a, const Tile& t, int m) {
 }
 
 constexpr float kLog2e = 1.4426950408889634f;
+// ex2.approx is off by 2^-22 of the result, as much again as the rounding of its argument makes at
+// |x| = 4, and costs one instruction where expf takes several in an epilogue that every logit passes
+// through: loss and lse are off by 8.6e-7 of their size instead of 8e-8.
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -224,7 +227,8 @@ __device__ __forceinline__ void row_epilogue(const Args& a, uint32_t tacc, int m
       float top = mx;
 #pragma unroll
       for (int e = 0; e < 32; ++e) top = fmaxf(top, __uint_as_float(r[e]));
-      const float base = top == -INFINITY ? 0.0f : top;  // no logit above -inf yet: every term is 0
+      // no logit above -inf yet: every term is 0; one of +inf: its term and the sum are infinite
+      const float base = fabsf(top) == INFINITY ? 0.0f : top;
       float acc[4] = {};
 #pragma unroll
       for (int e = 0; e < 32; ++e) acc[e & 3] += exp2_fast((__uint_as_float(r[e]) - base) * kLog2e);

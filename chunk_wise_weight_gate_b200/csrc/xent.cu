@@ -186,10 +186,12 @@ cudaError_t sgemm(const Sgemm& g, cudaStream_t st) {
 
 // ------------------------------------------------------------------ the rows' statistics and gradients
 
-__device__ __forceinline__ float2 merge(float2 a, float2 b) {  // (maximum, sum) of two sets of logits
+// (maximum, sum) of two sets of logits.  fmaxf leaves NaN out, the sums do not: a NaN as a set's maximum or
+// sum makes the sum NaN.  At its own maximum a sum stays as it is (an infinity minus itself is
+// NaN): a logit of infinity gives an infinite lse, logits of -infinity alone one of -infinity.
+__device__ __forceinline__ float2 merge(float2 a, float2 b) {
   const float m = fmaxf(a.x, b.x);
-  if (m == -INFINITY) return make_float2(m, 0.0f);
-  return make_float2(m, a.y * expf(a.x - m) + b.y * expf(b.x - m));
+  return make_float2(m, (a.x == m ? a.y : a.y * expf(a.x - m)) + (b.x == m ? b.y : b.y * expf(b.x - m)));
 }
 
 __device__ __forceinline__ float2 block_merge(float2 v, float2* sh) {
