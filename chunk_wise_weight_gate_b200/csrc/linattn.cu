@@ -50,6 +50,7 @@ __device__ __forceinline__ void fma4(float4& acc, float s, float4 v) {
   acc.z = fmaf(s, v.z, acc.z);
   acc.w = fmaf(s, v.w, acc.w);
 }
+__device__ __forceinline__ bool finite4(float4 v) { return isfinite(v.x) && isfinite(v.y) && isfinite(v.z) && isfinite(v.w); }
 __device__ __forceinline__ float4 scale4(float4 a, float s) { return make_float4(a.x * s, a.y * s, a.z * s, a.w * s); }
 
 // ------------------------------------------------------------------ document starts
@@ -114,6 +115,7 @@ __global__ void __launch_bounds__(kThreads) k_pass(const Pass p) {
   const float g = p.log_decay[h];
   if (threadIdx.x == 0 && !(g <= 0.0f)) set_status(p.status, IPTTT_ERR_ARG);
   if (threadIdx.x <= L) pw[threadIdx.x] = decay_pow(g, threadIdx.x);
+  const bool no_past = decay_pow(g, 1) == 0.0f;
   const T* A = static_cast<const T*>(p.a) + (long long)b * p.T * p.lda + (long long)(h / p.ga) * Da;
   const T* Bm = static_cast<const T*>(p.b) + (long long)b * p.T * p.ldb + (long long)(h / p.gb) * Da;
   const T* C = static_cast<const T*>(p.c) + (long long)b * p.T * p.ldc + (long long)(h / p.gc) * p.Dc;
@@ -179,12 +181,21 @@ __global__ void __launch_bounds__(kThreads) k_pass(const Pass p) {
       const int i = threadIdx.x;
       const bool in = p.rev ? i >= last_start : i < first_start;
       const bool out = p.rev ? i < first_start : i >= last_start;
-      win[i] = in && i < len ? pw[p.rev ? len - i - lag : i + 1] : 0.0f;
-      wout[i] = out && i < len ? pw[p.rev ? i : len - 1 - i] : 0.0f;
+      const int ni = p.rev ? len - i - lag : i + 1, no = p.rev ? i : len - 1 - i;
+      win[i] = in && i < len && !(no_past && ni > 0) ? pw[ni] : kNone;
+      wout[i] = out && i < len && !(no_past && no > 0) ? pw[no] : kNone;
     }
     __syncthreads();
     if (!only_state) {
       float s[2][2] = {};
+      int from[2], to[2];  // the tokens of row i's document on the side the pass looks at: [from, to)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int i = ty + 16 * u;
+        const uint32_t below = w & ((2u << i) - 1u), above = i == 31 ? 0u : w >> (i + 1);
+        from[u] = p.rev || no_past ? i : (below ? 31 - __clz(below) : 0);
+        to[u] = p.rev && !no_past ? (above ? i + __ffs(above) : L) : i + 1;
+      }
       for (int d = 0; d < Da; d += 4) {
         float4 x[2], y[2];
 #pragma unroll
@@ -201,14 +212,10 @@ __global__ void __launch_bounds__(kThreads) k_pass(const Pass p) {
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const int i = ty + 16 * u;
-        // the tokens of i's document on the side the pass looks at: [from, to)
-        const uint32_t below = w & ((2u << i) - 1u), above = i == 31 ? 0u : w >> (i + 1);
-        const int from = p.rev ? i : (below ? 31 - __clz(below) : 0);
-        const int to = p.rev ? (above ? i + __ffs(above) : L) : i + 1;
 #pragma unroll
         for (int v = 0; v < 2; ++v) {
           const int j = tx + 16 * v;
-          sp[i * kSp + j] = j >= from && j < to ? s[u][v] * pw[abs(i - j)] : 0.0f;
+          sp[i * kSp + j] = j >= from[u] && j < to[u] ? s[u][v] * pw[abs(i - j)] : 0.0f;
         }
       }
       __syncthreads();
@@ -238,7 +245,11 @@ __global__ void __launch_bounds__(kThreads) k_pass(const Pass p) {
       for (int u = 0; u < 2; ++u) {
         const int i = ty + 16 * u;
         if (i >= len || c >= p.Dc) continue;
-        if (win[i] != 0.0f) fma4(o[u], win[i], e[u]);
+        if (!finite4(o[u])) {  // 0 times a value of a token that the row does not see is NaN: those it sees alone
+          o[u] = zero;
+          for (int j = from[u]; j < min(to[u], len); ++j) fma4(o[u], sp[i * kSp + j], load4(sc + j * kSlice + 4 * tx));
+        }
+        if (win[i] >= 0.0f) fma4(o[u], win[i], e[u]);
         const long long at = ((long long)b * p.T + t0 + i) * p.ldo + (long long)h * p.Dc + c;
         const float4 r = scale4(o[u], p.scale);
         if (p.out_f32) store4(static_cast<float*>(p.out) + at, r);
@@ -246,19 +257,19 @@ __global__ void __launch_bounds__(kThreads) k_pass(const Pass p) {
       }
       __syncthreads();
     }
-    const float keep = w ? 0.0f : pw[len - lag];
+    const float keep = w || (no_past && len > lag) ? kNone : pw[len - lag];
     // four rows of the state at a time, so that a row of c is read once for them
     for (int r0 = ty; r0 < Da; r0 += 64) {
       float4 f[4];
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         const int r = r0 + 16 * u;
-        f[u] = keep != 0.0f && r < Da ? scale4(load4(F + r * kSlice + 4 * tx), keep) : zero;
+        f[u] = keep >= 0.0f && r < Da ? scale4(load4(F + r * kSlice + 4 * tx), keep) : zero;
       }
 #pragma unroll 4
       for (int j = 0; j < len; ++j) {
         const float x = wout[j];
-        if (x == 0.0f) continue;
+        if (x < 0.0f) continue;
         const float4 v = scale4(load4(sc + j * kSlice + 4 * tx), x);
 #pragma unroll
         for (int u = 0; u < 4; ++u)
@@ -272,15 +283,21 @@ __global__ void __launch_bounds__(kThreads) k_pass(const Pass p) {
 
   float* dst = nullptr;
   float mul = 1.0f;
+  bool none = false;
   if (only_state) {
     dst = p.seg_state + (bh * p.segs + seg) * nstate;
   } else if (p.fin && (p.rev ? seg == 0 : seg == p.segs - 1)) {
     dst = p.fin + bh * nstate;
-    if (p.fin_scale) mul = p.scale * decay_pow(g, 1);
+    if (p.fin_scale) {
+      mul = p.scale * decay_pow(g, 1);
+      none = no_past;
+    }
   }
   if (dst && c < p.Dc) {
-    for (int r = ty; r < Da; r += 16)  // a thread's own elements: no barrier since they were written
-      store4(dst + (size_t)r * p.Dc + c, scale4(*reinterpret_cast<const float4*>(F + r * kSlice + 4 * tx), mul));
+    for (int r = ty; r < Da; r += 16) {  // a thread's own elements: no barrier since they were written
+      const float4 f = load4(F + r * kSlice + 4 * tx);
+      store4(dst + (size_t)r * p.Dc + c, none ? make_float4(0.0f, 0.0f, 0.0f, 0.0f) : scale4(f, mul));
+    }
   }
 }
 
@@ -300,7 +317,8 @@ __global__ void __launch_bounds__(kThreads) k_prefix(const Pass p) {
     const int lo = s * p.seg_chunks * p.chunk, hi = min(p.T, lo + p.seg_chunks * p.chunk);
     uint32_t any = 0;
     for (int w = lo / 32; words && 32 * w < hi; ++w) any |= words[w];
-    keep[s] = any ? 0.0f : decay_pow(g, hi - lo - (p.rev && hi == p.T ? 1 : 0));
+    const int n = hi - lo - (p.rev && hi == p.T ? 1 : 0);
+    keep[s] = any || (decay_pow(g, 1) == 0.0f && n > 0) ? kNone : decay_pow(g, n);
   }
   __syncthreads();
   const size_t e = 4 * ((size_t)blockIdx.x * kThreads + threadIdx.x);
@@ -330,7 +348,7 @@ __global__ void __launch_bounds__(kThreads) k_prefix(const Pass p) {
       store4(x + (size_t)s * nstate, f);
       if (n0 + u == p.segs - 1) continue;
       const float k = keep[s];
-      if (k == 0.0f) {  // whatever f holds
+      if (k < 0.0f) {  // whatever f holds
         f = own[u];
       } else {
         float4 y = own[u];

@@ -50,6 +50,11 @@ struct Pass {
   int* status;
 };
 
+// The weight of what a token does not see: another document's, or any past where gamma is 0 (below
+// the smallest fp32 number).  It is left out, not multiplied by 0, which would make NaN of a value
+// that is not finite; a weight that underflows is 0 and does make NaN of an infinity, which
+// the definition keeps.
+constexpr float kNone = -1.0f;
 __device__ __forceinline__ float decay_pow(float g, int n) { return n <= 0 ? 1.0f : expf(g * (float)n); }
 
 // The CUDA-core pass (any widths up to 256, fp32 or bf16 operands), chunks of 32 tokens.

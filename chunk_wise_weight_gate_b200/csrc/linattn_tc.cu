@@ -29,6 +29,11 @@
 // overran the instruction caches (a third of all stalls); one issuing thread instead of
 // two: 68 us; tiles brought into L2 ahead of their loads: 72 us.
 //
+// Masked places are products with 0, which is NaN for a value that is not finite.  An item that held one
+// is done again at the end, token by token (`walk`): the chunks' loop pays for telling by the state
+// alone, 0.5% (8 x 2047 tokens of 24 heads 114.2 -> 115.2 us); looking at every output too cost 2%, a
+// walk within the item with its state in registers 3%.
+//
 // Rows are cut into segments when rows and heads alone leave SMs idle: a first pass (STATES) forms
 // each segment's own state from b and c alone (1.5 to 1.7 us a chunk: 64 KB, HBM), and the full
 // pass starts each segment from their sum under the decay (many segments: from what k_prefix left).
@@ -156,16 +161,20 @@ __device__ __forceinline__ int nearest_start_warp(const Pass& p, int b, int at, 
 }
 
 // Factor with which segment s's own state, and the initial state (s = -1), reach the
-// segment of tokens [lo, hi): 0 where a document starts between.
+// segment of tokens [lo, hi): kNone where a document starts between, or there is no past.
 __device__ __forceinline__ float reach(const Pass& p, float g, int s, int lo, int hi, int start) {
+  bool seen;
+  int n;  // tokens between
   if (p.rev) {
-    if (s < 0) return start < p.T ? 0.0f : decay_pow(g, p.T - 1 - hi);
     const int s0 = s * p.seg_chunks * CH;
-    return s0 <= start ? decay_pow(g, s0 - hi) : 0.0f;
+    seen = s < 0 ? start >= p.T : s0 <= start;
+    n = s < 0 ? p.T - 1 - hi : s0 - hi;
+  } else {
+    const int end = s < 0 ? 0 : (s + 1) * p.seg_chunks * CH;
+    seen = s < 0 ? start < 0 : end > start;
+    n = lo - end;
   }
-  if (s < 0) return start >= 0 ? 0.0f : decay_pow(g, lo);
-  const int end = (s + 1) * p.seg_chunks * CH;
-  return end > start ? decay_pow(g, lo - end) : 0.0f;
+  return seen && (n <= 0 || decay_pow(g, 1) != 0.0f) ? decay_pow(g, n) : kNone;
 }
 
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
@@ -173,16 +182,139 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+// What the roles tell one another besides barriers; from W_ODD on, a bit for each item of the block.
+enum Word { W_TMEM = 0, W_ABORT = 1, W_TILES = 2, W_A_TILES = 3, W_ODD = 4 };
+
 // mbar_wait_or_abort in few instructions: there are some twenty waits in the kernel.
-__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile int* abort) {
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile uint32_t* words) {
   bool done = mbar_try_wait(bar, parity);
   if (!done) {
     const uint64_t t0 = global_timer_ns();
 #pragma unroll 1
     do done = mbar_try_wait(bar, parity);
-    while (!done && !*abort && global_timer_ns() - t0 < kWaitLimitNs);
+    while (!done && !words[W_ABORT] && global_timer_ns() - t0 < kWaitLimitNs);
   }
   return done;
+}
+
+// Where an item's last state goes (null: nowhere), and the factor on it; none: it is 0, as there is no
+// past that it could be the gradient of.
+struct Last {
+  float* dst;
+  float mul;
+  bool none;
+};
+template <bool STATE>
+__device__ __forceinline__ Last last_of(const Pass& p, const Item& it, float g) {
+  const size_t bh = (size_t)it.b * p.H + it.h, nstate = (size_t)p.Da * p.Dc;
+  Last to = {nullptr, 1.0f, false};
+  if (STATE) {
+    to.dst = p.seg_state + (bh * p.segs + it.seg) * nstate;
+  } else if (p.fin && (p.rev ? it.seg == 0 : it.seg == it.segs - 1)) {
+    to.dst = p.fin + bh * nstate;
+    if (p.fin_scale) {
+      to.mul = p.scale * decay_pow(g, 1);
+      to.none = decay_pow(g, 1) == 0.0f;
+    }
+  }
+  return to;
+}
+
+// An item by the recurrence itself, token by token, on the 256 threads of the state warps (tid).  For items
+// alone that hold a value that is not finite: 0 times it, in masked places, is NaN, and the chunk's
+// other tokens and documents must not take it.  A thread has a column of the state, tid % DC, and
+// ROWS of its rows from tid / DC * ROWS on; the state lies in F (shared memory, as registers would
+// cost the chunks' loop), kWalk tokens at a time in `room`, as fp32.  A barrier joins the threads,
+// `met` times so far; false: a wait gave up.
+template <int DA, int DC, bool STATE>
+__device__ __forceinline__ bool walk(const Pass& p, const Item& it, float* F, float* room, int tid, uint64_t* bar,
+                                     uint32_t& met, volatile uint32_t* words) {
+  constexpr int ROWS = DA * DC / 256, GROUPS = 256 / DC;
+  float *sa = room, *sb = sa + kWalk * DA, *sc = sb + kWalk * DA;  // [kWalk][DA], [kWalk][DA], [kWalk][DC]
+  float* so = sc + kWalk * DC;                                     // [kWalk][GROUPS][DC]
+  const int col = tid % DC, r0 = tid / DC * ROWS;
+  const size_t bh = (size_t)it.b * p.H + it.h, nstate = (size_t)DA * DC;
+  const int lo = it.first * CH, hi = min(p.T, it.last * CH);
+  const uint32_t* starts = p.starts ? p.starts + it.b * p.words : nullptr;
+  const float g = p.log_decay[it.h], gamma = decay_pow(g, 1);
+  float* f = F + r0 * DC + col;  // the thread's first element; its rows are DC apart
+  auto meet = [&] {
+    __syncwarp();
+    if (tid % 32 == 0) mbar_arrive(bar);
+    return __all_sync(0xffffffffu, wait_for(bar, met++ & 1u, words)) != 0;
+  };
+#pragma unroll 1
+  for (int e = 0; e < ROWS; ++e) f[e * DC] = 0.0f;
+  if constexpr (!STATE) {
+    const bool prefixed = p.prefixed && it.segs > 1;
+    auto add = [&](const float* src, int transposed, float w) {
+#pragma unroll 1
+      for (int e = 0; e < ROWS; ++e)
+        f[e * DC] = fmaf(w, src[transposed ? (size_t)col * DA + r0 + e : (size_t)(r0 + e) * DC + col], f[e * DC]);
+    };
+    const int start = nearest_start_warp(p, it.b, p.rev ? hi : lo, tid & 31);
+    // s = -1: the initial state; then the segments before this one on the pass's way
+    for (int s = prefixed ? it.segs : -1; s < it.segs; s = s < 0 && p.rev ? it.seg + 1 : s + 1) {
+      if (s >= 0 && !p.rev && s >= it.seg) break;
+      const float w = reach(p, g, s, lo, hi, start);
+      if (s < 0 && p.init && w >= 0.0f) add(p.init + bh * nstate, p.init_t, p.init_mul * w);
+      if (s >= 0 && w >= 0.0f) add(p.seg_in + (bh * p.segs + s) * nstate, p.seg_t, w);
+    }
+    if (prefixed) add(p.seg_in + (bh * p.segs + it.seg) * nstate, p.seg_t, 1.0f);
+  }
+  const __nv_bfloat16* A = static_cast<const __nv_bfloat16*>(p.a) + (long long)it.b * p.T * p.lda + (long long)(it.h / p.ga) * DA;
+  const __nv_bfloat16* B = static_cast<const __nv_bfloat16*>(p.b) + (long long)it.b * p.T * p.ldb + (long long)(it.h / p.gb) * DA;
+  const __nv_bfloat16* C = static_cast<const __nv_bfloat16*>(p.c) + (long long)it.b * p.T * p.ldc + (long long)(it.h / p.gc) * DC;
+  if (!meet()) return false;
+#pragma unroll 1
+  for (int n0 = 0; n0 < hi - lo; n0 += kWalk) {
+    const int n = min(kWalk, hi - lo - n0);
+    auto token = [&](int k) { return p.rev ? hi - 1 - n0 - k : lo + n0 + k; };
+#pragma unroll 1
+    for (int i = tid; i < n * DA; i += 256) {
+      const int t = token(i / DA);
+      if constexpr (!STATE) sa[i] = to_f(A[t * p.lda + i % DA]);
+      sb[i] = to_f(B[t * p.ldb + i % DA]);
+    }
+#pragma unroll 1
+    for (int i = tid; i < n * DC; i += 256) sc[i] = to_f(C[token(i / DC) * p.ldc + i % DC]);
+    if (!meet()) return false;
+#pragma unroll 1
+    for (int k = 0; k < n; ++k) {
+      const int t = token(k);
+      const bool start = starts && (starts[t / 32] >> (t % 32) & 1u);
+      // no decay before the last token, whose state's gradient comes in as it is
+      const float keep = p.rev && t == p.T - 1 ? 1.0f : gamma;
+      const bool drop = keep == 0.0f || (!p.rev && start);
+      const bool ends = p.rev && start;  // the document, on the way back
+      const float c = sc[k * DC + col];
+      float o = 0.0f;
+#pragma unroll 4
+      for (int e = 0; e < ROWS; ++e) {
+        const float x = fmaf(sb[k * DA + r0 + e], c, drop ? 0.0f : keep * f[e * DC]);
+        if constexpr (!STATE) o = fmaf(sa[k * DA + r0 + e], x, o);
+        f[e * DC] = ends ? 0.0f : x;
+      }
+      if constexpr (!STATE) so[(k * GROUPS + tid / DC) * DC + col] = o;
+    }
+    if (!meet()) return false;
+    if constexpr (!STATE) {
+#pragma unroll 1
+      for (int i = tid; i < n * DC; i += 256) {
+        const int k = i / DC, d = i % DC;
+        float o = 0.0f;
+#pragma unroll
+        for (int q = 0; q < GROUPS; ++q) o += so[(k * GROUPS + q) * DC + d];
+        const long long at = ((long long)it.b * p.T + token(k)) * p.ldo + (long long)it.h * DC + d;
+        if (p.out_f32) static_cast<float*>(p.out)[at] = p.scale * o;
+        else static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(p.scale * o);
+      }
+    }
+  }
+  const Last to = last_of<STATE>(p, it, g);
+#pragma unroll 1
+  for (int e = 0; to.dst && e < ROWS; ++e) to.dst[(size_t)(r0 + e) * DC + col] = to.none ? 0.0f : to.mul * f[e * DC];
+  return true;
 }
 
 template <int DA, int DC, int KIND>
@@ -207,10 +339,9 @@ __global__ void __launch_bounds__(Cfg<DA, DC, KIND == STATES>::THREADS, 1) k_pas
   uint64_t *a_full = sc_full + 8, *a_empty = sc_full + 10;  // [2]: the a buffers
   uint64_t *p_ready = sc_full + 12, *f_ready = sc_full + 13, *o_full = sc_full + 14, *o_free = sc_full + 15;
   uint64_t *tab_ready = sc_full + 16, *f_free = sc_full + 17, *drain = sc_full + 18;
-  static_assert(Mem::bars(NS) == 2 * NS + 19, "the barriers above");
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Mem::at_words);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  uint32_t* issued = tmem_slot + 2;  // ring tiles and a tiles whose loads were issued
+  uint64_t *item_end = sc_full + 19, *all_done = sc_full + 20, *meet = sc_full + 21;
+  static_assert(Mem::bars(NS) == 2 * NS + 22, "the barriers above");
+  volatile uint32_t* words = reinterpret_cast<volatile uint32_t*>(smem + Mem::at_words);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (smem_u32(smem) % 1024 != 0) {  // the swizzled tiles need it; uniform over the block
@@ -237,8 +368,10 @@ __global__ void __launch_bounds__(Cfg<DA, DC, KIND == STATES>::THREADS, 1) k_pas
     mbar_init(o_free, 8);
     mbar_init(tab_ready, STATE ? 8 : 16);
     mbar_init(drain, STATE ? 1 : 2);
-    *abort_flag = 0;
-    issued[0] = issued[1] = 0;
+    mbar_init(item_end, 8);
+    mbar_init(all_done, STATE ? 8 : 16);
+    mbar_init(meet, 8);
+    for (int w = W_ABORT; w < Mem::WORDS; ++w) words[w] = 0;
     fence_mbar_init();
   }
   if (warp == 0 && lane == 0) {
@@ -250,13 +383,13 @@ __global__ void __launch_bounds__(Cfg<DA, DC, KIND == STATES>::THREADS, 1) k_pas
     prefetch_tmap(&ta.mc);
   }
   if (warp == 1) {
-    tmem_alloc(tmem_slot, 512);
+    tmem_alloc(reinterpret_cast<uint32_t*>(smem + Mem::at_words) + W_TMEM, 512);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tm = *tmem_slot;
+  const uint32_t tm = words[W_TMEM];
   // The pass may start while the one for its segments' states still runs (it reads them at
   // its cut segments' starts, and ends after it in any case).
   if (STATE) launch_dependents();
@@ -264,16 +397,18 @@ __global__ void __launch_bounds__(Cfg<DA, DC, KIND == STATES>::THREADS, 1) k_pas
   const int step = rev ? -1 : 1;
   // STATES has room for two chunks' lo halves and D, so that a chunk's scaling runs beside the last one's (4)
   constexpr uint32_t d_col = STATE ? 0 : col_d(DC), two_col = STATE ? DC : 0, two_lo = STATE ? 256 * DA / 16 : 0;
+  auto mark_odd = [&](uint32_t n) { atomicOr(reinterpret_cast<uint32_t*>(smem + Mem::at_words) + W_ODD + n / 32, 1u << n % 32); };
+  auto is_odd = [&](uint32_t n) { return (words[W_ODD + n / 32] >> n % 32 & 1u) != 0; };
   bool ok = true;
   // a wait that gives up ends the block's work: every role leaves its loops
 #define LA_WAIT(bar, parity)                                  \
-  if (!wait_for(bar, (parity) & 1u, abort_flag)) {           \
+  if (!wait_for(bar, (parity) & 1u, words)) {           \
     ok = false;                                               \
     break;                                                    \
   }
   // of all lanes of a warp alike: what follows are warp-wide TMEM accesses
 #define LA_WAIT_WARP(bar, parity)                                                      \
-  if (!__all_sync(0xffffffffu, wait_for(bar, (parity) & 1u, abort_flag))) {           \
+  if (!__all_sync(0xffffffffu, wait_for(bar, (parity) & 1u, words))) {           \
     ok = false;                                                                        \
     break;                                                                             \
   }
@@ -296,14 +431,14 @@ __global__ void __launch_bounds__(Cfg<DA, DC, KIND == STATES>::THREADS, 1) k_pas
           if constexpr (!STATE) {
             LA_WAIT(&a_empty[cc & 1], (cc >> 1) ^ 1u);
             load(a_buf + (cc & 1) * SLOT, &ta.ma, &a_full[cc & 1], DA, it.h / p.ga * DA, ch, it.b);
-            issued[1] = cc + 1;
+            words[W_A_TILES] = cc + 1;
           }
           LA_WAIT(&empty[tl % NS], (tl / NS) ^ 1u);
           load(ring + tl % NS * SLOT, &ta.mc, &full[tl % NS], DC, it.h / p.gc * DC, ch, it.b);
           ++tl;
         }
       }
-      issued[0] = tl;
+      words[W_TILES] = tl;
     } else if ((warp == 1 || warp == 2) && lane == 0 && !(STATE && warp == 1)) {
       // Two threads issue the MMAs, warp 1's (1), (2) and (3), warp 2's (4): issuing takes longer than
       // the tensor pipe does, and (4) is on the path that bounds a chunk, from state to state.
@@ -437,6 +572,9 @@ __global__ void __launch_bounds__(Cfg<DA, DC, KIND == STATES>::THREADS, 1) k_pas
                 const float* wt = pw + (rev ? -lane : lane);
                 tmem_ld_wait();
 #pragma unroll
+                for (int e = 0; e < 32; ++e)  // not times 0 alone: products of tokens far apart in size may overflow
+                  if (rev ? e < lane : e > lane) v[e] = 0u;
+#pragma unroll
                 for (int e = 0; e < 16; ++e)
                   w[e] = pack2(__uint_as_float(v[2 * e]) * wt[rev ? 2 * e : -2 * e],
                                __uint_as_float(v[2 * e + 1]) * wt[rev ? 2 * e + 1 : -2 * e - 1]);
@@ -470,7 +608,7 @@ __global__ void __launch_bounds__(Cfg<DA, DC, KIND == STATES>::THREADS, 1) k_pas
 
           const int lag = rev && t0 + len == p.T ? 1 : 0;
           const bool write = row < len;
-          const float win = in && write ? pw[rev ? len - row - lag : row + 1] : 0.0f;
+          const float win = in && write ? pw[rev ? len - row - lag : row + 1] : kNone;
           const float s1 = win * p.scale;
           // the output goes out through the a tile's place: (1) and (2) are done with it
           uint8_t* stage = a_buf + (cc & 1) * SLOT + half * (256 * HC);
@@ -485,7 +623,7 @@ __global__ void __launch_bounds__(Cfg<DA, DC, KIND == STATES>::THREADS, 1) k_pas
             float o[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) o[e] = p.scale * __uint_as_float(x[e]);
-            if (!any || win != 0.0f) {  // rows of another document take nothing of the state, whatever is in it
+            if (!any || win >= 0.0f) {  // rows of another document take nothing of the state, whatever is in it
 #pragma unroll
               for (int e = 0; e < 16; ++e) o[e] = fmaf(s1, __uint_as_float(y[e]), o[e]);
             }
@@ -522,7 +660,10 @@ __global__ void __launch_bounds__(Cfg<DA, DC, KIND == STATES>::THREADS, 1) k_pas
           }
         }
       }
-      if (lane == 0) bulk_wait<0>();
+      if (lane == 0) {
+        bulk_wait<0>();
+        mbar_arrive(all_done);
+      }
     }
   } else {
     if constexpr (!STATE) regs_inc<kRegsState>();
@@ -552,7 +693,6 @@ __global__ void __launch_bounds__(Cfg<DA, DC, KIND == STATES>::THREADS, 1) k_pas
         const bool prefixed = p.prefixed && it.segs > 1;
         const int start = !prefixed && (p.init || it.segs > 1) ? nearest_start_warp(p, it.b, rev ? hi : lo, lane) : 0;
         auto add = [&](const float* src, int transposed, float w) {
-          if (w == 0.0f) return;
           if (transposed) {
 #pragma unroll
             for (int e = 0; e < NC; ++e) f[e] = fmaf(w, src[(size_t)(c0 + e) * DA + row], f[e]);
@@ -567,20 +707,37 @@ __global__ void __launch_bounds__(Cfg<DA, DC, KIND == STATES>::THREADS, 1) k_pas
             }
           }
         };
-        if (p.init && !prefixed) add(p.init + bh * DA * DC, p.init_t, p.init_mul * reach(p, g, -1, lo, hi, start));
+        if (p.init && !prefixed) {
+          const float w = reach(p, g, -1, lo, hi, start);
+          if (w >= 0.0f) add(p.init + bh * DA * DC, p.init_t, p.init_mul * w);
+        }
         const int s0 = rev ? it.seg + 1 : 0, s1 = rev ? it.segs : it.seg;
         if (s0 < s1 || prefixed) wait_for_launch_before();
         if (prefixed) add(p.seg_in + (bh * p.segs + it.seg) * DA * DC, p.seg_t, 1.0f);
-        for (int s = s0; s < s1 && !prefixed; ++s)
-          add(p.seg_in + (bh * p.segs + s) * DA * DC, p.seg_t, reach(p, g, s, lo, hi, start));
+        for (int s = s0; s < s1 && !prefixed; ++s) {
+          const float w = reach(p, g, s, lo, hi, start);
+          if (w >= 0.0f) add(p.seg_in + (bh * p.segs + s) * DA * DC, p.seg_t, w);
+        }
       }
       LA_WAIT_WARP(tab_ready, ic);
 
+      // Masked places of b and c are multiplied by 0.  That is NaN for a value that is not finite: whatever
+      // its weight, D is then not finite, nor is the state until a document starts.  An item that met
+      // one is done again, by the recurrence itself.  (One of a touches its own row alone, where it
+      // belongs.)
+      auto look = [&] {
+        float odd = 0.0f;
+#pragma unroll
+        for (int e = 0; e < NC; ++e) odd = fmaf(f[e], 0.0f, odd);
+        if (isnan(odd)) mark_odd(ic);
+      };
       // f <- keep f + D of chunk number c
       auto advance = [&](float keep, uint32_t c) {
         tc_fence_after();
         const uint32_t addr = d_addr + two_col * (c & 1);
-        if (keep == 0.0f) {  // whatever f holds
+        if (keep < 0.0f) {  // whatever f holds
+          look();
+          keep = 0.0f;
 #pragma unroll
           for (int e = 0; e < NC; ++e) f[e] = 0.0f;
         }
@@ -671,7 +828,7 @@ __global__ void __launch_bounds__(Cfg<DA, DC, KIND == STATES>::THREADS, 1) k_pas
           __syncwarp();
           if (lane == 0) mbar_arrive(&conv_done[2 * (cc & 1) + half]);
         }
-        const float keep_now = any ? 0.0f : pw[len - lag];
+        const float keep_now = any ? kNone : pw[len - lag];
         if (n + 1 < it.last - it.first) weights(ch + step, next);
         if constexpr (STATE) {
           if (n > 0) {
@@ -690,34 +847,49 @@ __global__ void __launch_bounds__(Cfg<DA, DC, KIND == STATES>::THREADS, 1) k_pas
         advance(keep, cc - 1);
       }
       if (!ok) break;
-      float* dst = nullptr;
-      float mul = 1.0f;
-      if constexpr (STATE) {
-        dst = p.seg_state + (bh * p.segs + it.seg) * DA * DC;
-      } else if (p.fin && (rev ? it.seg == 0 : it.seg == it.segs - 1)) {
-        dst = p.fin + bh * DA * DC;
-        if (p.fin_scale) mul = p.scale * decay_pow(g, 1);
+      look();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(item_end);
+      const Last to = last_of<STATE>(p, it, g);
+      bool write = to.dst != nullptr;
+      if (!STATE && write && p.fin == p.init && it.segs == 1) {
+        // an item that is done again starts from the state that this would replace
+        LA_WAIT_WARP(item_end, ic);
+        write = !is_odd(ic);
       }
-      if (dst) {
+      if (write) {
+        float* dst = to.dst + (size_t)row * DC + c0;
 #pragma unroll
         for (int e = 0; e < NC; e += 4)
-          *reinterpret_cast<float4*>(dst + (size_t)row * DC + c0 + e) =
-              make_float4(mul * f[e], mul * f[e + 1], mul * f[e + 2], mul * f[e + 3]);
+          *reinterpret_cast<float4*>(dst + e) = make_float4(to.mul * f[e], to.mul * f[e + 1], to.mul * f[e + 2], to.mul * f[e + 3]);
       }
     }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(all_done);
+    do {  // (left by a wait that gives up)
+      if (!ok) break;
+      LA_WAIT_WARP(all_done, 0);  // the outputs have been written
+      uint32_t met = 0;
+#pragma unroll 1
+      for (uint32_t k = 0; ok && k < ic; ++k) {
+        if (k % 32 == 0 && words[W_ODD + k / 32] == 0) k += 31;
+        else if (is_odd(k)) ok = walk<DA, DC, STATE>(p, item_of(p, blockIdx.x + k * gridDim.x), reinterpret_cast<float*>(smem),
+                                                     reinterpret_cast<float*>(lo_buf), tid, meet, met, words);
+      }
+    } while (false);
   }
 #undef LA_WAIT
 #undef LA_WAIT_WARP
   if (!ok) {
-    *abort_flag = 1;
+    words[W_ABORT] = 1;
     set_status(p.status, IPTTT_ERR_TIMEOUT);
   }
 
   __syncthreads();
   if (!STATE && threadIdx.x == 0) wait_for_launch_before();
-  if (*abort_flag && threadIdx.x == 0) {
+  if (words[W_ABORT] && threadIdx.x == 0) {
     // copies that were issued land before the block's shared memory is given back
-    const uint32_t n = issued[0], na = issued[1];
+    const uint32_t n = words[W_TILES], na = words[W_A_TILES];
     for (uint32_t t = n > (uint32_t)NS ? n - NS : 0; t < n; ++t) mbar_wait(&full[t % NS], (t / NS) & 1);
     for (uint32_t t = na > 2 ? na - 2 : 0; t < na; ++t) mbar_wait(&a_full[t & 1], (t >> 1) & 1);
   }
@@ -752,7 +924,9 @@ cudaError_t launch(const TcArgs& a, cudaStream_t st) {
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3((unsigned)std::min(a.items, device_sms()));
+  const int blocks = std::min(a.items, device_sms());
+  if (blocks <= 0 || (a.items + blocks - 1) / blocks > kMostItems) return cudaErrorInvalidConfiguration;
+  cfg.gridDim = dim3((unsigned)blocks);
   cfg.blockDim = dim3(Cf::THREADS);
   cfg.dynamicSmemBytes = Cf::SMEM;
   cfg.stream = st;

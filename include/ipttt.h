@@ -434,10 +434,14 @@ IPTTT_API ipttt_status ipttt_qk_norm_rope_backward(const ipttt_qk_params* p, con
  * [B, H, Dk, Dv]; S_final_opt may be S0 itself.
  * Whole sequences are computed by chunks of tokens: the products of a chunk's
  * queries and keys under the decay, and the state carried over chunks.  A value that
- * is not finite reaches the other tokens of its chunk, its sequence's later tokens
- * included, but no other row or head.  bf16 head widths of 64 and 128 run on the
- * tensor cores with the state and every sum in fp32; other widths (multiples of 8
- * up to 256) and fp32 run on the CUDA cores. */
+ * is not finite reaches what depends on it by the definition (where gamma_h is 0, in
+ * fp32, no past does) and nothing else: not the tokens before it, other documents,
+ * rows or heads.  What depends on it is not finite, as an infinity or NaN.
+ * bf16 head widths of 64 and 128 run on the tensor cores with the state and every
+ * sum in fp32 (what a chunk adds to the state is formed from operands of 16 bits'
+ * precision, 2^-17 of each term; a part of a row that holds a value that is not
+ * finite is done again token by token, some ten times slower); other widths
+ * (multiples of 8 up to 256) and fp32 run on the CUDA cores. */
 typedef struct {
   int32_t B, T;             /* sequences, tokens of each                       */
   int32_t H, Hkv;           /* heads of q and o; heads of k and v (divides H)  */
