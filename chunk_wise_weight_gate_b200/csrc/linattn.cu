@@ -397,8 +397,8 @@ __global__ void __launch_bounds__(kThreads) k_step(float* S, const T* q, const T
   const int grp = threadIdx.x / LANES, c = blockIdx.y * COLS + 4 * (threadIdx.x % LANES);
   const float g = log_decay[h];
   if (threadIdx.x == 0 && !(g <= 0.0f)) set_status(status, IPTTT_ERR_ARG);
-  const bool fresh = starts && starts[b] != 0;
   const float gamma = decay_pow(g, 1);
+  const bool fresh = (starts && starts[b] != 0) || gamma == 0.0f;  // no past, whatever the state holds
   const T* qp = q + b * ldq + (long long)h * Dk;
   const T* kp = k + b * ldk + (long long)(h / G) * Dk;
   for (int i = threadIdx.x; i < Dk; i += kThreads) {

@@ -158,3 +158,23 @@ def test_linear_attention_large_finite_values():
     assert bool(O.isfinite().all())
     assert ref.relative(O[:, quiet], want[:, quiet]) <= 6e-3 and ref.relative(S, want_S) <= 1e-5
     assert status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("decay", [-math.inf, -200.0])
+def test_linear_attention_step_without_a_past(dtype, decay):
+    # gamma = 0: the state before is not read into the result, whatever it holds; as in the prompt
+    cfg, q, k, v, ld, S0, _ = attn_case(3, 1, 2, 2, 64, 64, dtype, (), True, [decay, -0.5])
+    S0[1, 0, 3], S0[2, 0] = math.inf, math.nan
+    S = S0.clone()
+    o = pkg.linear_attention_step(cfg, S, q[:, 0], k[:, 0], v[:, 0], ld)
+    want = torch.einsum("bk,bv->bkv", k[:, 0, 0].double(), v[:, 0, 0].double())
+    assert ref.relative(S[:, 0], want.cpu()) <= 1e-6
+    O, S2 = pkg.linear_attention(cfg, q, k, v, ld, S0=S0, S_final=True)
+    # products of bf16 are exact in fp32; in bf16 the prompt's state goes through two halves (2^-17)
+    assert ref.relative(S2, S.double().cpu()) <= 1e-5
+    # o = scale (q . k) v: fp32 sums of 64 terms either way, and the prompt's P rounded to bf16
+    terms = torch.einsum("bhk,bhk->bh", q[:, 0].abs().double(), k[:, 0].abs().double())[..., None] * v[:, 0].abs().double()
+    tol = (2.0 ** -7 if dtype == "bf16" else 2.0 ** -16) * cfg.scale * terms
+    assert bool(((o.double() - O[:, 0].double()).abs() <= tol)[:, 0].all())
+    assert status() == 0
