@@ -210,6 +210,7 @@ __device__ __forceinline__ void row_epilogue(const Args& a, uint32_t tacc, int m
 #pragma unroll 1
     for (int q = 0; q < 4; ++q) {
       uint32_t r[32];
+      __syncwarp();  // the warp loads as one; lanes without a row have skipped the last part
       tmem_ld32(tacc + 32 * q, r);
       tmem_ld_wait();
       const int left = s.cols - n - 32 * q;  // columns that exist
@@ -243,6 +244,7 @@ __device__ __forceinline__ void row_epilogue(const Args& a, uint32_t tacc, int m
 #pragma unroll 1
     for (int q = 0; q < 4; ++q) {
       uint32_t r[32];
+      __syncwarp();  // the warp loads as one; lanes without a row have skipped the last part
       tmem_ld32(tacc + 32 * q, r);
       tmem_ld_wait();
       if (!on || n + 32 * q >= a.N) continue;
@@ -426,6 +428,7 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_kernel(const __grid_constant_
 #pragma unroll 1
       for (int q = 0; q < (EPI == 0 ? 4 : 0); ++q) {
         uint32_t r[32];
+        __syncwarp();  // the warp loads as one; lanes without a row have skipped the last part
         tmem_ld32(tacc + 32 * q, r);
         tmem_ld_wait();
         const int n = t.n0 + 128 * half + 32 * q;
