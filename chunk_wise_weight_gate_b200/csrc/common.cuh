@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <initializer_list>
+
 #include "ipttt.h"
 
 namespace ipttt {
@@ -50,6 +52,18 @@ template <> __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float
 // for the all-fp32 path.
 __device__ __forceinline__ float silu_fast(float x) { return x / (1.0f + __expf(-x)); }
 __device__ __forceinline__ float silu_precise(float x) { return x / (1.0f + expf(-x)); }
+
+// Whether an output is an input's pointer, or another output's (null: not there).
+inline bool shared_pointer(std::initializer_list<const void*> outs, std::initializer_list<const void*> ins) {
+  for (auto o = outs.begin(); o != outs.end(); ++o) {
+    if (!*o) continue;
+    for (const void* i : ins)
+      if (*o == i) return true;
+    for (auto other = outs.begin(); other != o; ++other)
+      if (*o == *other) return true;
+  }
+  return false;
+}
 
 // Host helpers (implemented in api.cu).
 ipttt_status cuda_status(cudaError_t e);

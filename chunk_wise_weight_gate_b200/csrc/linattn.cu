@@ -557,11 +557,6 @@ bool aligned16(std::initializer_list<const void*> ps) {
   return any % 16 == 0;
 }
 
-// Whether an output is one of the inputs: other blocks, or later passes, still read them.
-bool any_of(const void* out, std::initializer_list<const void*> in) {
-  return std::find(in.begin(), in.end(), out) != in.end();
-}
-
 // bf16 of their widths always, short rows too: 20 heads of 128, 8192 tokens 73 us (958 on the CUDA
 // cores), 64 tokens 12.6 (24.7), 16 tokens 12.5 (12.0).
 bool on_tensor_cores(const ipttt_linattn_params& p) { return p.dtype == IPTTT_BF16 && tc_takes(p.Dk, p.Dv); }
@@ -661,7 +656,9 @@ ipttt_status ipttt_linattn_forward(const ipttt_linattn_params* pp, const void* q
   const ipttt_status rc = check(pp);
   if (rc != IPTTT_OK) return rc;
   if (!q || !k || !v || !log_decay || !O || n_doc_starts < 0 || (n_doc_starts > 0 && !doc_starts)) return IPTTT_ERR_ARG;
-  if (any_of(O, {q, k, v})) return IPTTT_ERR_ARG;
+  if (shared_pointer({O, workspace}, {q, k, v, log_decay, doc_starts, S0_opt, S_final_opt}) ||
+      shared_pointer({S_final_opt}, {q, k, v, log_decay, doc_starts}))
+    return IPTTT_ERR_ARG;
   if (!aligned16({q, k, v, O, S0_opt, S_final_opt})) return IPTTT_ERR_ALIGN;
   const Work w = work_of(*pp, false);
   if (!workspace || workspace_bytes < w.total) return IPTTT_ERR_WORKSPACE;
@@ -721,9 +718,9 @@ ipttt_status ipttt_linattn_backward(const ipttt_linattn_params* pp, const void* 
   if (rc != IPTTT_OK) return rc;
   if (!q || !k || !v || !log_decay || !gO || !gq || !gk || !gv || n_doc_starts < 0 || (n_doc_starts > 0 && !doc_starts))
     return IPTTT_ERR_ARG;
-  for (const void* g : {gq, gk, gv})
-    if (any_of(g, {q, k, v, gO})) return IPTTT_ERR_ARG;
-  if (gS0_opt && gS0_opt == gS_final_opt) return IPTTT_ERR_ARG;  // gS0 is written before gS_final's last reader
+  // (gS0 too: it is written before gS_final's last reader)
+  if (shared_pointer({gq, gk, gv, gS0_opt, workspace}, {q, k, v, log_decay, doc_starts, S0_opt, gO, gS_final_opt}))
+    return IPTTT_ERR_ARG;
   if (!aligned16({q, k, v, gO, gq, gk, gv, S0_opt, gS_final_opt, gS0_opt})) return IPTTT_ERR_ALIGN;
   const Work w = work_of(*pp, true);
   if (!workspace || workspace_bytes < w.total) return IPTTT_ERR_WORKSPACE;
@@ -828,7 +825,7 @@ ipttt_status ipttt_linattn_step(const ipttt_linattn_params* pp, float* S, const 
   const ipttt_status rc = check(pp);
   if (rc != IPTTT_OK) return rc;
   if (pp->T != 1 || !S || !q || !k || !v || !log_decay || !o) return IPTTT_ERR_ARG;
-  if (any_of(o, {q, k, v})) return IPTTT_ERR_ARG;
+  if (shared_pointer({S, o}, {q, k, v, log_decay, starts_opt})) return IPTTT_ERR_ARG;
   if (!aligned16({S, q, k, v, o})) return IPTTT_ERR_ALIGN;
   const ipttt_linattn_params p = filled(*pp);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);

@@ -509,7 +509,8 @@ ipttt_status ipttt_qk_norm_rope(const ipttt_qk_params* p, const void* q, const v
     return IPTTT_ERR_ALIGN;
   QkArgs a = args_of(*p);
   // in place means the same elements: another stride would write vectors not yet read
-  if ((q == q_out && a.ldq != a.ldqo) || (k == k_out && a.ldk != a.ldko) || q == k_out || k == q_out)
+  if ((q == q_out && a.ldq != a.ldqo) || (k == k_out && a.ldk != a.ldko) || q == k_out || k == q_out ||
+      shared_pointer({q_out, k_out}, {wq, wk, inv_freq, positions}))
     return IPTTT_ERR_ARG;
   a.q = q;
   a.k = k;
@@ -549,7 +550,9 @@ ipttt_status ipttt_qk_norm_rope_backward(const ipttt_qk_params* p, const void* q
   if (reinterpret_cast<uintptr_t>(workspace) % 256) return IPTTT_ERR_ALIGN;
   QkArgs a = args_of(*p);
   if ((gq == gqo && a.ldgq != a.ldqo) || (gk == gko && a.ldgk != a.ldko) || (gq == q && a.ldgq != a.ldq) ||
-      (gk == k && a.ldgk != a.ldk) || gq == k || gq == gko || gk == q || gk == gqo)
+      (gk == k && a.ldgk != a.ldk) || gq == k || gq == gko || gk == q || gk == gqo ||
+      shared_pointer({gq, gk, gwq, gwk, workspace}, {wq, wk, inv_freq, positions}) ||
+      shared_pointer({gwq, gwk, workspace}, {q, k, gqo, gko}))
     return IPTTT_ERR_ARG;
   a.q = q;
   a.k = k;

@@ -562,6 +562,7 @@ ipttt_status ipttt_xent_forward(const ipttt_xent_params* p, const void* H, const
   const ipttt_status rc = check(p);
   if (rc != IPTTT_OK) return rc;
   if (!H || !W || !targets || !loss || !lse) return IPTTT_ERR_ARG;
+  if (shared_pointer({loss, lse, workspace}, {H, W, targets})) return IPTTT_ERR_ARG;
   if (!aligned({H, W}, 16) || !aligned({targets}, 8) || !aligned({loss, lse}, 4)) return IPTTT_ERR_ALIGN;
   const Work w = work_of(*p, false);
   if (!workspace || workspace_bytes < w.total) return IPTTT_ERR_WORKSPACE;
@@ -580,7 +581,7 @@ ipttt_status ipttt_xent_backward(const ipttt_xent_params* p, const void* H, cons
   const ipttt_status rc = check(p);
   if (rc != IPTTT_OK) return rc;
   if (!H || !W || !targets || !lse || !gloss || !gH || !gW) return IPTTT_ERR_ARG;
-  if (gW == W || gW == H || gH == W || gH == H) return IPTTT_ERR_ARG;
+  if (shared_pointer({gH, gW, workspace}, {H, W, targets, lse, gloss})) return IPTTT_ERR_ARG;
   if (!aligned({H, W, gH, gW}, 16) || !aligned({targets}, 8) || !aligned({lse, gloss}, 4)) return IPTTT_ERR_ALIGN;
   const Work w = work_of(*p, true);
   if (!workspace || workspace_bytes < w.total) return IPTTT_ERR_WORKSPACE;

@@ -381,7 +381,8 @@ IPTTT_API ipttt_status ipttt_backward(const ipttt_params* p, const void* H, cons
  * current device, argument errors returned before any launch, results
  * deterministic run to run.  A workspace holds nothing between calls.  No output
  * overlaps an input or another output, except where a call says that it may be one;
- * an output that is an input's pointer all the same is refused (IPTTT_ERR_ARG).
+ * an output, or a workspace, that is an input's pointer or another output's all the
+ * same is refused (IPTTT_ERR_ARG).
  * Token tensors [B, T, heads, width] are read through a token stride: the elements
  * between a token and the next (b, t) -> (b*T + t) * ld, heads packed within a
  * token; 0 means packed tokens (heads * width).  Strides are multiples of 8
