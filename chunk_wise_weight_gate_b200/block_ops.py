@@ -244,9 +244,9 @@ def linear_attention(cfg: LinearAttentionConfig, q, k, v, log_decay, doc_starts=
 
 
 def linear_attention_backward(cfg: LinearAttentionConfig, q, k, v, log_decay, doc_starts, gO, *, S0=None,
-                              gS_final=None, workspace=None, stream=None):
-    """Gradients of <gO, O> + <gS_final, S_T>: a dict with q, k and v (the call's dtype) and,
-    when S0 is given, S0 (fp32)."""
+                              gS_final=None, gq=None, gk=None, gv=None, workspace=None, stream=None):
+    """Gradients of <gO, O> + <gS_final, S_T>: a dict with q, k and v (the call's dtype, packed unless
+    gq, gk, gv are given: views of one projection's gradient, say) and, when S0 is given, S0 (fp32)."""
     dt, dev, sh = _dtype(cfg.dtype)[1], q.device, cfg.shapes()
     f32 = torch.float32
     pq, ldq = _tokens(q, "q", sh["q"], dt, dev)
@@ -257,14 +257,15 @@ def linear_attention_backward(cfg: LinearAttentionConfig, q, k, v, log_decay, do
     p0 = _flat(S0, "S0", sh["S"], f32, dev)
     ps = _flat(gS_final, "gS_final", sh["S"], f32, dev)
     with _On(q, stream) as st:
-        out = {n: torch.empty_like(t, memory_format=_packed) for n, t in (("q", q), ("k", k), ("v", v))}
+        out = {n: torch.empty_like(t, memory_format=_packed) if g is None else g
+               for n, t, g in (("q", q, gq), ("k", k, gk), ("v", v, gv))}
+        grads = [_tokens(out[n], "g" + n, sh[n], dt, dev) for n in "qkv"]
         if S0 is not None:
             out["S0"] = torch.empty(sh["S"], dtype=f32, device=dev)
-        p = cfg.params(ldq, ldk, ldv, ldo)
+        p = cfg.params(ldq, ldk, ldv, ldo, *(ld for _, ld in grads))
         ws = _workspace(workspace, _size(lib().ipttt_linattn_backward_workspace_size, p, cfg), dev)
         dp, nd, keep = _starts(doc_starts, dev)
-        _check(lib().ipttt_linattn_backward(_byref(p), pq, pk, pv, pd, dp, nd, p0, pg, ps, out["q"].data_ptr(),
-                                            out["k"].data_ptr(), out["v"].data_ptr(),
+        _check(lib().ipttt_linattn_backward(_byref(p), pq, pk, pv, pd, dp, nd, p0, pg, ps, *(g for g, _ in grads),
                                             out["S0"].data_ptr() if S0 is not None else None, ws.data_ptr(),
                                             ws.numel(), st), "ipttt_linattn_backward")
     return out
