@@ -92,6 +92,10 @@ def _starts(doc_starts, device):
     if doc_starts is None:
         return None, 0, None
     ds = doc_starts if isinstance(doc_starts, torch.Tensor) else torch.as_tensor(doc_starts, dtype=torch.int32)
+    if ds.dtype == torch.int64:  # an offset beyond 32 bits stays out of range: the call reports it
+        ds = ds.clamp(-1, 2 ** 31 - 1)
+    elif ds.dtype != torch.int32:
+        raise ValueError(f"doc_starts: {ds.dtype}, expected int32 or int64 offsets")
     ds = ds.to(device=device, dtype=torch.int32).contiguous()
     return (ds.data_ptr() if ds.numel() else None), ds.numel(), ds
 
