@@ -27,6 +27,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "tc.cuh"
 #include "tc_kernels.h"
@@ -509,11 +510,10 @@ cudaLaunchConfig_t pair_config(int grid, cudaStream_t st, cudaLaunchAttribute* a
 // the pair kernel has the same threads and shared memory, and one block a SM, so the
 // plain one's number holds for all.
 int pair_workers(cudaStream_t st) {
-  static int cached[64];
-  static bool have[64];
+  static std::atomic<int> known[64];  // the number + 1; 0: not asked yet (several host threads may ask at once)
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
-  if (have[dev]) return cached[dev];
+  if (const int k = known[dev].load()) return k - 1;
   int n = 0;
   constexpr int smem = Cfg<true>::SMEM;
   if (cudaFuncSetAttribute(gemm_kernel<true, 0>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) == cudaSuccess &&
@@ -524,8 +524,7 @@ int pair_workers(cudaStream_t st) {
     if (cudaOccupancyMaxActiveClusters(&n, gemm_kernel<true, 0>, &cfg) != cudaSuccess) n = 0;
   }
   cudaGetLastError();
-  cached[dev] = n;
-  have[dev] = true;
+  known[dev].store(n + 1);
   return n;
 }
 
