@@ -187,6 +187,7 @@ __device__ __forceinline__ LanePlace place_of(const QkArgs& a, int l) {
 // would be a third of all instructions.
 template <typename T>
 __device__ __forceinline__ void fill_angles(const QkArgs& a, long long t0, int n, float* cs, float* sn) {
+  if (a.R == 0) return;  // there may be no positions
   for (int t = threadIdx.x >> 6; t < n; t += kThreads / 64) {
     const double pos = (double)a.pos[t0 + t];
     for (int f = threadIdx.x & 63; f < a.R / 2; f += 64) {
