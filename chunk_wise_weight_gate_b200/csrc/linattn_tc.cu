@@ -377,7 +377,7 @@ __global__ void __launch_bounds__(Cfg<DA, DC, KIND == STATES>::THREADS, 1) k_pas
   if (warp == 0 && lane == 0) {
     if (!STATE) {
       prefetch_tmap(&ta.ma);
-      prefetch_tmap(&ta.mo);
+      if (!p.out_f32) prefetch_tmap(&ta.mo);
     }
     prefetch_tmap(&ta.mb);
     prefetch_tmap(&ta.mc);
@@ -973,7 +973,7 @@ int tc_segments(int B, int T, int H, int* seg_chunks, int* whole) {
 }
 
 cudaError_t run_tc(const Pass& p, cudaStream_t st) {
-  TcArgs a;
+  TcArgs a = {};  // (a map that the pass does not use stays empty)
   a.p = p;
   a.items = (p.B * p.H - p.whole) * (p.out ? p.segs : p.segs - 1) + (p.out ? p.whole : 0);
   if (a.items <= 0) return cudaSuccess;
