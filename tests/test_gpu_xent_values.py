@@ -52,3 +52,17 @@ def test_cross_entropy_of_a_token_that_is_not_finite(N, V, dtype):
     keep[N // 2] = True
     assert torch.equal(g["H"][keep], want[keep]) and bool(g["H"][1].isnan().all()) and bool(g["W"].isnan().all())
     assert status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N,V,d,piece", [(150, 1000, 64, 256), (5, 300, 320, 0), (700, 2000, 96, 512)])
+def test_cross_entropy_rows_left_out_of_a_head_that_is_not_finite(N, V, d, piece, dtype):
+    cfg, H, W, t = xent_case(N, V, d, dtype, piece=piece)
+    for bad in (math.nan, math.inf):
+        w = W.clone()
+        w[V // 2, 1] = bad
+        loss, lse = pkg.cross_entropy(cfg, H, w, t)
+        g = pkg.cross_entropy_backward(cfg, H, w, t, lse, torch.full((N,), 1.0 / N, device="cuda"))
+        out = t == -100
+        assert bool(out.any()) and not loss[out].any() and not g["H"][out].any()
+    assert status() == 0
