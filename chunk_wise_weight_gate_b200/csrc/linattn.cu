@@ -718,6 +718,7 @@ ipttt_status ipttt_linattn_backward(const ipttt_linattn_params* pp, const void* 
   if (rc != IPTTT_OK) return rc;
   if (!q || !k || !v || !log_decay || !gO || !gq || !gk || !gv || n_doc_starts < 0 || (n_doc_starts > 0 && !doc_starts))
     return IPTTT_ERR_ARG;
+  if (gS_final_opt && !isfinite(1.0f / pp->scale)) return IPTTT_ERR_ARG;  // R is kept without the scale: gS_final / scale enters it
   // (gS0 too: it is written before gS_final's last reader)
   if (shared_pointer({gq, gk, gv, gS0_opt, workspace}, {q, k, v, log_decay, doc_starts, S0_opt, gO, gS_final_opt}))
     return IPTTT_ERR_ARG;

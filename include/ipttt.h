@@ -448,7 +448,7 @@ typedef struct {
   int32_t H, Hkv;           /* heads of q and o; heads of k and v (divides H)  */
   int32_t Dk, Dv;           /* widths of q and k; of v and o                   */
   int32_t dtype;            /* ipttt_dtype of q, k, v, o and their gradients   */
-  float scale;              /* finite, not 0                                   */
+  float scale;              /* finite, not 0; with gS_final, 1 / scale finite  */
   int64_t ldq, ldk, ldv;    /* token strides of q, k, v                        */
   int64_t ldo;              /* of o (backward: of gO)                          */
   int64_t ldgq, ldgk, ldgv; /* backward: of gq, gk, gv                         */
