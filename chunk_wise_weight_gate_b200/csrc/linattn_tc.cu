@@ -737,6 +737,7 @@ __global__ void __launch_bounds__(Cfg<DA, DC, KIND == STATES>::THREADS, 1) k_pas
         const uint32_t addr = d_addr + two_col * (c & 1);
         if (keep < 0.0f) {  // whatever f holds
           look();
+          __syncwarp();  // what follows is of the whole warp
           keep = 0.0f;
 #pragma unroll
           for (int e = 0; e < NC; ++e) f[e] = 0.0f;
@@ -871,10 +872,13 @@ __global__ void __launch_bounds__(Cfg<DA, DC, KIND == STATES>::THREADS, 1) k_pas
       LA_WAIT_WARP(all_done, 0);  // the outputs have been written
       uint32_t met = 0;
 #pragma unroll 1
-      for (uint32_t k = 0; ok && k < ic; ++k) {
-        if (k % 32 == 0 && words[W_ODD + k / 32] == 0) k += 31;
-        else if (is_odd(k)) ok = walk<DA, DC, STATE>(p, item_of(p, blockIdx.x + k * gridDim.x), reinterpret_cast<float*>(smem),
-                                                     reinterpret_cast<float*>(lo_buf), tid, meet, met, words);
+      for (uint32_t w = 0; ok && 32 * w < ic; ++w) {
+#pragma unroll 1
+        for (uint32_t bits = words[W_ODD + w]; ok && bits != 0; bits &= bits - 1) {
+          const int k = 32 * (int)w + __ffs(bits) - 1;
+          ok = walk<DA, DC, STATE>(p, item_of(p, blockIdx.x + k * gridDim.x), reinterpret_cast<float*>(smem),
+                                   reinterpret_cast<float*>(lo_buf), tid, meet, met, words);
+        }
       }
     } while (false);
   }

@@ -178,3 +178,35 @@ def test_linear_attention_step_without_a_past(dtype, decay):
     tol = (2.0 ** -7 if dtype == "bf16" else 2.0 ** -16) * cfg.scale * terms
     assert bool(((o.double() - O[:, 0].double()).abs() <= tol)[:, 0].all())
     assert status() == 0
+
+
+def test_linear_attention_bad_values_in_some_of_many_short_rows():
+    # some forty items a block, of which a few hold a bad value; state in place, captured and replayed
+    B, T, H, D = 300, 3, 20, 64
+    cfg, q, k, v, _, S0, _ = attn_case(B, T, H, H, D, D, "bf16", (), True)
+    ld = torch.log1p(-torch.exp2(-1.0 - 5.0 * torch.arange(H) / H)).cuda()
+    docs = torch.arange(2, B * T, 7, dtype=torch.int32).cuda()
+    gen = torch.Generator().manual_seed(8)
+    for x in (k, v):
+        rows, toks, heads = (torch.randint(0, n, (60,), generator=gen).cuda() for n in (B, T, H))
+        x[rows, toks, heads, 5] = math.nan
+    S0[7, 3, 2, 1] = math.inf
+    f32 = pkg.LinearAttentionConfig(B, T, H, H, D, D, cfg.scale, "f32")
+    want, want_S = pkg.linear_attention(f32, q.float(), k.float(), v.float(), ld, docs, S0=S0, S_final=True)
+    assert not bool(want.isfinite().all()) and bool(want.isfinite().any())
+    O, S = pkg.linear_attention(cfg, q, k, v, ld, docs, S0=S0, S_final=True)
+    same_but_for_bad(O, want, 6e-3)
+    same_but_for_bad(S, want_S, 1e-5)
+    S2 = S0.clone()
+    O2, _ = pkg.linear_attention(cfg, q, k, v, ld, docs, S0=S2, S_final=S2)
+    assert torch.equal(O.nan_to_num(7.0), O2.nan_to_num(7.0)) and torch.equal(S.nan_to_num(7.0), S2.nan_to_num(7.0))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        O3, _ = pkg.linear_attention(cfg, q, k, v, ld, docs, S0=S2, S_final=S2)
+    for _ in range(2):
+        S2.copy_(S0)
+        graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(O.nan_to_num(7.0), O3.nan_to_num(7.0)) and torch.equal(S.nan_to_num(7.0), S2.nan_to_num(7.0))
+    assert status() == 0
+    del graph
