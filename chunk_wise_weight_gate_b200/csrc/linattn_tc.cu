@@ -30,9 +30,9 @@
 // two: 68 us; tiles brought into L2 ahead of their loads: 72 us.
 //
 // Masked places are products with 0, which is NaN for a value that is not finite.  An item that held one
-// is done again at the end, token by token (`walk`): the chunks' loop pays for telling by the state
-// alone, 0.5% (8 x 2047 tokens of 24 heads 114.2 -> 115.2 us); looking at every output too cost 2%, a
-// walk within the item with its state in registers 3%.
+// is done again at the end, token by token (`walk`).  Telling by the state alone costs the chunks' loop
+// 1.3% (8 x 2047 tokens of 24 heads 112.1 -> 113.7 us, one box in turn); looking at the outputs too
+// cost 3%, a walk within the item with its state in registers 5%.
 //
 // Rows are cut into segments when rows and heads alone leave SMs idle: a first pass (STATES) forms
 // each segment's own state from b and c alone (1.5 to 1.7 us a chunk: 64 KB, HBM), and the full
@@ -225,7 +225,8 @@ __device__ __forceinline__ Last last_of(const Pass& p, const Item& it, float g) 
 // other tokens and documents must not take it.  A thread has a column of the state, tid % DC, and
 // ROWS of its rows from tid / DC * ROWS on; the state lies in F (shared memory, as registers would
 // cost the chunks' loop), kWalk tokens at a time in `room`, as fp32.  A barrier joins the threads,
-// `met` times so far; false: a wait gave up.
+// `met` times so far; false: a wait gave up.  2.0 us a token at width 128 (32768 tokens of 20 heads, a
+// bad value in each item: 9.5 ms): the shared memory's and the batches' latency.
 template <int DA, int DC, bool STATE>
 __device__ __forceinline__ bool walk(const Pass& p, const Item& it, float* F, float* room, int tid, uint64_t* bar,
                                      uint32_t& met, volatile uint32_t* words) {
@@ -270,30 +271,52 @@ __device__ __forceinline__ bool walk(const Pass& p, const Item& it, float* F, fl
   for (int n0 = 0; n0 < hi - lo; n0 += kWalk) {
     const int n = min(kWalk, hi - lo - n0);
     auto token = [&](int k) { return p.rev ? hi - 1 - n0 - k : lo + n0 + k; };
-#pragma unroll 1
-    for (int i = tid; i < n * DA; i += 256) {
-      const int t = token(i / DA);
-      if constexpr (!STATE) sa[i] = to_f(A[t * p.lda + i % DA]);
-      sb[i] = to_f(B[t * p.ldb + i % DA]);
+    const int word = token(0) / 32;  // the starts of the tokens lie in two words at most
+    const uint32_t bits0 = starts ? starts[word] : 0u, bits1 = starts ? starts[token(n - 1) / 32] : 0u;
+    // all of a thread's loads before its stores
+    constexpr int PA = kWalk * DA / 256, PC = kWalk * DC / 256;
+    float va[PA], vb[PA], vc[PC];
+#pragma unroll
+    for (int u = 0; u < PA; ++u) {
+      const int i = tid + 256 * u, t = token(i / DA);
+      va[u] = !STATE && i < n * DA ? to_f(A[t * p.lda + i % DA]) : 0.0f;
+      vb[u] = i < n * DA ? to_f(B[t * p.ldb + i % DA]) : 0.0f;
     }
-#pragma unroll 1
-    for (int i = tid; i < n * DC; i += 256) sc[i] = to_f(C[token(i / DC) * p.ldc + i % DC]);
+#pragma unroll
+    for (int u = 0; u < PC; ++u) {
+      const int i = tid + 256 * u;
+      vc[u] = i < n * DC ? to_f(C[token(i / DC) * p.ldc + i % DC]) : 0.0f;
+    }
+#pragma unroll
+    for (int u = 0; u < PA; ++u) {
+      if constexpr (!STATE) sa[tid + 256 * u] = va[u];
+      sb[tid + 256 * u] = vb[u];
+    }
+#pragma unroll
+    for (int u = 0; u < PC; ++u) sc[tid + 256 * u] = vc[u];
     if (!meet()) return false;
 #pragma unroll 1
     for (int k = 0; k < n; ++k) {
       const int t = token(k);
-      const bool start = starts && (starts[t / 32] >> (t % 32) & 1u);
+      const bool start = ((t / 32 == word ? bits0 : bits1) >> (t % 32) & 1u) != 0;
       // no decay before the last token, whose state's gradient comes in as it is
       const float keep = p.rev && t == p.T - 1 ? 1.0f : gamma;
       const bool drop = keep == 0.0f || (!p.rev && start);
       const bool ends = p.rev && start;  // the document, on the way back
       const float c = sc[k * DC + col];
       float o = 0.0f;
-#pragma unroll 4
-      for (int e = 0; e < ROWS; ++e) {
-        const float x = fmaf(sb[k * DA + r0 + e], c, drop ? 0.0f : keep * f[e * DC]);
-        if constexpr (!STATE) o = fmaf(sa[k * DA + r0 + e], x, o);
-        f[e * DC] = ends ? 0.0f : x;
+#pragma unroll 1
+      for (int e0 = 0; e0 < ROWS; e0 += 16) {  // all loads of 16 rows before their stores
+        float x[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) x[e] = f[(e0 + e) * DC];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          x[e] = fmaf(sb[k * DA + r0 + e0 + e], c, drop ? 0.0f : keep * x[e]);
+          if constexpr (!STATE) o = fmaf(sa[k * DA + r0 + e0 + e], x[e], o);
+        }
+#pragma unroll
+        for (int e = 0; e < 16; ++e) f[(e0 + e) * DC] = ends ? 0.0f : x[e];
       }
       if constexpr (!STATE) so[(k * GROUPS + tid / DC) * DC + col] = o;
     }
