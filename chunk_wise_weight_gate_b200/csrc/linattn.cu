@@ -693,6 +693,7 @@ ipttt_status ipttt_linattn_forward(const ipttt_linattn_params* pp, const void* q
   a.ldo = p.ldo;
   a.init = S0_opt;
   a.fin = S_final_opt;
+  a.fine = S_final_opt != nullptr;
   a.segs = w.segs;
   a.seg_chunks = w.seg_chunks;
   a.whole = w.whole;
@@ -807,6 +808,7 @@ ipttt_status ipttt_linattn_backward(const ipttt_linattn_params* pp, const void* 
   if (e == cudaSuccess) {
     Pass s = pass_of(xk, xq, xg, p.Dk, p.Dv);  // gv, and R's last value gives gS0
     s.fin = gS0_opt;
+    s.fine = gS0_opt != nullptr;
     s.fin_scale = 1;
     e = shared(s, gv, p.ldgv, p.Dv, false);
   }

@@ -43,6 +43,7 @@ struct Pass {
   int prefixed;
   int segs, seg_chunks, chunk;   // segments of a row, chunks of each (the last may have fewer), tokens of a chunk
   int after_states;              // the launch before is the pass for this one's segment states
+  int fine;                      // the state goes out: formed to fp32's accuracy, see linattn_tc.cu
   int whole;                     // (row, head) pairs b * H + h below this are not cut into segments
   int B, T, H, Da, Dc;
   int rev;

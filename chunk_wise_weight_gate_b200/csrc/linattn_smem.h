@@ -17,11 +17,14 @@ template <int DA, int DC, bool STATE>
 struct Smem {
   static constexpr int SLOT = 256 * (DA > DC ? DA : DC);  // a tile of 128 tokens (an a tile, then the output in its place)
   static constexpr int NA = STATE ? 0 : 2;
-  static constexpr int LO = 256 * DA * (STATE ? 2 : 1);   // lo half of the scaled B (STATES: of two chunks in turn)
+  // The scaled B's lower parts: of a chunk in one (STATES: of two chunks in turn), or, where the state is an
+  // output, in two of half a chunk each (STATES: of two half chunks in turn).
+  static constexpr int LO = 256 * DA * (STATE ? 2 : 1);
+  static constexpr int LO_SLOTS = STATE ? 2 : 1, LO_PART = LO / LO_SLOTS / 2;  // the latter: half chunks, bytes of a part
   static constexpr int FB = STATE ? 0 : DA * DC * 2;      // bf16 state
   static constexpr int TABS = 2 * kTab * 4;
   static constexpr int MOST = 6;                          // tiles of the ring at most
-  static constexpr int bars(int ns) { return 2 * ns + 22; }  // full, empty for each tile, and the others
+  static constexpr int bars(int ns) { return 2 * ns + 24; }  // full, empty for each tile, and the others
   static constexpr int WORDS = 4 + kMostItems / 32;  // TMEM address, abort flag, tiles issued (ring, a), a bit for each item
   static constexpr int tail(int ns) { return (8 * bars(ns) + 4 * WORDS + 15) / 16 * 16; }
   static constexpr int FIXED = NA * SLOT + LO + FB + TABS + tail(MOST);

@@ -340,7 +340,7 @@ __device__ __forceinline__ bool walk(const Pass& p, const Item& it, float* F, fl
   return true;
 }
 
-template <int DA, int DC, int KIND>
+template <int DA, int DC, int KIND, bool FINE>
 __global__ void __launch_bounds__(Cfg<DA, DC, KIND == STATES>::THREADS, 1) k_pass_tc(const __grid_constant__ TcArgs ta) {
   constexpr bool STATE = KIND == STATES;
   using Cf = Cfg<DA, DC, STATE>;
@@ -363,7 +363,8 @@ __global__ void __launch_bounds__(Cfg<DA, DC, KIND == STATES>::THREADS, 1) k_pas
   uint64_t *p_ready = sc_full + 12, *f_ready = sc_full + 13, *o_full = sc_full + 14, *o_free = sc_full + 15;
   uint64_t *tab_ready = sc_full + 16, *f_free = sc_full + 17, *drain = sc_full + 18;
   uint64_t *item_end = sc_full + 19, *all_done = sc_full + 20, *meet = sc_full + 21;
-  static_assert(Mem::bars(NS) == 2 * NS + 22, "the barriers above");
+  uint64_t* lo_free = sc_full + 22;  // [2]
+  static_assert(Mem::bars(NS) == 2 * NS + 24, "the barriers above");
   volatile uint32_t* words = reinterpret_cast<volatile uint32_t*>(smem + Mem::at_words);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -381,6 +382,7 @@ __global__ void __launch_bounds__(Cfg<DA, DC, KIND == STATES>::THREADS, 1) k_pas
       mbar_init(&conv_done[2 * s], 8);
       mbar_init(&conv_done[2 * s + 1], 8);
       mbar_init(&d_full[s], 1);
+      mbar_init(&lo_free[s], 1);
       mbar_init(&a_full[s], 1);
       mbar_init(&a_empty[s], 8);
     }
@@ -512,7 +514,7 @@ __global__ void __launch_bounds__(Cfg<DA, DC, KIND == STATES>::THREADS, 1) k_pas
           mma_commit(o_full);
         }
       } else {
-        const uint64_t b_mn = mn_major(ring, lbo4), lo_mn = mn_major(lo_buf, lbo4);
+        const uint64_t b_mn = mn_major(ring, lbo4), lo_mn = mn_major(lo_buf, lbo4), part_mn = mn_major(lo_buf, lbo4 / 2);
         for (uint32_t c = 0; c < total; ++c) {
           const uint32_t sb = tile(2 * c), sc = tile(2 * c + 1);
           const uint64_t db = b_mn + sb * (SLOT / 16), dc = c_mn + sc * (SLOT / 16), dl = lo_mn + (c & 1) * two_lo;
@@ -520,16 +522,35 @@ __global__ void __launch_bounds__(Cfg<DA, DC, KIND == STATES>::THREADS, 1) k_pas
           LA_WAIT(&full[sc], (2 * c + 1) / NS);
           LA_WAIT(&conv_done[2 * (c & 1)], c >> 1);  // the first 64 tokens (and the last chunk's D has been read)
           tc_fence_after();
+          if constexpr (FINE) {
+            // the lower parts first: the next half's take their place meanwhile
+            auto half = [&](int h) {
+              const int slot = Mem::LO_SLOTS == 2 ? h : 0;
+              const uint64_t l1 = part_mn + slot * (2 * Mem::LO_PART / 16), l2 = l1 + Mem::LO_PART / 16;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) mma_bf16(d, db + k * 128, dc + k * 128, id4, k > 0);
+              for (int k = 0; k < 4; ++k) mma_bf16(d, l1 + k * 128, dc + (4 * h + k) * 128, id4, h + k > 0);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) mma_bf16(d, dl + k * 128, dc + k * 128, id4, 1);
-          LA_WAIT(&conv_done[2 * (c & 1) + 1], c >> 1);
-          tc_fence_after();
+              for (int k = 0; k < 4; ++k) mma_bf16(d, l2 + k * 128, dc + (4 * h + k) * 128, id4, 1);
+              mma_commit(&lo_free[slot]);
 #pragma unroll
-          for (int k = 4; k < 8; ++k) mma_bf16(d, db + k * 128, dc + k * 128, id4, 1);
+              for (int k = 0; k < 4; ++k) mma_bf16(d, db + (4 * h + k) * 128, dc + (4 * h + k) * 128, id4, 1);
+            };
+            half(0);
+            LA_WAIT(&conv_done[2 * (c & 1) + 1], c >> 1);
+            tc_fence_after();
+            half(1);
+          } else {
 #pragma unroll
-          for (int k = 4; k < 8; ++k) mma_bf16(d, dl + k * 128, dc + k * 128, id4, 1);
+            for (int k = 0; k < 4; ++k) mma_bf16(d, db + k * 128, dc + k * 128, id4, k > 0);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mma_bf16(d, dl + k * 128, dc + k * 128, id4, 1);
+            LA_WAIT(&conv_done[2 * (c & 1) + 1], c >> 1);
+            tc_fence_after();
+#pragma unroll
+            for (int k = 4; k < 8; ++k) mma_bf16(d, db + k * 128, dc + k * 128, id4, 1);
+#pragma unroll
+            for (int k = 4; k < 8; ++k) mma_bf16(d, dl + k * 128, dc + k * 128, id4, 1);
+          }
           mma_commit(&d_full[c & 1]);
           mma_commit(&empty[sb]);
           mma_commit(&empty[sc]);
@@ -776,8 +797,8 @@ __global__ void __launch_bounds__(Cfg<DA, DC, KIND == STATES>::THREADS, 1) k_pas
           for (int e = 0; e < STEP; ++e) f[STEP * q + e] = fmaf(keep, f[STEP * q + e], __uint_as_float(r[e]));
         }
       };
-      // each row's weight in a chunk as wh + wl (bf16 each); a thread's 16-byte units lie in four rows
-      __nv_bfloat162 wh[4], wl[4];
+      // each row's weight in a chunk as wh + wl (FINE: + wm) in bf16; a thread's 16-byte units lie in four rows
+      __nv_bfloat162 wh[4], wl[4], wm[FINE ? 4 : 1];
       auto weights = [&](int ch, const Starts& st) {
         const int len = min(CH, p.T - ch * CH);
         // rows that reach the state at the chunk's far end
@@ -786,9 +807,15 @@ __global__ void __launch_bounds__(Cfg<DA, DC, KIND == STATES>::THREADS, 1) k_pas
         for (int m = 0; m < 4; ++m) {
           const int j = (tid >> 3) + 32 * m;
           const float w = j >= from && j < to ? pw[rev ? j : len - 1 - j] : 0.0f;
-          const __nv_bfloat16 x = __float2bfloat16_rn(w);
+          float y = w;
+          if constexpr (FINE) {  // the nearest power of two first
+            const float x = __uint_as_float((__float_as_uint(w) + 0x00400000u) & 0x7f800000u);
+            wm[m] = __float2bfloat162_rn(x);
+            y = w - x;
+          }
+          const __nv_bfloat16 x = __float2bfloat16_rn(y);
           wh[m] = __bfloat162bfloat162(x);
-          wl[m] = __float2bfloat162_rn(w - __bfloat162float(x));
+          wl[m] = __float2bfloat162_rn(y - __bfloat162float(x));
         }
       };
       float keep = 0.0f;
@@ -822,10 +849,13 @@ __global__ void __launch_bounds__(Cfg<DA, DC, KIND == STATES>::THREADS, 1) k_pas
         uint8_t* bt = ring + sb * SLOT + tid * 16;
         uint8_t* lt = lo_buf + (cc & 1) * (two_lo * 16) + tid * 16;
         if constexpr (!STATE) LA_WAIT_WARP(&sc_full[cc & 1], cc >> 1);  // (1) has read B: it may be overwritten
-        // hi = bf16(b wh); b wh - hi is a bf16 number, so lo = bf16(b wl + (b wh - hi)) loses 2^-9 of lo
-        // alone.  64 tokens at a time: the first half's (4) starts while the second is scaled.
+        // hi = bf16(b wh); b wh - hi is a bf16 number, so lo = bf16(b wl + (b wh - hi)) loses 2^-8 of lo
+        // alone.  FINE: b times the power of two, exact, in b's place, and hi and lo of the rest, a third of the
+        // weight at most.  64 tokens at a time: the first half's (4) starts while the second is scaled.
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
+          constexpr int SLOTS = Mem::LO_SLOTS;
+          const int slot = SLOTS == 2 ? half : 0;
           uint4 v[DA / 32];
 #pragma unroll
           for (int m = 0; m < DA / 32; ++m)
@@ -834,7 +864,7 @@ __global__ void __launch_bounds__(Cfg<DA, DC, KIND == STATES>::THREADS, 1) k_pas
           for (int m = 0; m < DA / 32; ++m) {
             const __nv_bfloat162 h = wh[2 * half + (m & 1)], l = wl[2 * half + (m & 1)];
             const uint32_t u[4] = {v[m].x, v[m].y, v[m].z, v[m].w};
-            uint32_t hi4[4], lo4[4];
+            uint32_t hi4[4], lo4[4], top4[FINE ? 4 : 1];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const __nv_bfloat162 x = *reinterpret_cast<const __nv_bfloat162*>(&u[e]);
@@ -842,16 +872,33 @@ __global__ void __launch_bounds__(Cfg<DA, DC, KIND == STATES>::THREADS, 1) k_pas
               const __nv_bfloat162 l2 = __hfma2(x, l, __hfma2(x, h, __hneg2(h2)));
               hi4[e] = *reinterpret_cast<const uint32_t*>(&h2);
               lo4[e] = *reinterpret_cast<const uint32_t*>(&l2);
+              if constexpr (FINE) {
+                const __nv_bfloat162 t2 = __hmul2(x, wm[2 * half + (m & 1)]);
+                top4[e] = *reinterpret_cast<const uint32_t*>(&t2);
+              }
             }
             const int at = (2 * half + (m & 1) + 4 * (m >> 1)) * 4096;
-            *reinterpret_cast<uint4*>(bt + at) = make_uint4(hi4[0], hi4[1], hi4[2], hi4[3]);
-            *reinterpret_cast<uint4*>(lt + at) = make_uint4(lo4[0], lo4[1], lo4[2], lo4[3]);
+            if constexpr (FINE) {
+              if (m == 0 && cc * 2 + half >= SLOTS) {  // the half chunk before in this place has been multiplied
+                const uint32_t use = (cc * 2 + half) / SLOTS - 1;
+                ok = __all_sync(0xffffffffu, wait_for(&lo_free[slot], use & 1u, words)) != 0;
+              }
+              uint8_t* part = lo_buf + slot * (2 * Mem::LO_PART) + tid * 16 + ((m & 1) + 2 * (m >> 1)) * 4096;
+              *reinterpret_cast<uint4*>(bt + at) = make_uint4(top4[0], top4[1], top4[2], top4[3]);
+              *reinterpret_cast<uint4*>(part) = make_uint4(hi4[0], hi4[1], hi4[2], hi4[3]);
+              *reinterpret_cast<uint4*>(part + Mem::LO_PART) = make_uint4(lo4[0], lo4[1], lo4[2], lo4[3]);
+            } else {
+              *reinterpret_cast<uint4*>(bt + at) = make_uint4(hi4[0], hi4[1], hi4[2], hi4[3]);
+              *reinterpret_cast<uint4*>(lt + at) = make_uint4(lo4[0], lo4[1], lo4[2], lo4[3]);
+            }
           }
+          if (FINE && !ok) break;
           fence_proxy_async_smem();
           tc_fence_before();  // the last chunk's D has been read
           __syncwarp();
           if (lane == 0) mbar_arrive(&conv_done[2 * (cc & 1) + half]);
         }
+        if (FINE && !ok) break;
         const float keep_now = any ? kNone : pw[len - lag];
         if (n + 1 < it.last - it.first) weights(ch + step, next);
         if constexpr (STATE) {
@@ -928,7 +975,7 @@ __global__ void __launch_bounds__(Cfg<DA, DC, KIND == STATES>::THREADS, 1) k_pas
   }
 }
 
-template <int DA, int DC, int KIND>
+template <int DA, int DC, int KIND, bool FINE>
 cudaError_t launch(const TcArgs& a, cudaStream_t st) {
   using Cf = Cfg<DA, DC, KIND == STATES>;
   // once a device: the shared memory, and a check of the registers.  The register split takes what
@@ -939,10 +986,10 @@ cudaError_t launch(const TcArgs& a, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!ready[dev].load()) {
-    e = cudaFuncSetAttribute(k_pass_tc<DA, DC, KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cf::SMEM);
+    e = cudaFuncSetAttribute(k_pass_tc<DA, DC, KIND, FINE>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cf::SMEM);
     if (e != cudaSuccess) return e;
     cudaFuncAttributes at;
-    e = cudaFuncGetAttributes(&at, k_pass_tc<DA, DC, KIND>);
+    e = cudaFuncGetAttributes(&at, k_pass_tc<DA, DC, KIND, FINE>);
     if (e != cudaSuccess) return e;
     if (KIND != STATES && at.numRegs < kRegsLaunch) return cudaErrorInvalidConfiguration;
     ready[dev].store(true);
@@ -959,13 +1006,18 @@ cudaError_t launch(const TcArgs& a, cudaStream_t st) {
   cfg.stream = st;
   cfg.attrs = &attr;
   cfg.numAttrs = a.p.after_states ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, k_pass_tc<DA, DC, KIND>, a);
+  return cudaLaunchKernelEx(&cfg, k_pass_tc<DA, DC, KIND, FINE>, a);
+}
+
+template <int DA, int DC, bool FINE>
+cudaError_t launch(const TcArgs& a, cudaStream_t st) {
+  if (!a.p.out) return launch<DA, DC, STATES, FINE>(a, st);
+  return a.p.rev ? launch<DA, DC, REVERSE, FINE>(a, st) : launch<DA, DC, FORWARD, FINE>(a, st);
 }
 
 template <int DA, int DC>
 cudaError_t launch(const TcArgs& a, cudaStream_t st) {
-  if (!a.p.out) return launch<DA, DC, STATES>(a, st);
-  return a.p.rev ? launch<DA, DC, REVERSE>(a, st) : launch<DA, DC, FORWARD>(a, st);
+  return a.p.fine ? launch<DA, DC, true>(a, st) : launch<DA, DC, false>(a, st);
 }
 
 }  // namespace
