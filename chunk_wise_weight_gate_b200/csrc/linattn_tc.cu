@@ -8,9 +8,13 @@
 //   (3) O2 = P C                   P = SC under the decay and the masks, bf16, in TMEM
 //   (4) D  = (w B)^T C             the chunk's own addition to the state
 // out = scale (O2 + w_in O1); F <- keep F + D in fp32 registers.  w B, each row times its
-// decay to the chunk's end, is split in two bf16 halves (hi + lo, 2^-17 relative), so
-// the fp32 state is good to fp32-like accuracy; P and the operand copy of F are
-// rounded to bf16 once, like the inputs and outputs are.
+// decay to the chunk's end, is split in two bf16 halves (hi + lo): the state is off by 4e-6 of
+// its norm, far below what its operand copy loses.  P and that copy are rounded to bf16
+// once, like the inputs and outputs are (outputs off by 2.3e-3 where their own rounding
+// makes 1.7e-3).  Where the state itself goes out (FINE), w B is three parts: B times the power of
+// two nearest to w, exact, and two of the rest, a third of w at most: 7e-7, for a third more of
+// (4)'s products; lower parts of 64 tokens at a time share the place of the one.  8 x 2047 tokens
+// of 24 heads with states: 127.6 us, 112.5 in two parts (one box in turn).
 //
 // Roles: warp 0 issues the TMA loads, a thread of warp 1 the MMAs (1) to (3), a thread of
 // warp 2 those of (4); 8 warps turn SC into P (two a quarter of the rows, 64 columns
@@ -797,25 +801,29 @@ __global__ void __launch_bounds__(Cfg<DA, DC, KIND == STATES>::THREADS, 1) k_pas
           for (int e = 0; e < STEP; ++e) f[STEP * q + e] = fmaf(keep, f[STEP * q + e], __uint_as_float(r[e]));
         }
       };
-      // each row's weight in a chunk as wh + wl (FINE: + wm) in bf16; a thread's 16-byte units lie in four rows
-      __nv_bfloat162 wh[4], wl[4], wm[FINE ? 4 : 1];
+      // each row's weight in a chunk as wh + wl (FINE: + wm) in bf16; a thread's 16-byte units lie in four
+      // rows, two a half chunk
+      __nv_bfloat162 wh[2], wl[2], wm[FINE ? 2 : 1];
+      auto half_of = [](__nv_bfloat162 x, int i) { return i == 0 ? __low2bfloat162(x) : __high2bfloat162(x); };
       auto weights = [&](int ch, const Starts& st) {
         const int len = min(CH, p.T - ch * CH);
         // rows that reach the state at the chunk's far end
         const int from = rev ? 0 : st.last(), to = rev ? min(len, st.first()) : len;
 #pragma unroll
-        for (int m = 0; m < 4; ++m) {
-          const int j = (tid >> 3) + 32 * m;
-          const float w = j >= from && j < to ? pw[rev ? j : len - 1 - j] : 0.0f;
-          float y = w;
-          if constexpr (FINE) {  // the nearest power of two first
-            const float x = __uint_as_float((__float_as_uint(w) + 0x00400000u) & 0x7f800000u);
-            wm[m] = __float2bfloat162_rn(x);
-            y = w - x;
+        for (int m = 0; m < 2; ++m) {
+          float w[2], x[2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int j = (tid >> 3) + 32 * (2 * m + i);
+            w[i] = j >= from && j < to ? pw[rev ? j : len - 1 - j] : 0.0f;
+            if constexpr (FINE) {  // the nearest power of two first
+              x[i] = __uint_as_float((__float_as_uint(w[i]) + 0x00400000u) & 0x7f800000u);
+              w[i] -= x[i];
+            }
           }
-          const __nv_bfloat16 x = __float2bfloat16_rn(y);
-          wh[m] = __bfloat162bfloat162(x);
-          wl[m] = __float2bfloat162_rn(y - __bfloat162float(x));
+          if constexpr (FINE) wm[m] = __floats2bfloat162_rn(x[0], x[1]);
+          wh[m] = __floats2bfloat162_rn(w[0], w[1]);
+          wl[m] = __floats2bfloat162_rn(w[0] - __low2float(wh[m]), w[1] - __high2float(wh[m]));
         }
       };
       float keep = 0.0f;
@@ -860,11 +868,27 @@ __global__ void __launch_bounds__(Cfg<DA, DC, KIND == STATES>::THREADS, 1) k_pas
 #pragma unroll
           for (int m = 0; m < DA / 32; ++m)
             v[m] = *reinterpret_cast<const uint4*>(bt + (2 * half + (m & 1) + 4 * (m >> 1)) * 4096);
+          if constexpr (FINE) {
+            // the exact parts first, while the half chunk before is multiplied out of the others' place
+#pragma unroll
+            for (int m = 0; m < DA / 32; ++m) {
+              const __nv_bfloat162 top = half_of(wm[half], m & 1);
+              const uint32_t u[4] = {v[m].x, v[m].y, v[m].z, v[m].w};
+              uint32_t t[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const __nv_bfloat162 t2 = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&u[e]), top);
+                t[e] = *reinterpret_cast<const uint32_t*>(&t2);
+              }
+              *reinterpret_cast<uint4*>(bt + (2 * half + (m & 1) + 4 * (m >> 1)) * 4096) = make_uint4(t[0], t[1], t[2], t[3]);
+            }
+            if (2 * cc + half >= SLOTS) LA_WAIT_WARP(&lo_free[slot], (2 * cc + half) / SLOTS - 1);
+          }
 #pragma unroll
           for (int m = 0; m < DA / 32; ++m) {
-            const __nv_bfloat162 h = wh[2 * half + (m & 1)], l = wl[2 * half + (m & 1)];
+            const __nv_bfloat162 h = half_of(wh[half], m & 1), l = half_of(wl[half], m & 1);
             const uint32_t u[4] = {v[m].x, v[m].y, v[m].z, v[m].w};
-            uint32_t hi4[4], lo4[4], top4[FINE ? 4 : 1];
+            uint32_t hi4[4], lo4[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const __nv_bfloat162 x = *reinterpret_cast<const __nv_bfloat162*>(&u[e]);
@@ -872,27 +896,13 @@ __global__ void __launch_bounds__(Cfg<DA, DC, KIND == STATES>::THREADS, 1) k_pas
               const __nv_bfloat162 l2 = __hfma2(x, l, __hfma2(x, h, __hneg2(h2)));
               hi4[e] = *reinterpret_cast<const uint32_t*>(&h2);
               lo4[e] = *reinterpret_cast<const uint32_t*>(&l2);
-              if constexpr (FINE) {
-                const __nv_bfloat162 t2 = __hmul2(x, wm[2 * half + (m & 1)]);
-                top4[e] = *reinterpret_cast<const uint32_t*>(&t2);
-              }
             }
-            const int at = (2 * half + (m & 1) + 4 * (m >> 1)) * 4096;
-            if constexpr (FINE) {
-              if (m == 0 && cc * 2 + half >= SLOTS) {  // the half chunk before in this place has been multiplied
-                const uint32_t use = (cc * 2 + half) / SLOTS - 1;
-                ok = __all_sync(0xffffffffu, wait_for(&lo_free[slot], use & 1u, words)) != 0;
-              }
-              uint8_t* part = lo_buf + slot * (2 * Mem::LO_PART) + tid * 16 + ((m & 1) + 2 * (m >> 1)) * 4096;
-              *reinterpret_cast<uint4*>(bt + at) = make_uint4(top4[0], top4[1], top4[2], top4[3]);
-              *reinterpret_cast<uint4*>(part) = make_uint4(hi4[0], hi4[1], hi4[2], hi4[3]);
-              *reinterpret_cast<uint4*>(part + Mem::LO_PART) = make_uint4(lo4[0], lo4[1], lo4[2], lo4[3]);
-            } else {
-              *reinterpret_cast<uint4*>(bt + at) = make_uint4(hi4[0], hi4[1], hi4[2], hi4[3]);
-              *reinterpret_cast<uint4*>(lt + at) = make_uint4(lo4[0], lo4[1], lo4[2], lo4[3]);
-            }
+            const int at = (2 * half + (m & 1) + 4 * (m >> 1)) * 4096, in_part = ((m & 1) + 2 * (m >> 1)) * 4096;
+            uint8_t* hi_at = FINE ? lo_buf + slot * (2 * Mem::LO_PART) + tid * 16 + in_part : bt + at;
+            uint8_t* lo_at = FINE ? hi_at + Mem::LO_PART : lt + at;
+            *reinterpret_cast<uint4*>(hi_at) = make_uint4(hi4[0], hi4[1], hi4[2], hi4[3]);
+            *reinterpret_cast<uint4*>(lo_at) = make_uint4(lo4[0], lo4[1], lo4[2], lo4[3]);
           }
-          if (FINE && !ok) break;
           fence_proxy_async_smem();
           tc_fence_before();  // the last chunk's D has been read
           __syncwarp();

@@ -439,10 +439,12 @@ IPTTT_API ipttt_status ipttt_qk_norm_rope_backward(const ipttt_qk_params* p, con
  * fp32, no past does) and nothing else: not the tokens before it, other documents,
  * rows or heads.  What depends on it is not finite, as an infinity or NaN.
  * bf16 head widths of 64 and 128 run on the tensor cores with the state and every
- * sum in fp32 (what a chunk adds to the state is formed from operands of 16 bits'
- * precision, 2^-17 of each term; a part of a row and head that holds a value that is
- * not finite is done again token by token, 2 us a token); other widths (multiples of
- * 8 up to 256) and fp32 run on the CUDA cores. */
+ * sum in fp32 (states and their gradients that a call gives out are good to 1e-6 of
+ * their norm; the products under the decay and the state as an operand of o are
+ * rounded to bf16 once each; a part of a row and head that holds a value that is not
+ * finite is done again token by token, 2 us a token); other widths (multiples of 8 up
+ * to 256) and fp32 run on the CUDA cores.  A chunk's products of queries and keys
+ * are formed before their decay and must stay within fp32's range. */
 typedef struct {
   int32_t B, T;             /* sequences, tokens of each                       */
   int32_t H, Hkv;           /* heads of q and o; heads of k and v (divides H)  */
