@@ -186,6 +186,19 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+// Zeros on the far side of the diagonal block's row `lane`, 32 bf16 numbers, whatever they are: not times 0
+// alone, as products of tokens far apart in size may overflow.  (PTX shifts by more than 31 leave 0.)
+__device__ __forceinline__ void far_side_off(uint32_t (&w)[16], int lane, bool rev) {
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    const int bits = rev ? max(16 * (2 * e + 2 - lane), 0) : max(16 * (lane + 1 - 2 * e), 0);  // kept, from the near side
+    uint32_t off;
+    if (rev) asm("shr.u32 %0, %1, %2;" : "=r"(off) : "r"(0xffffffffu), "r"(bits));
+    else asm("shl.b32 %0, %1, %2;" : "=r"(off) : "r"(0xffffffffu), "r"(bits));
+    w[e] &= ~off;
+  }
+}
+
 // What the roles tell one another besides barriers; from W_ODD on, a bit for each item of the block.
 enum Word { W_TMEM = 0, W_ABORT = 1, W_TILES = 2, W_A_TILES = 3, W_ODD = 4 };
 
@@ -344,7 +357,7 @@ __device__ __forceinline__ bool walk(const Pass& p, const Item& it, float* F, fl
   return true;
 }
 
-template <int DA, int DC, int KIND, bool FINE>
+template <int DA, int DC, int KIND, bool FINE, bool BRIEF>
 __global__ void __launch_bounds__(Cfg<DA, DC, KIND == STATES>::THREADS, 1) k_pass_tc(const __grid_constant__ TcArgs ta) {
   constexpr bool STATE = KIND == STATES;
   using Cf = Cfg<DA, DC, STATE>;
@@ -510,10 +523,10 @@ __global__ void __launch_bounds__(Cfg<DA, DC, KIND == STATES>::THREADS, 1) k_pas
           LA_WAIT(p_ready, c);
           LA_WAIT(&full[sc], (2 * c + 1) / NS);
           tc_fence_after();
-          // P lies in columns 0-31 and 64-95 of the scores' place
+          // P lies in columns 0-31 and 64-95 of the scores' place (BRIEF: its lower part in the latter)
 #pragma unroll
           for (int k = 0; k < CH / 16; ++k)
-            mma_bf16_ta(tm + col_o2(DC), tm + kSC + 8 * k + (k < 4 ? 0 : 32), dc + k * 128, id3, k > 0);
+            mma_bf16_ta(tm + col_o2(DC), tm + kSC + 8 * k + (k < 4 ? 0 : 32), dc + (BRIEF && k >= 4 ? k - 4 : k) * 128, id3, k > 0);
           mma_commit(&empty[sc]);
           mma_commit(o_full);
         }
@@ -607,47 +620,64 @@ __global__ void __launch_bounds__(Cfg<DA, DC, KIND == STATES>::THREADS, 1) k_pas
           // 32 columns at a time; P takes the place of scores already read.  (Loops stay rolled:
           // unrolled, the roles' code overran the instruction caches, a third of all stalls.)
 #pragma unroll 1
-          for (int q = 0; q < 2; ++q) {
+          for (int q = 0; q < (BRIEF && half == 1 ? 0 : 2); ++q) {
             const int block = 2 * half + q;
             uint32_t w[16];
             if (rev ? block < quarter : block > quarter) {  // on the other side of every row of the warp
 #pragma unroll
               for (int e = 0; e < 16; ++e) w[e] = 0u;
-            } else {
-              uint32_t v[32];
-              tmem_ld32(sc_addr + 32 * q, v);
-              if (block == quarter) {  // the diagonal: gamma^|row - j|, 0 on the far side
-                const float* wt = pw + (rev ? -lane : lane);
-                tmem_ld_wait();
+              tmem_st16(sc_addr + 16 * q, w);
+              if constexpr (BRIEF) tmem_st16(sc_addr + 64 + 16 * q, w);
+              continue;
+            }
+            uint32_t v[32];
+            tmem_ld32(sc_addr + 32 * q, v);
+            if (block == quarter) {  // the diagonal: gamma^|row - j|, 0 on the far side
+              const float* wt = pw + (rev ? -lane : lane);
+              tmem_ld_wait();
 #pragma unroll
-                for (int e = 0; e < 32; ++e)  // not times 0 alone: products of tokens far apart in size may overflow
-                  if (rev ? e < lane : e > lane) v[e] = 0u;
+              for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * wt[rev ? e : -e]);
+            } else {  // a factor of the column times one of the row, neither above 1
+              const float rf = rev ? pw[32 * block - row] : pw[row - 32 * block - 31];
+              const float4* col = reinterpret_cast<const float4*>(rev ? pw : pw - 128 + kPw);
+              tmem_ld_wait();
 #pragma unroll
-                for (int e = 0; e < 16; ++e)
-                  w[e] = pack2(__uint_as_float(v[2 * e]) * wt[rev ? 2 * e : -2 * e],
-                               __uint_as_float(v[2 * e + 1]) * wt[rev ? 2 * e + 1 : -2 * e - 1]);
-              } else {  // a factor of the column times one of the row, neither above 1
-                const float rf = rev ? pw[32 * block - row] : pw[row - 32 * block - 31];
-                const float4* col = reinterpret_cast<const float4*>(rev ? pw : pw - 128 + kPw);
-                tmem_ld_wait();
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                  const float4 c = col[e];
-                  w[2 * e] = pack2(__uint_as_float(v[4 * e]) * c.x * rf, __uint_as_float(v[4 * e + 1]) * c.y * rf);
-                  w[2 * e + 1] = pack2(__uint_as_float(v[4 * e + 2]) * c.z * rf, __uint_as_float(v[4 * e + 3]) * c.w * rf);
-                }
-              }
-              if (any) {
-                // bit j of the mask: column j of the block is in the row's document and on its side
-                const int lo = min(max(from - 32 * block, 0), 32), hi = min(max(to - 32 * block, 0), 32);
-                const uint32_t below_hi = hi == 32 ? 0xffffffffu : (1u << hi) - 1u;
-                const uint32_t mask = lo == 32 ? 0u : below_hi & (0xffffffffu << lo);
-#pragma unroll
-                for (int e = 0; e < 16; ++e)
-                  w[e] &= (mask >> (2 * e) & 1u ? 0x0000ffffu : 0u) | (mask >> (2 * e) & 2u ? 0xffff0000u : 0u);
+              for (int e = 0; e < 8; ++e) {
+                const float4 c = col[e];
+                v[4 * e] = __float_as_uint(__uint_as_float(v[4 * e]) * c.x * rf);
+                v[4 * e + 1] = __float_as_uint(__uint_as_float(v[4 * e + 1]) * c.y * rf);
+                v[4 * e + 2] = __float_as_uint(__uint_as_float(v[4 * e + 2]) * c.z * rf);
+                v[4 * e + 3] = __float_as_uint(__uint_as_float(v[4 * e + 3]) * c.w * rf);
               }
             }
+            auto masked = [&] {
+              // bit j of the mask: column j of the block is in the row's document and on its side
+              const int lo = min(max(from - 32 * block, 0), 32), hi = min(max(to - 32 * block, 0), 32);
+              const uint32_t below_hi = hi == 32 ? 0xffffffffu : (1u << hi) - 1u;
+              const uint32_t mask = lo == 32 ? 0u : below_hi & (0xffffffffu << lo);
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                w[e] &= (mask >> (2 * e) & 1u ? 0x0000ffffu : 0u) | (mask >> (2 * e) & 2u ? 0xffff0000u : 0u);
+            };
+#pragma unroll
+            for (int e = 0; e < 16; ++e) w[e] = pack2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]));
+            if (block == quarter) far_side_off(w, lane, rev);
+            if constexpr (BRIEF) {  // what the rounding left, before either is masked
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                v[2 * e] = __float_as_uint(__uint_as_float(v[2 * e]) - __uint_as_float(w[e] << 16));
+                v[2 * e + 1] = __float_as_uint(__uint_as_float(v[2 * e + 1]) - __uint_as_float(w[e] & 0xffff0000u));
+              }
+            }
+            if (any) masked();
             tmem_st16(sc_addr + 16 * q, w);
+            if constexpr (BRIEF) {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) w[e] = pack2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]));
+              if (block == quarter) far_side_off(w, lane, rev);
+              if (any) masked();
+              tmem_st16(sc_addr + 64 + 16 * q, w);
+            }
           }
           tmem_st_wait();
           tc_fence_before();
@@ -720,7 +750,7 @@ __global__ void __launch_bounds__(Cfg<DA, DC, KIND == STATES>::THREADS, 1) k_pas
     const int row = DA == 128 ? quarter * 32 + lane : (quarter & 1) * 32 + lane;
     const int c0 = (DA == 128 ? half : half * 2 + (quarter >> 1)) * NC;  // its columns: [c0, c0 + NC)
     const uint32_t d_addr = tm + d_col + ((uint32_t)(quarter * 32) << 16) + c0;
-    uint32_t tl = 0, cc = 0, ic = 0;
+    uint32_t tl = 0, cc = 0, ic = 0, in_place = 0;
     float f[NC];
     for (int i = blockIdx.x; ok && i < ta.items; i += gridDim.x, ++ic) {
       const Item it = item_of(p, i);
@@ -930,12 +960,13 @@ __global__ void __launch_bounds__(Cfg<DA, DC, KIND == STATES>::THREADS, 1) k_pas
       if (!ok) break;
       look();
       __syncwarp();
-      if (lane == 0) mbar_arrive(item_end);
       const Last to = last_of<STATE>(p, it, g);
       bool write = to.dst != nullptr;
       if (!STATE && write && p.fin == p.init && it.segs == 1) {
         // an item that is done again starts from the state that this would replace
-        LA_WAIT_WARP(item_end, ic);
+        if (lane == 0) mbar_arrive(item_end);
+        LA_WAIT_WARP(item_end, in_place);
+        ++in_place;
         write = !is_odd(ic);
       }
       if (write) {
@@ -985,7 +1016,7 @@ __global__ void __launch_bounds__(Cfg<DA, DC, KIND == STATES>::THREADS, 1) k_pas
   }
 }
 
-template <int DA, int DC, int KIND, bool FINE>
+template <int DA, int DC, int KIND, bool FINE, bool BRIEF>
 cudaError_t launch(const TcArgs& a, cudaStream_t st) {
   using Cf = Cfg<DA, DC, KIND == STATES>;
   // once a device: the shared memory, and a check of the registers.  The register split takes what
@@ -996,10 +1027,10 @@ cudaError_t launch(const TcArgs& a, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!ready[dev].load()) {
-    e = cudaFuncSetAttribute(k_pass_tc<DA, DC, KIND, FINE>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cf::SMEM);
+    e = cudaFuncSetAttribute(k_pass_tc<DA, DC, KIND, FINE, BRIEF>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cf::SMEM);
     if (e != cudaSuccess) return e;
     cudaFuncAttributes at;
-    e = cudaFuncGetAttributes(&at, k_pass_tc<DA, DC, KIND, FINE>);
+    e = cudaFuncGetAttributes(&at, k_pass_tc<DA, DC, KIND, FINE, BRIEF>);
     if (e != cudaSuccess) return e;
     if (KIND != STATES && at.numRegs < kRegsLaunch) return cudaErrorInvalidConfiguration;
     ready[dev].store(true);
@@ -1016,13 +1047,21 @@ cudaError_t launch(const TcArgs& a, cudaStream_t st) {
   cfg.stream = st;
   cfg.attrs = &attr;
   cfg.numAttrs = a.p.after_states ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, k_pass_tc<DA, DC, KIND, FINE>, a);
+  return cudaLaunchKernelEx(&cfg, k_pass_tc<DA, DC, KIND, FINE, BRIEF>, a);
+}
+
+// Rows of up to 64 tokens leave half of P's place empty: it takes what the rounding of P to bf16 left
+// (BRIEF).  In short rows that rounding is common to a row of o and does not average out: one
+// token's o = scale (q . k) v would be off by up to 2^-8 as a whole, besides its own rounding.
+template <int DA, int DC, bool FINE, bool BRIEF>
+cudaError_t launch(const TcArgs& a, cudaStream_t st) {
+  return a.p.rev ? launch<DA, DC, REVERSE, FINE, BRIEF>(a, st) : launch<DA, DC, FORWARD, FINE, BRIEF>(a, st);
 }
 
 template <int DA, int DC, bool FINE>
 cudaError_t launch(const TcArgs& a, cudaStream_t st) {
-  if (!a.p.out) return launch<DA, DC, STATES, FINE>(a, st);
-  return a.p.rev ? launch<DA, DC, REVERSE, FINE>(a, st) : launch<DA, DC, FORWARD, FINE>(a, st);
+  if (!a.p.out) return launch<DA, DC, STATES, FINE, false>(a, st);
+  return a.p.T <= CH / 2 ? launch<DA, DC, FINE, true>(a, st) : launch<DA, DC, FINE, false>(a, st);
 }
 
 template <int DA, int DC>
