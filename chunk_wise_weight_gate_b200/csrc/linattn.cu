@@ -19,9 +19,9 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kMaxWidth = 256;
 constexpr int kMaxSegs = 148;      // segments of a row
-// The tensor-core pass sums up to so many segments' states itself, which saves a launch: 2 rows of 20
-// heads of 128 x 8192 tokens 118 us (136 by k_prefix), 20 heads of 32768 tokens, 7 segments,
-// 198 (206).  Above it k_prefix does: 10 heads of 32768 tokens 124 us (134 summed by
+// The tensor-core pass sums up to so many segments' states itself, which saves a launch (full clocks):
+// 2 rows of 20 heads of 128 x 8192 tokens 118 us (136 by k_prefix), 20 heads of 32768 tokens, 7
+// segments, 198 (206; under load 227 to 240).  Above it k_prefix does: 10 heads of 32768 tokens 124 us (134 summed by
 // every segment), 2 heads 55 (102), 2 heads of 131072 tokens 109 (169).
 constexpr int kDirectStates = 8;
 constexpr long long kSmemSm = 233472;  // shared memory of an SM
@@ -558,7 +558,8 @@ bool aligned16(std::initializer_list<const void*> ps) {
 }
 
 // bf16 of their widths always, short rows too: 20 heads of 128, 8192 tokens 73 us (958 on the CUDA
-// cores), 64 tokens 12.6 (24.7), 16 tokens 12.5 (12.0).
+// cores), 64 tokens 7.1 (24.2; with states 13.3 and 25.2), one token 6.8 (9.2; 13.3 and 10.4), 1280 rows and
+// heads of one token 52 (111).
 bool on_tensor_cores(const ipttt_linattn_params& p) { return p.dtype == IPTTT_BF16 && tc_takes(p.Dk, p.Dv); }
 
 struct Work {

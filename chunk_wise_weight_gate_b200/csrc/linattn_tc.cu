@@ -14,7 +14,7 @@
 // makes 1.7e-3).  Where the state itself goes out (FINE), w B is three parts: B times the power of
 // two nearest to w, exact, and two of the rest, a third of w at most: 7e-7, for a third more of
 // (4)'s products; lower parts of 64 tokens at a time share the place of the one.  8 x 2047 tokens
-// of 24 heads with states: 127.6 us, 112.5 in two parts (one box in turn).
+// of 24 heads with states: 126.2 us, 112.4 in two parts (one box in turn).
 //
 // Roles: warp 0 issues the TMA loads, a thread of warp 1 the MMAs (1) to (3), a thread of
 // warp 2 those of (4); 8 warps turn SC into P (two a quarter of the rows, 64 columns
@@ -34,9 +34,10 @@
 // two: 68 us; tiles brought into L2 ahead of their loads: 72 us.
 //
 // Masked places are products with 0, which is NaN for a value that is not finite.  An item that held one
-// is done again at the end, token by token (`walk`).  Telling by the state alone costs the chunks' loop
-// 1.3% (8 x 2047 tokens of 24 heads 112.1 -> 113.7 us, one box in turn); looking at the outputs too
-// cost 3%, a walk within the item with its state in registers 5%.
+// is done again at the end, token by token (`walk`).  Telling by the state alone, and the masks, cost
+// 2 x 8192 tokens of 20 heads backwards 0.4% (337.6 -> 339.0 us, one box in turn) and 32768 forwards
+// nothing; looking at the outputs too cost 2% more, a walk within the item with its state in
+// registers 5%.  Rows of one chunk pay more: 1280 of 64 wide 36.5 -> 43.6 us with P's lower part.
 //
 // Rows are cut into segments when rows and heads alone leave SMs idle: a first pass (STATES) forms
 // each segment's own state from b and c alone (1.5 to 1.7 us a chunk: 64 KB, HBM), and the full

@@ -17,10 +17,14 @@
 // (2i, 2i+1), and elements that do not turn).  A block takes a tile of tokens at a time with
 // all their heads; a group of lanes stays with one token, whose sines and cosines
 // (angle reduced to a turn in 64 bits) are computed once for all heads and then stay in
-// registers.  Now 116 us for those 32768 tokens (671 MB, 5.8 TB/s; 89% of the copy
-// bandwidth), 5.4 for 300, 3.5 for 16.  Backwards, 3 x 4099 tokens of 20 + 4 heads of 128, half of
-// each turned: 68 us with the weights' sum (227 MB, 3.3 TB/s); it is at the rate its
-// instructions issue, 330 for 512 elements of x and gy.
+// registers.  Now 116 us at full clocks, 118 to 123 under load, for those 32768 tokens (671 MB, 5.5 to
+// 5.8 TB/s; 83 to 89% of the copy bandwidth), 5.4 for 300, 3.5 for 16.  Backwards, 3 x 4099
+// tokens of 20 + 4 heads of 128, half of each turned: 68 to 72 us with the weights' sum (227 MB,
+// 3.2 TB/s).  What bounds it is latency: two blocks of 8 warps an SM, a barrier on either side
+// of a tile's angles and one round of loads ahead leave half of the issue slots and 60% of DRAM's
+// time unused (stalls of an instruction at 16384 tokens: 2.3 for loads, 1.2 at barriers).
+// In fp32 the forms of 16 elements a lane spill (forwards 700 bytes a thread at 80 registers,
+// backwards 88); the bf16 ones do not.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -413,7 +417,8 @@ QkArgs args_of(const ipttt_qk_params& p) {
   a.inv_d = 1.0f / (float)p.D;
   // a token a tile while every block has one at most, else eight, whose angles and loads share a
   // block's latency: 32 + 8 heads of 128, 300 tokens 5.4 us (6.2 by eights), 1184 tokens 6.7 by
-  // eights (12.9 one by one), 32768 tokens 116 (298)
+  // eights (12.9 one by one), 32768 tokens 116 (298).  Measured at those heads alone: with one head
+  // of q and k three quarters of a tile's groups of lanes have none
   a.shift = a.tokens > kForwardBlocks ? 3 : 0;
   static_assert(kTokens == 8, "shift");
   return a;

@@ -335,7 +335,10 @@ __global__ void __launch_bounds__(kThreads) k_sum_slices(const float* part, T* o
 
 size_t al256(size_t x) { return (x + 255) & ~size_t(255); }
 
-constexpr size_t kPieceBytes = size_t(256) << 20;  // of a piece's p (fp32: of its logits, p in their place)
+// Of a piece's p (fp32: of its logits, p in their place).  128 to 512 MB are within 1% at 8192 tokens of
+// 65536 words; more tokens make a piece fewer words (131072: 1024), whose gW product has fewer tiles than
+// SMs and whose gH is added up more often: not measured there, `piece` may say otherwise.
+constexpr size_t kPieceBytes = size_t(256) << 20;
 
 ipttt_status check(const ipttt_xent_params* p) {
   if (!p) return IPTTT_ERR_ARG;
