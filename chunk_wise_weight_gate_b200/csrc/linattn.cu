@@ -107,6 +107,7 @@ __global__ void __launch_bounds__(kThreads) k_pass(const Pass p) {
   float* pw = sp + L * kSp;         // [L + 1] powers of gamma
   float* win = pw + L + 1;              // [L] the state's weight in each row
   float* wout = win + L;                // [L] each row's weight in the new state
+  float* fade = wout + L;               // [3] the factor of a whole chunk
 
   const int b = blockIdx.y / p.H, h = blockIdx.y % p.H;
   const int seg = blockIdx.z;
@@ -115,6 +116,13 @@ __global__ void __launch_bounds__(kThreads) k_pass(const Pass p) {
   const float g = p.log_decay[h];
   if (threadIdx.x == 0 && !(g <= 0.0f)) set_status(p.status, IPTTT_ERR_ARG);
   if (threadIdx.x <= L) pw[threadIdx.x] = decay_pow(g, threadIdx.x);
+  if (threadIdx.x == L) {
+    const Fade f = fade_of(g, L);
+    fade[0] = f.hi;
+    fade[1] = f.lo;
+    fade[2] = f.inv;
+  }
+  float left = 0.0f;
   const bool no_past = decay_pow(g, 1) == 0.0f;
   const T* A = static_cast<const T*>(p.a) + (long long)b * p.T * p.lda + (long long)(h / p.ga) * Da;
   const T* Bm = static_cast<const T*>(p.b) + (long long)b * p.T * p.ldb + (long long)(h / p.gb) * Da;
@@ -257,7 +265,8 @@ __global__ void __launch_bounds__(kThreads) k_pass(const Pass p) {
       }
       __syncthreads();
     }
-    const float keep = w || (no_past && len > lag) ? kNone : pw[len - lag];
+    float keep = len - lag == L ? fade_next({fade[0], fade[1], fade[2]}, left) : pw[len - lag];
+    if (w || (no_past && len > lag)) keep = kNone;
     // four rows of the state at a time, so that a row of c is read once for them
     for (int r0 = ty; r0 < Da; r0 += 64) {
       float4 f[4];
@@ -307,7 +316,7 @@ __global__ void __launch_bounds__(kThreads) k_pass(const Pass p) {
 // thread takes four elements.  4.7 us for 12 heads of 13 states of 64 x 96.  (Every segment's block summing the
 // states before it reads them segments^2 / 2 times, most of the time of a long row in many.)
 __global__ void __launch_bounds__(kThreads) k_prefix(const Pass p) {
-  __shared__ float keep[kMaxSegs];
+  __shared__ float keep[kMaxSegs], keep_lo[kMaxSegs];
   const size_t bh = p.whole + blockIdx.y, nstate = (size_t)p.Da * p.Dc;
   const int b = (int)(bh / p.H), h = (int)(bh % p.H);
   tc::launch_dependents();  // the pass may set itself up meanwhile
@@ -318,7 +327,9 @@ __global__ void __launch_bounds__(kThreads) k_prefix(const Pass p) {
     uint32_t any = 0;
     for (int w = lo / 32; words && 32 * w < hi; ++w) any |= words[w];
     const int n = hi - lo - (p.rev && hi == p.T ? 1 : 0);
-    keep[s] = any || (decay_pow(g, 1) == 0.0f && n > 0) ? kNone : decay_pow(g, n);
+    const Fade f = fade_of(g, n);
+    keep[s] = any || (decay_pow(g, 1) == 0.0f && n > 0) ? kNone : f.hi;
+    keep_lo[s] = f.lo;
   }
   __syncthreads();
   const size_t e = 4 * ((size_t)blockIdx.x * kThreads + threadIdx.x);
@@ -352,6 +363,7 @@ __global__ void __launch_bounds__(kThreads) k_prefix(const Pass p) {
         f = own[u];
       } else {
         float4 y = own[u];
+        fma4(y, keep_lo[s], f);
         fma4(y, k, f);
         f = y;
       }

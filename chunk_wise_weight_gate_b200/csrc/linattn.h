@@ -58,6 +58,26 @@ struct Pass {
 constexpr float kNone = -1.0f;
 __device__ __forceinline__ float decay_pow(float g, int n) { return n <= 0 ? 1.0f : expf(g * (float)n); }
 
+// A power of gamma that a state is multiplied by again and again.  Its rounding to fp32 would be the same
+// each time and grow with the tokens remembered (5e-6 of a state at 16k); so what a factor's
+// rounding left goes into the next one, and any number of them is off by two roundings.
+struct Fade {
+  float hi, lo, inv;  // hi + lo is the power, inv = 1 / hi
+};
+__device__ __forceinline__ Fade fade_of(float g, int n) {
+  const double x = exp((double)g * n);
+  Fade f;
+  f.hi = (float)x;
+  f.lo = f.hi > 0.0f ? (float)(x - f.hi) : 0.0f;
+  f.inv = f.hi > 1e-30f ? 1.0f / f.hi : 0.0f;  // below it no state remembers two of them
+  return f;
+}
+__device__ __forceinline__ float fade_next(const Fade& f, float& left) {
+  const float t = fmaf(f.hi, left, f.lo), x = f.hi + t;
+  left = ((f.hi - x) + t) * f.inv;
+  return x;
+}
+
 // The CUDA-core pass (any widths up to 256, fp32 or bf16 operands), chunks of 32 tokens.
 constexpr int kSimtChunk = 32;
 cudaError_t run_simt(const Pass& p, int dtype, cudaStream_t st);

@@ -5,7 +5,8 @@
 namespace ipttt {
 namespace la {
 
-// Per head: pw[128 + n] = gamma^n for 0 <= n <= 128 and 0 for n < 0, then gamma^{31 - n}, n < 32.
+// Per head: pw[128 + n] = gamma^n for 0 <= n <= 128 and 0 for n < 0, what fade_next takes besides gamma^128, then
+// (from kPw on) gamma^{31 - n}, n < 32.
 constexpr int kPw = 260, kTab = kPw + 32;
 constexpr int kSmemBlock = 232448;  // most shared memory of a block
 constexpr int kWalk = 8;            // tokens at a time, where an item is walked token by token

@@ -255,7 +255,9 @@ __device__ __forceinline__ bool walk(const Pass& p, const Item& it, float* F, fl
   const size_t bh = (size_t)it.b * p.H + it.h, nstate = (size_t)DA * DC;
   const int lo = it.first * CH, hi = min(p.T, it.last * CH);
   const uint32_t* starts = p.starts ? p.starts + it.b * p.words : nullptr;
-  const float g = p.log_decay[it.h], gamma = decay_pow(g, 1);
+  const float g = p.log_decay[it.h];
+  const Fade gamma = fade_of(g, 1);
+  float left = 0.0f;
   float* f = F + r0 * DC + col;  // the thread's first element; its rows are DC apart
   auto meet = [&] {
     __syncwarp();
@@ -318,7 +320,7 @@ __device__ __forceinline__ bool walk(const Pass& p, const Item& it, float* F, fl
       const int t = token(k);
       const bool start = ((t / 32 == word ? bits0 : bits1) >> (t % 32) & 1u) != 0;
       // no decay before the last token, whose state's gradient comes in as it is
-      const float keep = p.rev && t == p.T - 1 ? 1.0f : gamma;
+      const float keep = p.rev && t == p.T - 1 ? 1.0f : fade_next(gamma, left);
       const bool drop = keep == 0.0f || (!p.rev && start);
       const bool ends = p.rev && start;  // the document, on the way back
       const float c = sc[k * DC + col];
@@ -761,7 +763,17 @@ __global__ void __launch_bounds__(Cfg<DA, DC, KIND == STATES>::THREADS, 1) k_pas
       float* pw = tabs + (ic & 1) * kTab + 128;
       pw[tid - 128] = tid < 128 ? 0.0f : decay_pow(g, tid - 128);
       if (tid < 32) pw[kPw - 128 + tid] = decay_pow(g, 31 - tid);
-      if (tid == 32) pw[128] = decay_pow(g, 128);
+      if (tid == 32) {
+        if constexpr (FINE) {
+          const Fade fd = fade_of(g, CH);
+          pw[128] = fd.hi;
+          pw[129] = fd.lo;
+          pw[130] = fd.inv;
+        } else {
+          pw[128] = decay_pow(g, 128);
+        }
+      }
+      float left = 0.0f;
       __syncwarp();
       if (lane == 0) mbar_arrive(tab_ready);
       const int lo = it.first * CH, hi = min(p.T, it.last * CH);
@@ -940,7 +952,9 @@ __global__ void __launch_bounds__(Cfg<DA, DC, KIND == STATES>::THREADS, 1) k_pas
           if (lane == 0) mbar_arrive(&conv_done[2 * (cc & 1) + half]);
         }
         if (FINE && !ok) break;
-        const float keep_now = any ? kNone : pw[len - lag];
+        float keep_now = pw[len - lag];
+        if (FINE && len - lag == CH) keep_now = fade_next({keep_now, pw[129], pw[130]}, left);
+        if (any) keep_now = kNone;
         if (n + 1 < it.last - it.first) weights(ch + step, next);
         if constexpr (STATE) {
           if (n > 0) {

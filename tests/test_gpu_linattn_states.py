@@ -49,3 +49,35 @@ def test_states_of_rows_in_segments(B, T, H, Dk, Dv):
         w = pkg.linear_attention_backward(f32, q.float(), k.float(), v.float(), ld, ds, gO.float(), S0=S0)
         assert ref.relative(g["S0"], w["S0"].cpu()) <= 1.2e-6
     assert status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("B,T,H,D", [(1, 16384, 16, 64), (1, 8192, 40, 128), (2, 3000, 160, 64)])
+def test_states_of_long_memories(B, T, H, D, dtype):
+    # decays of any mantissa, that remember up to 16k tokens: the same factor is multiplied on up to 512 times.
+    # S_T = sum of gamma^{T-1-t} k_t v_t^T, by its closed form in 64 bits; fp32: sums of up to 512 chunks, each rounded at
+    # 2^-24 of a state that grows as its root: 1e-6
+    cfg, q, k, v, _, _, _ = attn_case(B, T, H, H, D, D, dtype)
+    ld = -torch.exp2(-13.0 * torch.rand(H, generator=torch.Generator().manual_seed(6))).cuda()
+    _, S = pkg.linear_attention(cfg, q, k, v, ld, S_final=True)
+    t = torch.arange(T - 1, -1, -1, device="cuda", dtype=torch.float64)
+    for h in range(H):
+        w = torch.exp(ld[h].double() * t)[None, :, None]
+        want = torch.matmul((k[:, :, h].double() * w).transpose(1, 2), v[:, :, h].double())
+        assert ref.relative(S[:, h], want.cpu()) <= 1.2e-6, h
+    assert status() == 0
+
+
+def test_states_after_a_walk_by_tokens():
+    # a bad value in a finished document: the state after 4000 more tokens, each times gamma, is as exact
+    T, H, D = 4500, 12, 64
+    cfg, q, k, v, _, _, ds = attn_case(1, T, H, H, D, D, "bf16", (500,))
+    ld = -torch.exp2(-4.0 - 9.0 * torch.rand(H, generator=torch.Generator().manual_seed(7))).cuda()
+    k[0, 3, :, 1] = float("nan")
+    _, S = pkg.linear_attention(cfg, q, k, v, ld, ds, S_final=True)
+    t = torch.arange(T - 501, -1, -1, device="cuda", dtype=torch.float64)
+    for h in range(H):
+        w = torch.exp(ld[h].double() * t)[:, None]
+        want = (k[0, 500:, h].double() * w).t() @ v[0, 500:, h].double()
+        assert ref.relative(S[0, h], want.cpu()) <= 2e-6, h
+    assert status() == 0
