@@ -486,7 +486,9 @@ IPTTT_API ipttt_status ipttt_linattn_step(const ipttt_linattn_params* p, float* 
  * kept.  A target equal to ignore_index leaves its row out: loss 0, no gradient; its
  * lse is computed all the same.  Any other target outside [0, V) fails on the device
  * (IPTTT_ERR_ARG) and its row is left out.  What a row of H that is left out holds, values
- * that are not finite included, reaches no loss and no gradient.
+ * that are not finite included, reaches no loss and no gradient, and its own row of gH is 0
+ * whatever W holds.  Elsewhere a NaN logit makes its row's lse and loss NaN, one of +infinity
+ * makes its lse infinite.
  * The backward takes the forward's lse and gloss = dL/dloss (fp32 [N]) and forms each
  * piece's logits again: p = (exp(l - lse) - onehot) gloss, gH = p W, gW = p^T H, both in
  * the call's dtype, summed in fp32; bf16 calls round p to bf16 for the two products.
