@@ -261,15 +261,22 @@ def linear_attention_backward(cfg: LinearAttentionConfig, q, k, v, log_decay, do
     p0 = _flat(S0, "S0", sh["S"], f32, dev)
     ps = _flat(gS_final, "gS_final", sh["S"], f32, dev)
     with _On(q, stream) as st:
-        out = {n: torch.empty_like(t, memory_format=_packed) if g is None else g
-               for n, t, g in (("q", q, gq), ("k", k, gk), ("v", v, gv))}
-        grads = [_tokens(out[n], "g" + n, sh[n], dt, dev) for n in "qkv"]
+        out, grads, lds = {}, [], []
+        for n, t, g in (("q", q, gq), ("k", k, gk), ("v", v, gv)):
+            if g is None:
+                g = torch.empty_like(t, memory_format=_packed)
+                at, ld = g.data_ptr(), 0
+            else:
+                at, ld = _tokens(g, "g" + n, sh[n], dt, dev)
+            out[n] = g
+            grads.append(at)
+            lds.append(ld)
         if S0 is not None:
             out["S0"] = torch.empty(sh["S"], dtype=f32, device=dev)
-        p = cfg.params(ldq, ldk, ldv, ldo, *(ld for _, ld in grads))
+        p = cfg.params(ldq, ldk, ldv, ldo, *lds)
         ws = _workspace(workspace, _size(lib().ipttt_linattn_backward_workspace_size, p, cfg), dev)
         dp, nd, keep = _starts(doc_starts, dev)
-        _check(lib().ipttt_linattn_backward(_byref(p), pq, pk, pv, pd, dp, nd, p0, pg, ps, *(g for g, _ in grads),
+        _check(lib().ipttt_linattn_backward(_byref(p), pq, pk, pv, pd, dp, nd, p0, pg, ps, *grads,
                                             out["S0"].data_ptr() if S0 is not None else None, ws.data_ptr(),
                                             ws.numel(), st), "ipttt_linattn_backward")
     return out
